@@ -1,5 +1,6 @@
 // Internal launch interface between the host pool manager (pool.cpp) and
-// the sm_103a kernels (resolve.cu, hostcopy.cu, gather.cu, append.cu).
+// the sm_103a kernels (resolve.cu, hostcopy.cu, gather.cu, append.cu,
+// attend.cu, fork.cu).
 // Not part of the C ABI.
 //
 // Item tables travel by value in the kernel parameter space
@@ -285,6 +286,71 @@ cudaError_t launch_gather_later(const GatherCommon& c, int ctas, cudaStream_t st
 // *tma_ok: whether the TMA gather's 16-row tile of this row size fits in
 // `optin` bytes of shared memory per block (else only the vector gather runs).
 cudaError_t gather_set_smem_limit(int row_bytes, int optin, bool* tma_ok);
+
+// ------------------------------------------------------------ attention
+constexpr int kAttendItemsLarge = 240, kAttendItemsSmall = 16;
+constexpr int kAttendMaxKey = 576, kAttendMaxValue = 512;
+
+struct AttendItem {
+  const uint8_t* q;
+  const uint32_t* loc;    // located items, else null
+  const int32_t* index;   // union positions, or null
+  const int32_t* range;   // history items: [Q][2], or null = causal
+  uint8_t* out;
+  float* lse;             // or null
+  const uint8_t* host;    // history items: device-visible host rows, null for a window
+  int64_t first, len;     // history items: rows served [first, first + len); else len = k
+  int32_t pair;
+  int32_t complete;       // history items: complete imported pages
+  int32_t Q;
+  int32_t job0;           // first job of this item in the launch
+};
+
+struct AttendCommon {
+  const uint8_t* tail;
+  const uint8_t* opt;
+  const uint8_t* hot;
+  const int32_t* map;     // [pairs][Pmax]
+  uint32_t tail_rows, opt_rows, hot_rows;  // arena sizes in rows
+  int32_t row_bytes, T, Pmax, page_shift;
+  uint32_t* status;
+  int32_t n_items, n_jobs;
+  int32_t f16;            // rows are f16, else bf16
+  int32_t heads, group;   // query heads, query heads per kv head
+  int32_t dk, dv;         // elements of a key and of a value
+  int32_t key_off, val_off, key_stride, val_stride;  // bytes within a row
+  float scale;
+  int64_t q_qs, q_hs, o_qs, o_hs;  // bytes
+};
+
+cudaError_t launch_attend(const AttendCommon& c, const AttendItem* items, int n_items,
+                          cudaStream_t stream);
+
+// ------------------------------------------------------------ forks
+constexpr int kForkSourcesMax = 256;
+
+struct ForkSource {
+  const uint8_t* host_from;  // device-visible host rows (null: a window source)
+  uint8_t* host_to;
+  int64_t L;
+  int32_t from, to;          // pairs
+  int32_t complete;          // complete imported pages
+  int32_t unit0;             // first work unit of this source in the launch
+};
+
+struct ForkCommon {
+  uint8_t* tail;
+  uint8_t* opt;
+  uint8_t* hot;
+  int32_t* tags;
+  uint32_t* stamps;
+  const int32_t* map;
+  int32_t row_bytes, T, B, Pmax, page_shift;
+  int32_t n_sources, n_units;
+};
+
+cudaError_t launch_fork(const ForkCommon& c, const ForkSource* sources, int n_sources, int sms,
+                        cudaStream_t stream);
 
 // ------------------------------------------------------------ append (A0)
 constexpr int kAppendThreads = 256;

@@ -164,6 +164,7 @@ struct dhs_pool {
   std::vector<int32_t> map_host;  // [pairs][pmax] mirror of the device map
   std::vector<int32_t> slot_pair, slot_page;
   int64_t first_free = 0, used = 0;
+  int64_t capacity = 0;  // optional page slots in use or free (dhs_compact lowers it)
   int64_t dirty_lo = INT64_MAX, dirty_hi = -1;  // pairs whose map changed
   bool any_pending = false;
   int copy_ctas = 0;
@@ -219,6 +220,7 @@ struct dhs_pool {
   };
   std::vector<LocKey> loc_keys;
   std::vector<dhs::AppendItem> aitems;
+  std::vector<dhs::AttendItem> titems;
   std::vector<uint8_t> seen;
   std::vector<int32_t> app_of_pair;  // decode step: append item of each pair, -1 = none
   std::vector<int64_t> l0_of_pair;   // length of each resolved pair before this step's append
@@ -490,7 +492,7 @@ void free_slot(dhs_pool* p, int64_t slot) {
 }
 
 int64_t lowest_free_slot(dhs_pool* p) {
-  for (int64_t i = p->first_free; i < p->cfg.optional_pages; ++i)
+  for (int64_t i = p->first_free; i < p->capacity; ++i)
     if (p->slot_pair[i] < 0) {
       p->first_free = i;
       return i;
@@ -626,6 +628,7 @@ int dhs_pool_create(const dhs_pool_config* cfg, dhs_pool** out) {
   if (!p) return DHS_ENOMEM;
   try {
     p->cfg = *cfg;
+    p->capacity = cfg->optional_pages;
     p->union_ok = union_ok;
     p->gather_impl = dhs::kGatherTma;
     p->sm_count = sms;
@@ -827,7 +830,7 @@ int dhs_admit(dhs_pool* p, int32_t req, int32_t src, void* host_rows, int64_t n_
   const int64_t complete = n_rows / c.page_rows;
   int64_t want = 0;
   for (int64_t q = 0; q < complete; ++q) want += (!mask || mask[q]) ? 1 : 0;
-  const int64_t usable = c.optional_pages - c.admission_reserve_pages;
+  const int64_t usable = p->capacity - c.admission_reserve_pages;
   if (p->used + want > usable) {
     if (deficit) *deficit = p->used + want - usable;
     return DHS_EWOULDWAIT;
@@ -892,7 +895,7 @@ int dhs_admit_device(dhs_pool* p, int32_t req, int32_t src, const void* dev_rows
   const int64_t complete = n_rows / c.page_rows;
   int64_t want = 0;
   for (int64_t q = 0; q < complete; ++q) want += (!mask || mask[q]) ? 1 : 0;
-  const int64_t usable = c.optional_pages - c.admission_reserve_pages;
+  const int64_t usable = p->capacity - c.admission_reserve_pages;
   if (p->used + want > usable) {
     if (deficit) *deficit = p->used + want - usable;
     return DHS_EWOULDWAIT;
@@ -1014,7 +1017,7 @@ int dhs_refill(dhs_pool* p, int64_t max_pages, int64_t* filled) {
   if (filled) *filled = 0;
   if (!p || max_pages < 0) return DHS_EINVAL;
   const dhs_pool_config& c = p->cfg;
-  const int64_t usable = c.optional_pages - c.admission_reserve_pages;
+  const int64_t usable = p->capacity - c.admission_reserve_pages;
   int64_t n = 0, idle = 0;
   int32_t r = p->rr;
   while (n < max_pages && p->used < usable && idle < c.max_requests) {
@@ -1387,7 +1390,7 @@ static int launch_gathers(dhs_pool* p, const dhs_step* st, bool fused) {
   g.hot = (const uint8_t*)c.hot_dev;
   g.map = p->map;
   g.tail_rows = (uint32_t)(p->pairs * c.tail_rows);
-  g.opt_rows = (uint32_t)(c.optional_pages * c.page_rows);
+  g.opt_rows = (uint32_t)(p->capacity * c.page_rows);
   g.hot_rows = (uint32_t)(p->pairs * c.hot_rows);
   g.row_bytes = c.row_bytes;
   g.status = p->status;
@@ -1515,14 +1518,17 @@ int dhs_gather(dhs_pool* p, const dhs_step* st) {
   return launch_gathers(p, st, false);
 }
 
-int dhs_gather_on(dhs_pool* p, const dhs_step* st, void* stream) {
-  if (!p || !stream) return DHS_EINVAL;
-  int rc = validate_step(p, st, false);
-  if (rc) return rc;
-  if ((rc = enter_gather(p, st))) return rc;
-  if ((rc = flush(p))) return rc;
+// Run `launch` on a caller's stream: after everything the pool's stream holds,
+// and joined by the pool's next call that can change rows.
+static int on_stream(dhs_pool* p, void* stream, const std::function<int()>& launch) {
   cudaStream_t other = (cudaStream_t)stream;
   cudaEvent_t done = nullptr;
+  try {
+    p->ev_gathers.reserve(p->ev_gathers.size() + 1);
+    p->ev_free.reserve(p->ev_free.size() + p->ev_gathers.size() + 1);
+  } catch (...) {
+    return DHS_ENOMEM;
+  }
   if (!p->ev_free.empty()) {
     done = p->ev_free.back();
     p->ev_free.pop_back();
@@ -1537,7 +1543,7 @@ int dhs_gather_on(dhs_pool* p, const dhs_step* st, void* stream) {
   }
   cudaStream_t main = p->stream;
   p->stream = other;
-  rc = launch_gathers(p, st, false);
+  const int rc = launch();
   p->stream = main;
   // joined before the pool's next call that can change rows, even if the
   // launch failed part way
@@ -1547,6 +1553,15 @@ int dhs_gather_on(dhs_pool* p, const dhs_step* st, void* stream) {
   }
   p->ev_gathers.push_back(done);
   return rc;
+}
+
+int dhs_gather_on(dhs_pool* p, const dhs_step* st, void* stream) {
+  if (!p || !stream) return DHS_EINVAL;
+  int rc = validate_step(p, st, false);
+  if (rc) return rc;
+  if ((rc = enter_gather(p, st))) return rc;
+  if ((rc = flush(p))) return rc;
+  return on_stream(p, stream, [&] { return launch_gathers(p, st, false); });
 }
 
 int dhs_resolve_gather(dhs_pool* p, const dhs_step* st) {
@@ -1700,6 +1715,319 @@ int dhs_read_state(dhs_pool* p, int32_t req, int32_t src, int32_t* tags, uint32_
   }
   return DHS_OK;
 }
+
+// ---------------------------------------------------------------------------
+// Attention over located rows and histories (attend.cu).
+
+static int validate_attend(dhs_pool* p, const dhs_attend_step* st) {
+  if (!p || !st || st->n_items < 0 || (st->n_items > 0 && !st->items)) return DHS_EINVAL;
+  const dhs_pool_config& c = p->cfg;
+  if (st->dtype != DHS_BF16 && st->dtype != DHS_F16) return DHS_EINVAL;
+  if (st->kv_heads < 1 || st->heads < 1 || st->heads % st->kv_heads) return DHS_EINVAL;
+  if (st->key_elems < 8 || st->key_elems > DHS_ATTEND_MAX_KEY || st->value_elems < 8 ||
+      st->value_elems > DHS_ATTEND_MAX_VALUE)
+    return DHS_EINVAL;
+  if ((st->key_elems | st->value_elems | st->key_offset | st->value_offset) & 7) return DHS_EINVAL;
+  // every head's key and value lie inside the row
+  auto inside = [&](int64_t off, int64_t stride, int64_t n) {
+    if (off < 0 || (st->kv_heads > 1 && (stride < 0 || stride & 7))) return false;
+    const int64_t last = st->kv_heads > 1 ? (st->kv_heads - 1) * stride : 0;
+    return (off + last + n) * 2 <= c.row_bytes;
+  };
+  if (!inside(st->key_offset, st->key_stride, st->key_elems) ||
+      !inside(st->value_offset, st->value_stride, st->value_elems))
+    return DHS_EINVAL;
+  if (!(st->scale - st->scale == 0.f)) return DHS_EINVAL;  // finite
+  for (int32_t i = 0; i < st->n_items; ++i) {
+    const dhs_attend_item& it = st->items[i];
+    if (it.queries < 0 || it.topk < 0 || (it.flags & ~DHS_ATTEND_HISTORY)) return DHS_EINVAL;
+    if ((int64_t)it.queries * st->heads > (int64_t)1 << 24) return DHS_EINVAL;
+    if (it.queries > 0 && (!it.q_dev || !it.out_dev)) return DHS_EINVAL;
+    if (((uintptr_t)it.q_dev | (uintptr_t)it.out_dev) & 1 || (uintptr_t)it.lse_dev & 3)
+      return DHS_EINVAL;
+    if (it.flags & DHS_ATTEND_HISTORY) {
+      if (it.req < 0 || it.req >= c.max_requests || it.src < 0 || it.src >= c.sources)
+        return DHS_EINVAL;
+      if (!p->ps[(int64_t)it.req * c.sources + it.src].admitted) return DHS_ESTATE;
+    } else {
+      const int64_t n = (int64_t)it.queries * it.topk;
+      if (n > INT32_MAX || (n > 0 && !it.loc_dev)) return DHS_EINVAL;
+    }
+  }
+  return DHS_OK;
+}
+
+int dhs_attend_bytes(dhs_pool* p, const dhs_attend_step* st, size_t* bytes) {
+  if (bytes) *bytes = 0;
+  if (!bytes) return DHS_EINVAL;
+  return validate_attend(p, st);
+}
+
+// Launch the attention of every item of a validated, flushed step.
+static int launch_attends(dhs_pool* p, const dhs_attend_step* st) {
+  const dhs_pool_config& c = p->cfg;
+  dhs::AttendCommon a{};
+  a.tail = (const uint8_t*)c.tail_dev;
+  a.opt = (const uint8_t*)c.opt_dev;
+  a.hot = (const uint8_t*)c.hot_dev;
+  a.map = p->map;
+  a.tail_rows = (uint32_t)(p->pairs * c.tail_rows);
+  a.opt_rows = (uint32_t)(p->capacity * c.page_rows);
+  a.hot_rows = (uint32_t)(p->pairs * c.hot_rows);
+  a.row_bytes = c.row_bytes;
+  a.T = c.tail_rows;
+  a.Pmax = (int32_t)p->pmax;
+  a.page_shift = p->page_shift;
+  a.status = p->status;
+  a.f16 = st->dtype == DHS_F16;
+  a.heads = st->heads;
+  a.group = st->heads / st->kv_heads;
+  a.dk = st->key_elems;
+  a.dv = st->value_elems;
+  a.key_off = st->key_offset * 2;
+  a.val_off = st->value_offset * 2;
+  a.key_stride = st->key_stride * 2;
+  a.val_stride = st->value_stride * 2;
+  a.scale = st->scale;
+  a.q_qs = st->q_query_stride * 2;
+  a.q_hs = st->q_head_stride * 2;
+  a.o_qs = st->out_query_stride * 2;
+  a.o_hs = st->out_head_stride * 2;
+  try {
+    p->titems.clear();
+    for (int32_t i = 0; i < st->n_items; ++i) {
+      const dhs_attend_item& it = st->items[i];
+      if (it.queries == 0) continue;
+      dhs::AttendItem t{};
+      t.q = (const uint8_t*)it.q_dev;
+      t.out = (uint8_t*)it.out_dev;
+      t.lse = it.lse_dev;
+      t.Q = it.queries;
+      if (it.flags & DHS_ATTEND_HISTORY) {
+        const int64_t pair = (int64_t)it.req * c.sources + it.src;
+        const PairState& s = p->ps[pair];
+        t.pair = (int32_t)pair;
+        t.range = it.range_dev;
+        t.host = s.host_dev;
+        t.first = s.window ? std::max<int64_t>(0, s.L - c.tail_rows) : 0;
+        t.len = s.L - t.first;
+        t.complete = (int32_t)(s.N >> p->page_shift);
+      } else {
+        t.loc = it.loc_dev;
+        t.index = it.index_dev;
+        t.len = it.topk;
+      }
+      p->titems.push_back(t);
+    }
+  } catch (...) {
+    return DHS_ENOMEM;
+  }
+  for (size_t b = 0; b < p->titems.size(); b += dhs::kAttendItemsLarge) {
+    const int n = (int)std::min<size_t>(dhs::kAttendItemsLarge, p->titems.size() - b);
+    if (dhs::launch_attend(a, p->titems.data() + b, n, p->stream) != cudaSuccess)
+      return DHS_ECUDA;
+  }
+  return DHS_OK;
+}
+
+// Attention only reads rows: gathers and attentions still running on other
+// streams need not be joined, an outstanding prefetch (which fills hot slots
+// that a location vector may name) is.
+static int enter_attend(dhs_pool* p) {
+  p->join_gathers = false;
+  const int rc = enter(p);
+  p->join_gathers = true;
+  return rc;
+}
+
+int dhs_attend(dhs_pool* p, const dhs_attend_step* st) {
+  int rc = validate_attend(p, st);
+  if (rc) return rc;
+  if ((rc = enter_attend(p))) return rc;
+  if ((rc = flush(p))) return rc;
+  return launch_attends(p, st);
+}
+
+int dhs_attend_on(dhs_pool* p, const dhs_attend_step* st, void* stream) {
+  if (!stream) return DHS_EINVAL;
+  int rc = validate_attend(p, st);
+  if (rc) return rc;
+  if ((rc = enter_attend(p))) return rc;
+  if ((rc = flush(p))) return rc;
+  return on_stream(p, stream, [&] { return launch_attends(p, st); });
+}
+
+// ---------------------------------------------------------------------------
+// Forks and compaction (fork.cu).
+
+// Forget everything of a child that dhs_fork could not complete.
+static void undo_fork(dhs_pool* p, int32_t child) {
+  for (int32_t s = 0; s < p->cfg.sources; ++s) {
+    const int64_t pair = (int64_t)child * p->cfg.sources + s;
+    if (!p->ps[pair].admitted) continue;
+    drop_pages(p, pair, false);
+    p->complete_pages -= p->ps[pair].N >> p->page_shift;
+    p->ps[pair] = PairState();
+  }
+}
+
+int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
+             const uint8_t* const* masks, int64_t* deficit) {
+  if (deficit) *deficit = 0;
+  if (!p || req < 0 || req >= p->cfg.max_requests || child < 0 ||
+      child >= p->cfg.max_requests || child == req)
+    return DHS_EINVAL;
+  const dhs_pool_config& c = p->cfg;
+  const int64_t from0 = (int64_t)req * c.sources, to0 = (int64_t)child * c.sources;
+  const int64_t host_bytes = c.max_rows_per_request * (int64_t)c.row_bytes;
+  bool any = false;
+  int64_t want = 0;
+  for (int32_t s = 0; s < c.sources; ++s) {
+    const PairState& f = p->ps[from0 + s];
+    if (p->ps[to0 + s].admitted) return DHS_ESTATE;
+    if (!f.admitted) continue;
+    any = true;
+    if (f.window) continue;
+    const uint8_t* h = host_rows ? (const uint8_t*)host_rows[s] : nullptr;
+    if (!h || (uintptr_t)h % 16) return DHS_EINVAL;
+    if (h < f.host + host_bytes && f.host < h + host_bytes) return DHS_EINVAL;
+    const uint8_t* mask = masks ? masks[s] : nullptr;
+    const int32_t* pm = p->map_host.data() + (from0 + s) * p->pmax;
+    for (int64_t q = 0; q < f.N >> p->page_shift; ++q) want += mask ? mask[q] != 0 : pm[q] >= 0;
+  }
+  if (!any) return DHS_ESTATE;
+  int rc = enter(p);
+  if (rc) return rc;
+  std::vector<dhs::ForkSource> src;
+  try {
+    src.reserve(c.sources);
+    for (int32_t s = 0; s < c.sources; ++s) {
+      const PairState& f = p->ps[from0 + s];
+      if (!f.admitted) continue;
+      dhs::ForkSource k{};
+      k.from = (int32_t)(from0 + s);
+      k.to = (int32_t)(to0 + s);
+      k.L = f.L;
+      if (!f.window) {
+        void* hdev = nullptr;
+        if (cudaHostGetDevicePointer(&hdev, host_rows[s], 0) != cudaSuccess || !hdev ||
+            (uintptr_t)hdev % 16) {
+          cudaGetLastError();
+          return DHS_EINVAL;
+        }
+        k.host_from = f.host_dev;
+        k.host_to = (uint8_t*)hdev;
+        k.complete = (int32_t)(f.N >> p->page_shift);
+      }
+      src.push_back(k);
+    }
+    const int64_t usable = p->capacity - c.admission_reserve_pages;
+    if (p->used + want > usable) {
+      if (deficit) *deficit = p->used + want - usable;
+      return DHS_EWOULDWAIT;
+    }
+    for (const dhs::ForkSource& k : src) {
+      const int32_t s = (int32_t)(k.to - to0);
+      const PairState& f = p->ps[k.from];
+      PairState& t = p->ps[k.to];
+      if (!f.window) t.backup.assign((size_t)p->pmax, 0);
+      t.admitted = true;
+      t.window = f.window;
+      t.N = f.N;
+      t.L = f.L;
+      t.host = f.window ? nullptr : (uint8_t*)host_rows[s];
+      t.host_dev = k.host_to;
+      p->complete_pages += f.N >> p->page_shift;
+      const uint8_t* mask = masks && !f.window ? masks[s] : nullptr;
+      const int32_t* pm = p->map_host.data() + (int64_t)k.from * p->pmax;
+      int32_t* to = p->map_host.data() + (int64_t)k.to * p->pmax;
+      mark_dirty(p, k.to);
+      for (int64_t q = 0; q < k.complete; ++q) {
+        if (mask ? !mask[q] : pm[q] < 0) continue;
+        p->backup_order.insert({++p->bseq, (int64_t)k.to * p->pmax + q});
+        t.backup[q] = p->bseq;
+        const int64_t slot = lowest_free_slot(p);
+        p->slot_pair[slot] = k.to;
+        p->slot_page[slot] = (int32_t)q;
+        p->used += 1;
+        to[q] = (int32_t)slot;
+      }
+    }
+    // the parent's pending pages and both page maps, before the copy reads them
+    rc = flush(p);
+  } catch (...) {
+    rc = DHS_ENOMEM;
+  }
+  if (rc) {
+    undo_fork(p, child);
+    return rc;
+  }
+  dhs::ForkCommon f{};
+  f.tail = (uint8_t*)c.tail_dev;
+  f.opt = (uint8_t*)c.opt_dev;
+  f.hot = (uint8_t*)c.hot_dev;
+  f.tags = p->tags;
+  f.stamps = p->stamps;
+  f.map = p->map;
+  f.row_bytes = c.row_bytes;
+  f.T = c.tail_rows;
+  f.B = c.hot_rows;
+  f.Pmax = (int32_t)p->pmax;
+  f.page_shift = p->page_shift;
+  for (size_t b = 0; b < src.size(); b += dhs::kForkSourcesMax) {
+    const int n = (int)std::min<size_t>(dhs::kForkSourcesMax, src.size() - b);
+    if (dhs::launch_fork(f, src.data() + b, n, std::max(1, p->sm_count), p->stream) !=
+        cudaSuccess) {
+      undo_fork(p, child);
+      return DHS_ECUDA;
+    }
+  }
+  return DHS_OK;
+}
+
+int dhs_compact(dhs_pool* p, int64_t capacity, int64_t* moved) {
+  if (moved) *moved = 0;
+  if (!p || capacity < 0 || capacity > p->cfg.optional_pages) return DHS_EINVAL;
+  if (capacity < p->used) return DHS_EWOULDWAIT;
+  int rc = enter(p);
+  if (rc) return rc;
+  // pages still to be filled are filled where they are, then moved
+  if ((rc = flush(p))) return rc;
+  const int64_t pb = (int64_t)p->cfg.page_rows * p->cfg.row_bytes;
+  uint8_t* opt = (uint8_t*)p->cfg.opt_dev;
+  int64_t n = 0;
+  for (int64_t i = capacity; i < p->capacity; ++i) n += p->slot_pair[i] >= 0;
+  p->moves.clear();
+  try {
+    p->moves.reserve(n);
+  } catch (...) {
+    return DHS_ENOMEM;
+  }
+  int64_t to = p->first_free;
+  for (int64_t i = capacity; i < p->capacity; ++i) {
+    if (p->slot_pair[i] < 0) continue;
+    while (p->slot_pair[to] >= 0) ++to;
+    p->moves.push_back({opt + i * pb, opt + to * pb});
+    p->slot_pair[to] = p->slot_pair[i];
+    p->slot_page[to] = p->slot_page[i];
+    p->slot_pair[i] = p->slot_page[i] = -1;
+    p->map_host[p->slot_pair[to] * p->pmax + p->slot_page[to]] = (int32_t)to;
+    mark_dirty(p, p->slot_pair[to]);
+  }
+  p->first_free = to;
+  p->capacity = capacity;
+  if (moved) *moved = n;
+  if (!small_pages(p)) {  // pages too large for the page kernel
+    for (const dhs::PageMove& m : p->moves)
+      if (cudaMemcpyAsync(m.dst, m.src, pb, cudaMemcpyDeviceToDevice, p->stream) != cudaSuccess)
+        return DHS_ECUDA;
+    p->moves.clear();
+  }
+  if ((rc = run_moves(p))) return rc;
+  return flush(p);
+}
+
+int64_t dhs_pool_capacity(const dhs_pool* p) { return p ? p->capacity : -1; }
 
 }  // extern "C"
 

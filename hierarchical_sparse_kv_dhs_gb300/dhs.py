@@ -50,6 +50,9 @@ DHS_OPT_COPY_PDL = 9
 DHS_OPT_RESOLVE_PAIRED = 10
 DHS_OPT_COPY_STEAL = 11
 DHS_OPT_RESOLVE_CTAS = 12
+DHS_BF16, DHS_F16 = 0, 1
+DHS_ATTEND_HISTORY = 1
+DHS_ATTEND_MAX_KEY, DHS_ATTEND_MAX_VALUE = 576, 512
 DHS_BUF_HOT, DHS_BUF_TAIL, DHS_BUF_OPT, DHS_BUF_META = range(4)
 
 _i32, _i64, _u32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_void_p
@@ -79,6 +82,23 @@ class dhs_item(ctypes.Structure):
 
 class dhs_copy(ctypes.Structure):
     _fields_ = [("dst", _vp), ("src", _vp), ("bytes", ctypes.c_size_t)]
+
+
+class dhs_attend_item(ctypes.Structure):
+    _fields_ = [("req", _i32), ("src", _i32), ("queries", _i32), ("topk", _i32),
+                ("flags", _u32), ("reserved", _i32), ("q_dev", _vp), ("loc_dev", _vp),
+                ("index_dev", _vp), ("range_dev", _vp), ("out_dev", _vp), ("lse_dev", _vp)]
+
+
+class dhs_attend_step(ctypes.Structure):
+    _fields_ = [("n_items", _i32), ("dtype", _i32), ("heads", _i32), ("kv_heads", _i32),
+                ("key_elems", _i32), ("value_elems", _i32), ("key_offset", _i32),
+                ("value_offset", _i32), ("key_stride", _i32), ("value_stride", _i32),
+                ("scale", ctypes.c_float), ("reserved", _i32),
+                ("q_query_stride", _i64), ("q_head_stride", _i64),
+                ("out_query_stride", _i64), ("out_head_stride", _i64),
+                ("items", ctypes.POINTER(dhs_attend_item)), ("work_dev", _vp),
+                ("work_bytes", ctypes.c_size_t)]
 
 
 class dhs_step(ctypes.Structure):
@@ -116,6 +136,12 @@ def _load():
         "dhs_gather": (ctypes.c_int, [_vp, P(dhs_step)]),
         "dhs_resolve_gather": (ctypes.c_int, [_vp, P(dhs_step)]),
         "dhs_decode_step": (ctypes.c_int, [_vp, P(dhs_append_item), _i32, P(dhs_step)]),
+        "dhs_attend_bytes": (ctypes.c_int, [_vp, P(dhs_attend_step), P(ctypes.c_size_t)]),
+        "dhs_attend": (ctypes.c_int, [_vp, P(dhs_attend_step)]),
+        "dhs_attend_on": (ctypes.c_int, [_vp, P(dhs_attend_step), _vp]),
+        "dhs_fork": (ctypes.c_int, [_vp, _i32, _i32, P(_vp), P(_vp), P(_i64)]),
+        "dhs_compact": (ctypes.c_int, [_vp, _i64, P(_i64)]),
+        "dhs_pool_capacity": (_i64, [_vp]),
         "dhs_status": (ctypes.c_int, [_vp, P(_u32)]),
         "dhs_read_state": (ctypes.c_int, [_vp, _i32, _i32, _vp, _vp, _vp, _vp]),
         "dhs_set_option": (ctypes.c_int, [_vp, _i32, _i64]),
@@ -229,6 +255,71 @@ def make_step(step: int, items) -> tuple:
     return dhs_step(step, len(items), arr), arr
 
 
+def attend_item(*, queries, q, out, req=0, src=0, topk=0, flags=0, loc=None, index=None,
+                range_=None, lse=None) -> dhs_attend_item:
+    """A dhs_attend_item from torch tensors (or device addresses)."""
+    ptr = lambda t: t.data_ptr() if hasattr(t, "data_ptr") else t
+    it = dhs_attend_item()
+    it.req, it.src, it.queries, it.topk, it.flags = req, src, queries, topk, flags
+    it.q_dev, it.out_dev, it.loc_dev = ptr(q), ptr(out), ptr(loc)
+    it.index_dev, it.range_dev, it.lse_dev = ptr(index), ptr(range_), ptr(lse)
+    return it
+
+
+def make_attend(items, *, heads, key_elems, value_elems, scale, kv_heads=1, key_offset=0,
+                value_offset=0, key_stride=None, value_stride=None, q_strides=None,
+                out_strides=None, dtype="bf16") -> tuple:
+    """A dhs_attend_step (without a workspace) plus the item array that must
+    stay alive with it.  Strides are in elements: between kv heads (default:
+    back to back) and (between queries, between heads) of the queries and the
+    outputs (default: contiguous [Q][heads][elems])."""
+    arr = (dhs_attend_item * max(1, len(items)))(*items)
+    st = dhs_attend_step()
+    st.n_items, st.items = len(items), arr
+    st.dtype = {"bf16": DHS_BF16, "f16": DHS_F16}[dtype]
+    st.heads, st.kv_heads, st.scale = heads, kv_heads, scale
+    st.key_elems, st.value_elems = key_elems, value_elems
+    st.key_offset, st.value_offset = key_offset, value_offset
+    st.key_stride = key_elems if key_stride is None else key_stride
+    st.value_stride = value_elems if value_stride is None else value_stride
+    st.q_query_stride, st.q_head_stride = q_strides or (heads * key_elems, key_elems)
+    st.out_query_stride, st.out_head_stride = out_strides or (heads * value_elems, value_elems)
+    return st, arr
+
+
+def dhs_attend_bytes(h, st: dhs_attend_step) -> int:
+    n = ctypes.c_size_t(0)
+    check(lib.dhs_attend_bytes(h, ctypes.byref(st), ctypes.byref(n)), "dhs_attend_bytes")
+    return n.value
+
+
+def dhs_attend(h, st: dhs_attend_step):
+    return lib.dhs_attend(h, ctypes.byref(st))
+
+
+def dhs_attend_on(h, st: dhs_attend_step, stream):
+    return lib.dhs_attend_on(h, ctypes.byref(st), stream)
+
+
+def dhs_fork(h, req, child, host_ptrs, masks=None):
+    """host_ptrs: one pinned address per source (0: none); masks: None, or one
+    resident-page mask or None per source."""
+    hosts = (_vp * max(1, len(host_ptrs)))(*host_ptrs)
+    keep, mp = [], None
+    if masks is not None:
+        keep = [None if m is None else np.ascontiguousarray(m, np.uint8) for m in masks]
+        mp = (_vp * max(1, len(keep)))(*[None if m is None else m.ctypes.data for m in keep])
+    d = _i64(0)
+    rc = lib.dhs_fork(h, req, child, hosts, mp, ctypes.byref(d))
+    return rc, d.value
+
+
+def dhs_compact(h, capacity_pages):
+    n = _i64(0)
+    rc = lib.dhs_compact(h, capacity_pages, ctypes.byref(n))
+    return rc, n.value
+
+
 def dhs_resolve(h, st: dhs_step):
     return lib.dhs_resolve(h, ctypes.byref(st))
 
@@ -321,12 +412,15 @@ class HostRows:
 
 
 class Pool:
-    """A dhs pool with its four device arenas allocated by torch."""
+    """A dhs pool with its four device arenas allocated by torch, or with the
+    caller's own hot, tail and optional arenas (`arenas`, contiguous uint8
+    tensors of dhs_pool_bytes' sizes).  A caller's hot arena must not hold
+    rows the pool should know: a pool starts with empty hot caches."""
 
     def __init__(self, *, max_requests, sources, row_bytes, page_rows, tail_rows,
                  hot_rows, max_queries, max_topk, max_rows_per_request,
                  optional_pages, admission_reserve_pages=0, device=None,
-                 stream=None):
+                 stream=None, arenas=None):
         import torch
         self.device = torch.device(device or "cuda")
         if self.device.index is None:
@@ -340,8 +434,12 @@ class Pool:
         cfg.optional_pages = optional_pages
         cfg.admission_reserve_pages = admission_reserve_pages
         sizes = dhs_pool_bytes(cfg)
-        self.buffers = [torch.empty(max(s, 256), dtype=torch.uint8, device=self.device)
-                        for s in sizes]
+        given = list(arenas or ())
+        for a, s in zip(given, sizes):
+            if a.dtype != torch.uint8 or not a.is_contiguous() or a.numel() < s:
+                raise ValueError(f"an arena of {s} contiguous bytes is needed")
+        self.buffers = given + [torch.empty(max(s, 256), dtype=torch.uint8, device=self.device)
+                                for s in sizes[len(given):]]
         cfg.hot_dev, cfg.tail_dev, cfg.opt_dev, cfg.meta_dev = [
             b.data_ptr() for b in self.buffers]
         cfg.stream = self.stream.cuda_stream
@@ -415,6 +513,24 @@ class Pool:
 
     def resolve_gather(self, st):
         return dhs_resolve_gather(self.h, st)
+
+    def attend_bytes(self, st):
+        return dhs_attend_bytes(self.h, st)
+
+    def attend(self, st):
+        return dhs_attend(self.h, st)
+
+    def attend_on(self, st, stream):
+        return dhs_attend_on(self.h, st, stream)
+
+    def fork(self, req, child, host_ptrs, masks=None):
+        return dhs_fork(self.h, req, child, host_ptrs, masks)
+
+    def compact(self, capacity_pages):
+        return dhs_compact(self.h, capacity_pages)
+
+    def capacity(self):
+        return int(lib.dhs_pool_capacity(self.h))
 
     def status(self):
         return dhs_status(self.h)

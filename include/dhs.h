@@ -496,6 +496,156 @@ int dhs_decode_step_host_async(dhs_pool *pool, const dhs_copy *in, int32_t n_in,
                                int32_t n_appends, const dhs_step *step,
                                const dhs_copy *out, int32_t n_out, void *out_stream);
 
+/* --------------------------------------------------------- attention */
+
+/* Element type of rows, queries and outputs (2 bytes each). */
+#define DHS_BF16 0
+#define DHS_F16 1
+
+#define DHS_ATTEND_HISTORY 1u /* attend a source's rows, not a location vector */
+
+/* Largest head sizes dhs_attend takes, in elements. */
+#define DHS_ATTEND_MAX_KEY 576
+#define DHS_ATTEND_MAX_VALUE 512
+
+/*
+ * One item of an attention step: Q queries of `heads` heads each, over
+ *   - located items: the rows that loc_dev names, query i the entries
+ *     [i*k, (i+1)*k).  An entry of DHS_NO_LOC or DHS_END_LOC is no row and
+ *     takes no part; one that lies outside its arena takes no part either
+ *     and raises DHS_STATUS_ELOC.  With index_dev (a union item's), entry e
+ *     is the row at loc_dev[index_dev[e]] and a negative index is no row; an
+ *     index of Q*k or above is DHS_STATUS_ELOC.  req and src are unused.
+ *   - DHS_ATTEND_HISTORY items: the rows of (req, src) by number, each at the
+ *     first of the tail ring, a ready optional page, and the pinned host
+ *     copy (read over the host link).  Query i attends rows
+ *     [range_dev[2i], range_dev[2i+1]) as far as the source serves them:
+ *     [0, L), or [L - tail_rows, L) of a window source.  range_dev NULL: the
+ *     queries are the last Q rows of the source, causally: query i attends
+ *     the served rows below L - Q + 1 + i.  topk, loc_dev and index_dev are
+ *     unused.
+ *   q_dev     [Q][heads][key_elems], out_dev [Q][heads][value_elems], by the
+ *             step's strides; 2-byte aligned (16-byte aligned queries whose
+ *             strides are multiples of 8 load faster)
+ *   lse_dev   float [Q][heads]: ln of the sum of exp(scale * score), or NULL
+ * A query with no row to attend, or whose scores are all -infinity, gives
+ * zeros and a log-sum of -infinity.
+ */
+typedef struct {
+  int32_t req;
+  int32_t src;
+  int32_t queries;
+  int32_t topk;
+  uint32_t flags;
+  int32_t reserved;
+  const void *q_dev;
+  const uint32_t *loc_dev;
+  const int32_t *index_dev;
+  const int32_t *range_dev;
+  void *out_dev;
+  float *lse_dev;
+} dhs_attend_item;
+
+/*
+ * Row layout (elements of `dtype` within a row): key head g lies at
+ * key_offset + g * key_stride, value head g at value_offset + g *
+ * value_stride, g < kv_heads; query heads [g * heads/kv_heads, ...) use
+ * them.  The key and the value may overlap: one latent row serving all
+ * heads has kv_heads 1, key_elems 576, value_elems 512, both offsets 0.
+ * Head sizes, offsets and strides are multiples of 8.
+ *   work_dev  device memory, 256-byte aligned, work_bytes of at least
+ *             dhs_attend_bytes (NULL when that is 0); holds partial results
+ *             of rows split over several blocks, rewritten by every call:
+ *             calls that may overlap (other streams) need one each.
+ */
+typedef struct {
+  int32_t n_items;
+  int32_t dtype;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t key_elems;
+  int32_t value_elems;
+  int32_t key_offset;
+  int32_t value_offset;
+  int32_t key_stride;
+  int32_t value_stride;
+  float scale;
+  int32_t reserved;
+  int64_t q_query_stride;   /* elements between queries */
+  int64_t q_head_stride;    /* elements between heads */
+  int64_t out_query_stride;
+  int64_t out_head_stride;
+  const dhs_attend_item *items;
+  void *work_dev;
+  size_t work_bytes;
+} dhs_attend_step;
+
+/* Bytes of work_dev that dhs_attend needs for `st` now (history items: at
+ * the sources' present lengths).  Pool and
+ * step are validated as in dhs_attend, except for work_dev.  Host
+ * arithmetic only.  Errors: as dhs_attend. */
+int dhs_attend_bytes(dhs_pool *pool, const dhs_attend_step *st, size_t *bytes);
+
+/*
+ * "Memory split" names sparse attention as what reads the selected rows; the
+ * pages leave it to the model.  This call is that attention: for every item,
+ * query i and head h, with x_j the key and y_j the value of the j-th row
+ * attended,
+ *   out = sum_j p_j y_j / sum_j p_j,  p_j = exp(scale * (q . x_j) - m).
+ * It reads rows where they lie, so a step that attends needs no staging and
+ * no dhs_gather.  Scores, sums and outputs are accumulated in float; the
+ * weights p_j are rounded to `dtype` for the second product, out once more.
+ * Asynchronous, in order on the pool's stream; results do not depend on how
+ * the rows were split (no atomics), only on the GPU's number of SMs.
+ * Errors: DHS_EINVAL (arguments, sizes, alignment, workspace), DHS_ESTATE
+ * (history of a source that is not admitted), DHS_ECUDA.
+ */
+int dhs_attend(dhs_pool *pool, const dhs_attend_step *st);
+
+/* dhs_attend on a caller's stream (not NULL), ordered as dhs_gather_on. */
+int dhs_attend_on(dhs_pool *pool, const dhs_attend_step *st, void *stream);
+
+/* --------------------------------------------------------- forks */
+
+/*
+ * Copy the whole state of request `req` into the empty request slot `child`
+ * (parallel samples, branches of a draft): for every admitted source its
+ * length, resident pages, tail ring and hot cache (rows, tags, stamps).  A
+ * step on the child then resolves as the same step on the parent would.
+ *   host_rows[src]      the child's own pinned rows, as for dhs_admit (entries
+ *                       of sources that are not admitted, and of window
+ *                       sources, are ignored); must not overlap the parent's
+ *   resident_masks      NULL: the child keeps the pages resident that the
+ *                       parent has resident; else resident_masks[src] is a
+ *                       mask as for dhs_admit or NULL for the parent's
+ * Pages take the lowest free slots, sources and pages ascending, under
+ * dhs_admit's capacity rule.  Pages are copied, not shared: dhs_reclaim
+ * promises that taking a request's pages frees them.  Rows that no resident
+ * page of the child holds are written to its host rows now; the resident
+ * pages' backup is deferred as in dhs_admit_device.  Everything is enqueued
+ * on the pool's stream.  Errors: DHS_EINVAL, DHS_ESTATE (nothing of req is
+ * admitted, or something of child is), DHS_EWOULDWAIT (*deficit_pages set),
+ * DHS_ENOMEM, DHS_ECUDA; the child stays empty.
+ */
+int dhs_fork(dhs_pool *pool, int32_t req, int32_t child, void *const *host_rows,
+             const uint8_t *const *resident_masks, int64_t *deficit_pages);
+
+/*
+ * Limit the optional capacity to the first `capacity_pages` page slots (at
+ * most the pool's optional_pages) and move every page that lies beyond them
+ * into the lowest free slots, lowest page slot first; *moved = pages moved.
+ * Afterwards no call reads or writes opt_dev past capacity_pages * page_rows
+ * rows (in stream order), so its owner may lend that memory out, and give it
+ * back with a larger capacity.  dhs_pool_used() packs the pages without a
+ * hole.  Location vectors that name moved pages go stale.  Errors:
+ * DHS_EINVAL, DHS_EWOULDWAIT (more pages in use than capacity_pages: nothing
+ * changed; dhs_reclaim frees some), DHS_ENOMEM, DHS_ECUDA.
+ */
+int dhs_compact(dhs_pool *pool, int64_t capacity_pages, int64_t *moved);
+
+/* The optional capacity in pages that dhs_compact set (-1: null pool). */
+int64_t dhs_pool_capacity(const dhs_pool *pool);
+
 /*
  * Synchronise the pool's stream, read and clear the sticky device status.
  * The pages have no passage for this call: device-side errors cannot be
