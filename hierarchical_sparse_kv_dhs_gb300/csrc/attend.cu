@@ -3,35 +3,286 @@
 //
 // "Adaptive DHiSparse", How it works / Memory split: sparse attention reads
 // the selected rows.  With x_j, y_j the key and the value of row j and s_j =
-// scale (q . x_j), one pass keeps m = max s_j, l = sum exp(s_j - m) and
-// o = sum exp(s_j - m) y_j; when m grows, l and o are scaled by
-// exp(m_old - m_new).  out = o / l, log-sum = m + ln l.
+// scale (q . x_j), one pass keeps a reference m, l = sum exp(s_j - m) and
+// o = sum exp(s_j - m) y_j.  m follows the running maximum: it moves only
+// when a score passes it by more than kSlack (a factor of 2^8, far inside
+// float and 16-bit range), and then l and o are scaled by exp(m_old - m_new).
+// out = o / l, log-sum = m + ln l.
+//
+// Both products run on the 5th-generation tensor cores with the rows as the
+// M side, because few query heads share a row and M is at least 64 there:
+//   S^T[128 rows x N] = X[128 x dk] . Q^T      (tile of 128 rows, N columns)
+//   O^T[dv x N]      += Y^T[dv x 128] . P^T    (M = 128 value elements)
+// A column is one (query, head) pair sharing the rows: up to 64 of them.
+// The tile of rows is staged once in shared memory and feeds both products
+// (as a K-major operand first, as an M-major one then); where keys and
+// values are the same bytes (one latent row) they are loaded once.  S^T, O^T
+// stay in tensor memory; a thread owns one row of S^T, so weights need no
+// shuffles, and the maximum is only reduced across rows when m moves.
+//
+// A block has 4 softmax warps, 8 loading warps and 1 issuing warp, joined by
+// mbarriers.  Rows lie at arbitrary addresses of four memories, so loads are
+// 16-byte asynchronous copies into the swizzled layout.  The launch is one
+// block per SM; all tiles of all jobs (a job: one item, kv head and block of
+// columns) are dealt out evenly in order, so that long and short items
+// balance; a job cut by a block's boundary leaves (m, l, o) parts that
+// merge_kernel joins in order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "dhs_internal.h"
 
 namespace dhs {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kTile = 128;                 // rows per tile
+constexpr int kSoftThreads = 128, kLoadThreads = 256;
+constexpr int kThreads = kSoftThreads + kLoadThreads + 32;
+constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk of a tile
+constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
+constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
+constexpr float kSlack = 8.f;              // log2 units
+constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
+constexpr int kLag = 3;                    // copy groups in flight per loading thread
+
+// How a launch's row slices are staged.
+struct Plan {
+  int32_t shared;        // the value is the key's beginning: loaded once
+  int32_t key_chunks;    // 64-element chunks of a key
+  int32_t only_chunks;   // of them in the key ring (all, unless shared)
+  int32_t units;         // value units
+  int32_t kslots, vslots;
+  int32_t alias;         // the weights take the key ring's only slot
+  uint32_t off_q, off_p, off_k, off_v;  // from the aligned shared-memory base
+  uint32_t smem;
+};
 
 template <int MAXI>
 struct AttendParams {
   AttendCommon c;
+  Plan plan;
   AttendItem items[MAXI];
 };
 static_assert(sizeof(AttendParams<kAttendItemsLarge>) <= 32764, "attend item table too large");
 
-__device__ __forceinline__ float to_float(const uint8_t* p, int f16) {
-  return f16 ? __half2float(*reinterpret_cast<const __half*>(p))
-             : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-// Row j of the item for query i: its address, or null when there is none.
-__device__ const uint8_t* row_of(const AttendCommon& c, const AttendItem& it, int i, int64_t j) {
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait.  A wait that runs out raises *gave_up; every later wait of
+// the block then falls through, so that all its warps still reach their end
+// (on wrong data: the launch's status says so).
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+  for (uint32_t n = 0; n < kWaitPolls; ++n) {
+    if (bar_try(bar, parity)) return;
+    if ((n & 255) == 255 && *gave_up) return;
+  }
+  *gave_up = 1;
+}
+
+// The same by whole warps, together again afterwards: what follows may be an
+// instruction that a warp executes as one (block barriers, tcgen05 loads).
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+  bar_wait(bar, parity, gave_up);
+  __syncwarp();
+}
+
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+// Arrives on `bar` once every product issued so far is done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tm_load16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"  // with the load: no use of it may move ahead
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tm_store16(uint32_t addr, const float (&v)[16]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(__float_as_uint(v[0])),
+      "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
+      "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])),
+      "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])),
+      "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])),
+      "r"(addr)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ bool named_or(int id, int threads, bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\n"
+      "bar.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Shared-memory operand descriptor: start, the two strides (bytes), swizzle
+// (2 = 128 B, 4 = 64 B, 6 = 32 B rows).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t sw) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lbo >> 4) << 16 |
+         (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)sw << 61;
+}
+
+// ------------------------------------------------------------------ jobs
+
+// A block's share of one job: tiles [t0, t1) of item `it`, columns [col0,
+// col0 + cols) of kv head g (column = query * group + head within the group
+// for a history; located items: query qbase, column = head).
+struct Segment {
+  const AttendItem* it;
+  int32_t tiles;     // of the whole job
+  int32_t t0, t1;    // the segment's tiles before clipping to visible rows
+  int32_t g, qbase, col0, cols;
+  int64_t lo, hi;    // rows any of the columns may see, relative to it->first
+  int32_t v0, v1;    // tiles that hold some of them (v0 >= v1: none)
+  __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// Rows [lo, hi) (relative to it.first) that query i of a history item sees.
+__device__ __forceinline__ void query_rows(const AttendItem& it, int i, int64_t& lo, int64_t& hi) {
+  const int64_t L = it.first + it.len;
+  lo = it.range ? max((int64_t)it.range[2 * i] - it.first, (int64_t)0) : 0;
+  hi = (it.range ? min((int64_t)it.range[2 * i + 1], L) : L - it.Q + 1 + i) - it.first;
+}
+
+// The segment that begins at tile `t` of the launch and ends before `te`.
+// Called by whole warps.
+template <int N, int MAXI>
+__device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te) {
+  const AttendCommon& c = P.c;
+  __syncwarp();
+  int a = 0, b = c.n_items;  // last item whose first tile is <= t (empty items have no tiles)
+  while (b - a > 1) {
+    const int m = (a + b) >> 1;
+    if (P.items[m].tile0 <= t) a = m;
+    else b = m;
+  }
+  Segment s;
+  s.it = &P.items[a];
+  const AttendItem& it = *s.it;
+  const bool located = it.loc != nullptr;
+  s.tiles = it.tiles;
+  int32_t job = (t - it.tile0) / it.tiles;
+  s.t0 = (t - it.tile0) - job * it.tiles;
+  s.t1 = min(it.tiles, s.t0 + (te - t));
+  const int32_t columns = located ? c.group : it.Q * c.group;
+  const int32_t nblk = (columns + N - 1) / N, width = (columns + nblk - 1) / nblk;
+  const int32_t blk = job % nblk;
+  job /= nblk;
+  const int32_t kv = c.heads / c.group;
+  s.g = job % kv;
+  s.qbase = job / kv;
+  s.col0 = blk * width;
+  s.cols = min(width, columns - s.col0);
+  s.lo = 0;
+  s.hi = it.len;
+  if (!located) {
+    const int q0 = s.col0 / c.group, q1 = (s.col0 + s.cols - 1) / c.group;
+    int64_t lo = it.len, hi = 0;
+    for (int i = q0 + (threadIdx.x & 31); i <= q1; i += 32) {
+      int64_t x, y;
+      query_rows(it, i, x, y);
+      if (x < y) {
+        lo = min(lo, x);
+        hi = max(hi, y);
+      }
+    }
+    for (int w = 16; w; w >>= 1) {
+      lo = min(lo, (int64_t)__shfl_xor_sync(~0u, (long long)lo, w));
+      hi = max(hi, (int64_t)__shfl_xor_sync(~0u, (long long)hi, w));
+    }
+    s.lo = lo;
+    s.hi = hi;
+  }
+  s.v0 = max(s.t0, (int32_t)(s.lo / kTile));
+  s.v1 = min(s.t1, (int32_t)((s.hi + kTile - 1) / kTile));
+  return s;
+}
+
+__host__ __device__ __forceinline__ int32_t first_tile(int64_t total, int blocks, int b) {
+  return (int32_t)(total * b / blocks);
+}
+
+// Address of row j of the job, or null when there is none.
+__device__ __forceinline__ const uint8_t* row_of(const AttendCommon& c, const Segment& s, int64_t j) {
+  const AttendItem& it = *s.it;
+  if (j < s.lo || j >= s.hi) return nullptr;
   if (it.loc) {
-    const int64_t e = (int64_t)i * it.len + j;
+    const int64_t e = (int64_t)s.qbase * it.len + j;
     uint32_t loc;
     if (it.index) {
       const int32_t u = it.index[e];
@@ -66,103 +317,879 @@ __device__ const uint8_t* row_of(const AttendCommon& c, const AttendItem& it, in
   return it.host + (size_t)r * c.row_bytes;
 }
 
-// One CTA per (item, query, head): warps take 32 rows in turn for the
-// scores, then every thread adds the rows to its output elements.
-template <int MAXI>
-__global__ void __launch_bounds__(kThreads)
-    attend_kernel(const __grid_constant__ AttendParams<MAXI> P) {
+// ------------------------------------------------------------------ kernel
+
+struct Control {
+  uint64_t kfull[kMaxK], kempty[kMaxK], vfull[kMaxV], vempty[kMaxV];
+  uint64_t qfull, qempty, sfull, pfull, ofull, oempty, rfull[2], rempty[2], drain;
+  uint64_t unused[13];  // to 64: two barriers a lane
+  const uint8_t* row[2][kTile];
+  int64_t out_off[64];
+  int32_t lse_at[64];
+  int32_t col_lo[64], col_hi[64];
+  float m[64], base[64], fac[64];
+  float part[4][64];
+  uint32_t odd[4];    // rows of the tile whose products are taken by hand
+  const uint8_t* odd_row;
+  uint32_t o_begun;   // the segment's sums hold such products before the first tile's
+  uint32_t tmem;
+  volatile uint32_t gave_up;
+};
+// Places of the single barriers in Control's order
+constexpr int kBarQfull = 2 * kMaxK + 2 * kMaxV, kBarPfull = kBarQfull + 3,
+              kBarOempty = kBarQfull + 5, kBarRfull = kBarQfull + 6, kBarRempty = kBarQfull + 8,
+              kBarDrain = kBarQfull + 10, kBarriers = 64;
+static_assert(kBarDrain + 1 + 13 == kBarriers, "barrier table");
+constexpr uint32_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
+
+// Parity bookkeeping of a ring of slots.
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__host__ __device__ constexpr uint32_t tmem_columns(int n) { return 5 * n <= 128 ? 128 : 5 * n <= 256 ? 256 : 512; }
+// Bytes of one row of weights, the swizzle of that row width, and its 8-row stride.
+__host__ __device__ constexpr int weight_row(int n) { return n <= 16 ? 32 : n <= 32 ? 64 : 128; }
+__host__ __device__ constexpr uint32_t weight_swizzle(int n) { return n <= 16 ? 6 : n <= 32 ? 4 : 2; }
+
+// Loading warps: queries once per segment, rows tile by tile.
+template <int N, int MAXI>
+__device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid,
+                          int32_t tb, int32_t te) {
   const AttendCommon& c = P.c;
-  __shared__ float sq[kAttendMaxKey];
-  __shared__ float sp[32];
-  __shared__ const uint8_t* srow[32];
-  const int job = blockIdx.x;
-  int n = 0;
-  while (n + 1 < c.n_items && P.items[n + 1].job0 <= job) ++n;
-  const AttendItem& it = P.items[n];
-  const int i = (job - it.job0) / c.heads, h = (job - it.job0) - i * c.heads;
-  const int g = h / c.group;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int d = tid; d < c.dk; d += kThreads)
-    sq[d] = to_float(it.q + i * c.q_qs + h * c.q_hs + 2 * d, c.f16);
-  int64_t lo = 0, hi = it.len;
-  if (!it.loc) {
-    const int64_t L = it.first + it.len;
-    const int64_t a = it.range ? it.range[2 * i] : 0;
-    const int64_t b = it.range ? it.range[2 * i + 1] : L - it.Q + 1 + i;
-    lo = max(a - it.first, (int64_t)0);
-    hi = min(b, L) - it.first;
-  }
-  float m = -INFINITY, l = 0.f, o[kAttendMaxValue / kThreads] = {};
-  for (int64_t j0 = lo; j0 < hi; j0 += 32) {
-    __syncthreads();
-    if (tid < 32) srow[tid] = j0 + tid < hi ? row_of(c, it, i, j0 + tid) : nullptr;
-    __syncthreads();
-    for (int j = warp; j < 32; j += kThreads / 32) {
-      const uint8_t* row = srow[j];
-      float s = 0.f;
-      if (row)
-        for (int d = lane; d < c.dk; d += 32)
-          s += sq[d] * to_float(row + c.key_off + (int64_t)g * c.key_stride + 2 * d, c.f16);
-      for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(~0u, s, w);
-      if (lane == 0) sp[j] = row ? s * c.scale : -INFINITY;
+  const Plan& pl = P.plan;
+  const uint32_t base = smem_u32(sm);
+  Ring kr, vr, rr;
+  uint32_t qphase = 0;
+  uint64_t fifo = 0;  // full barriers of the copy groups in flight, oldest in the low byte
+  int flying = 0;
+  auto full_bar = [&](uint32_t id) {
+    return id < kMaxK ? smem_u32(&ctl.kfull[id]) : smem_u32(&ctl.vfull[id - kMaxK]);
+  };
+  auto land = [&] {  // the oldest group has landed
+    fence_async();
+    bar_arrive(full_bar(fifo & 255));
+    fifo >>= 8;
+    --flying;
+  };
+  auto drain = [&] {
+    if (!flying) return;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    while (flying) land();
+  };
+  // wait for a slot, handing over what is in flight first: the consumer may
+  // need it before it frees the slot
+  auto wait_empty = [&](uint32_t bar, uint32_t parity) {
+    if (!bar_try(bar, parity)) {
+      drain();
+      bar_wait(bar, parity, &ctl.gave_up);
     }
-    __syncthreads();
-    float mn = m;
-    for (int j = 0; j < 32; ++j) mn = fmaxf(mn, sp[j]);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float f = expf(m - base);
-    l *= f;
-#pragma unroll
-    for (int u = 0; u < kAttendMaxValue / kThreads; ++u) o[u] *= f;
-    for (int j = 0; j < 32; ++j) {
-      if (!srow[j]) continue;
-      const float p = expf(sp[j] - base);
-      l += p;
-      const uint8_t* v = srow[j] + c.val_off + (int64_t)g * c.val_stride;
-#pragma unroll
-      for (int u = 0; u < kAttendMaxValue / kThreads; ++u)
-        if (tid + u * kThreads < c.dv) o[u] += p * to_float(v + 2 * (tid + u * kThreads), c.f16);
+    __syncwarp();
+  };
+  auto launch = [&](uint32_t id) {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    fifo |= (uint64_t)id << (8 * flying);
+    if (++flying > kLag) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+      land();
     }
-    m = mn;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  };
+  const int piece = tid & 7, r0 = tid >> 3;  // rows r0 + 32 i
+  bool first = true;
+  for (int32_t t = tb; t < te;) {
+    const Segment s = segment_at<N>(P, t, te);
+    t += s.t1 - s.t0;
+    if (s.v0 >= s.v1) continue;
+    const AttendItem& it = *s.it;
+    // queries: [chunk][column][128 B], zeros past the key and the columns
+    if (!first) {
+      drain();
+      warp_wait(smem_u32(&ctl.qempty), qphase, &ctl.gave_up);
+      qphase ^= 1;
+    }
+    first = false;
+    const bool aligned = !(((uintptr_t)it.q | c.q_qs | c.q_hs) & 15);
+    for (int e = tid; e < pl.key_chunks * N * 8; e += kLoadThreads) {
+      const int ch = e / (N * 8), col = e / 8 % N, pc = e & 7;
+      const int el = ch * 64 + pc * 8;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (el < c.dk && col < s.cols) {
+        const int qc = s.col0 + col;
+        const int qi = it.loc ? s.qbase : qc / c.group;
+        const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
+        const uint8_t* src = it.q + qi * c.q_qs + h * c.q_hs + 2 * el;
+        if (aligned) {
+          v = __ldg(reinterpret_cast<const uint4*>(src));
+        } else {
+          const uint16_t* s2 = reinterpret_cast<const uint16_t*>(src);
+          uint32_t w[4];
 #pragma unroll
-  for (int u = 0; u < kAttendMaxValue / kThreads; ++u) {
-    const int d = tid + u * kThreads;
-    if (d >= c.dv) continue;
-    uint8_t* out = it.out + i * c.o_qs + h * c.o_hs + 2 * d;
-    if (c.f16) *reinterpret_cast<__half*>(out) = __float2half_rn(o[u] * inv);
-    else *reinterpret_cast<__nv_bfloat16*>(out) = __float2bfloat16_rn(o[u] * inv);
+          for (int k = 0; k < 4; ++k) w[k] = s2[2 * k] | (uint32_t)s2[2 * k + 1] << 16;
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      *reinterpret_cast<uint4*>(sm + pl.off_q + (ch * N + col) * 128 + ((pc ^ (col & 7)) << 4)) = v;
+    }
+    fence_async();
+    bar_arrive(smem_u32(&ctl.qfull));
+
+    const uint32_t key_at = c.key_off + s.g * c.key_stride;
+    const uint32_t val_at = c.val_off + s.g * c.val_stride;
+    const uint8_t* ahead = tid < kTile ? row_of(c, s, (int64_t)s.v0 * kTile + tid) : nullptr;
+    for (int tile = s.v0; tile < s.v1; ++tile) {
+      // The tile's row addresses, to every loading thread and the softmax.
+      // Only the threads whose arrivals fill the slot wait for it: another
+      // could come late and find the phase it waits for already gone.
+      if (tid < kTile) {
+        wait_empty(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1);
+        ctl.row[rr.slot][tid] = ahead;
+        bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
+      }
+      named_sync(2, kLoadThreads);
+      const uint8_t* row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row[i] = ctl.row[rr.slot][r0 + 32 * i];
+      rr.next(2);
+      if (tid < kTile && tile + 1 < s.v1) ahead = row_of(c, s, (int64_t)(tile + 1) * kTile + tid);
+      // one 64-element chunk of the 128 rows: element el.. of a slice of
+      // `n` elements at byte `at` of each row
+      auto chunk = [&](uint32_t dst, uint32_t at, int el, int n) {
+        const int e = el + piece * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 32 * i;
+          const bool on = row[i] && e < n;
+          const uint8_t* src = on ? row[i] + at + 2 * e : c.tail;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           dst + r * 128 + ((piece ^ (r & 7)) << 4)),
+                       "l"(src), "r"(on ? 16 : 0)
+                       : "memory");
+        }
+      };
+      const int c0 = pl.key_chunks - pl.only_chunks;
+      for (int k = 0; k < pl.only_chunks; ++k) {
+        wait_empty(smem_u32(&ctl.kempty[kr.slot]), kr.phase ^ 1);
+        chunk(base + pl.off_k + kr.slot * kChunk, key_at, (c0 + k) * 64, c.dk);
+        launch(kr.slot);
+        kr.next(pl.kslots);
+      }
+      const int n = pl.shared ? c.dk : c.dv;
+      for (int u = 0; u < pl.units; ++u) {
+        wait_empty(smem_u32(&ctl.vempty[vr.slot]), vr.phase ^ 1);
+        const uint32_t dst = base + pl.off_v + vr.slot * kUnit;
+        chunk(dst, pl.shared ? key_at : val_at, u * 128, n);
+        if (u * 128 + 64 < n) chunk(dst + kChunk, pl.shared ? key_at : val_at, u * 128 + 64, n);
+        launch(kMaxK + vr.slot);
+        vr.next(pl.vslots);
+      }
+    }
   }
-  if (it.lse && tid == 0) it.lse[(size_t)i * c.heads + h] = l == 0.f ? -INFINITY : m + logf(l);
+  drain();
+}
+
+// Issuing warp.
+template <int N, int MAXI>
+__device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int lane,
+                               int32_t tb, int32_t te) {
+  const AttendCommon& c = P.c;
+  const Plan& pl = P.plan;
+  const uint32_t base = smem_u32(sm);
+  const uint32_t tm_s = ctl.tmem, tm_o = ctl.tmem + N;
+  const uint32_t type = c.f16 ? 0u : 1u;
+  // float accumulator, operand types, N, M = 128; the second product's
+  // operands are both M/N-major
+  const uint32_t id1 = 1u << 4 | type << 7 | type << 10 | (uint32_t)(N >> 3) << 17 | 8u << 24;
+  const uint32_t id2 = id1 | 1u << 15 | 1u << 16;
+  constexpr uint32_t psbo = 8 * weight_row(N), psw = weight_swizzle(N);
+  const uint32_t p_at = base + (pl.alias ? pl.off_k : pl.off_p);
+  Ring kr, vr;
+  uint32_t qphase = 0, pphase = 0, ophase = 0;
+  bool first = true;
+  for (int32_t t = tb; t < te;) {
+    const Segment s = segment_at<N>(P, t, te);
+    t += s.t1 - s.t0;
+    if (s.v0 >= s.v1) continue;
+    if (lane == 0) {
+      bar_wait(smem_u32(&ctl.qfull), qphase, &ctl.gave_up);
+      for (int tile = s.v0; tile < s.v1; ++tile) {
+        bool add = false;
+        auto scores = [&](uint32_t at, int ch) {  // chunk ch of the keys staged at `at`
+          const int steps = (min(64, c.dk - ch * 64) + 15) / 16;
+          for (int k = 0; k < steps; ++k) {
+            mma(tm_s, operand(at + k * 32, 16, 1024, 2),
+                operand(base + pl.off_q + ch * N * 128 + k * 32, 16, 1024, 2), id1, add);
+            add = true;
+          }
+        };
+        const int c0 = pl.key_chunks - pl.only_chunks;
+        const int kslot = kr.slot;
+        for (int k = 0; k < pl.only_chunks; ++k) {
+          bar_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
+          tc_after();
+          scores(base + pl.off_k + kr.slot * kChunk, c0 + k);
+          if (!pl.alias) commit(smem_u32(&ctl.kempty[kr.slot]));
+          kr.next(pl.kslots);
+        }
+        Ring v = vr;
+        if (pl.shared) {
+          for (int u = 0; u < pl.units; ++u) {
+            bar_wait(smem_u32(&ctl.vfull[v.slot]), v.phase, &ctl.gave_up);
+            tc_after();
+            const uint32_t at = base + pl.off_v + v.slot * kUnit;
+            scores(at, 2 * u);
+            if (2 * u + 1 < pl.key_chunks) scores(at + kChunk, 2 * u + 1);
+            v.next(pl.vslots);
+          }
+        }
+        commit(smem_u32(&ctl.sfull));
+        if (tile + 1 == s.v1) commit(smem_u32(&ctl.qempty));
+        bar_wait(smem_u32(&ctl.pfull), pphase, &ctl.gave_up);
+        pphase ^= 1;
+        if (tile == s.v0 && !first) {  // the previous segment's sums are read
+          bar_wait(smem_u32(&ctl.oempty), ophase, &ctl.gave_up);
+          ophase ^= 1;
+        }
+        tc_after();
+        const bool begun = *(volatile uint32_t*)&ctl.o_begun;
+        for (int u = 0; u < pl.units; ++u) {
+          if (!pl.shared) {
+            bar_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
+            tc_after();
+          }
+          const uint32_t at = base + pl.off_v + vr.slot * kUnit;
+          for (int k = 0; k < kTile / 16; ++k)
+            mma(tm_o + u * N, operand(at + k * 2048, kChunk, 1024, 2),
+                operand(p_at + k * 2 * psbo, 16, psbo, psw), id2, tile > s.v0 || k > 0 || begun);
+          commit(smem_u32(&ctl.vempty[vr.slot]));
+          vr.next(pl.vslots);
+        }
+        if (pl.alias) commit(smem_u32(&ctl.kempty[kslot]));
+      }
+      commit(smem_u32(&ctl.ofull));
+    }
+    qphase ^= 1;
+    first = false;
+    __syncwarp();
+  }
+  if (lane == 0) {  // nothing of ours is in flight when tensor memory goes back
+    commit(smem_u32(&ctl.drain));
+    for (uint32_t n = 0; n < kWaitPolls && !bar_try(smem_u32(&ctl.drain), 0); ++n) {
+    }
+  }
+}
+
+// Whether none of the n elements at `p` is an infinity or NaN.
+__device__ bool finite_row(const uint8_t* p, int n, int f16) {
+  const uint32_t e = f16 ? 0x7C00u : 0x7F80u;
+  bool ok = true;
+  for (int k = 0; k < n; k += 8) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 2 * k));
+    for (const uint32_t w : {v.x, v.y, v.z, v.w})
+      ok &= (w & e) != e && (w >> 16 & e) != e;
+  }
+  return ok;
+}
+
+// The products of the tile's rows marked `odd` (a thread's own row), added to
+// the sums of the columns that see them; their staged values become zeros.
+// Runs while no product is in flight: those of the tiles before are complete.
+template <int N, int MAXI, class F>
+__device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, const Segment& s, uint8_t* sm,
+                                      Control& ctl, int tid, bool odd, const uint8_t* row, Ring vr,
+                                      bool first, F load_scores) {
+  const AttendCommon& c = P.c;
+  const Plan& pl = P.plan;
+  const int warp = tid >> 5, lane = tid & 31;
+  const uint32_t tm_o = ctl.tmem + ((uint32_t)(warp * 32) << 16) + N;
+  const uint32_t marked = __ballot_sync(~0u, odd);
+  if (lane == 0) ctl.odd[warp] = marked;
+  if (first) {
+    for (int u = 0; u < pl.units; ++u)
+      for (int k0 = 0; k0 < N; k0 += 16) {
+        const float zero[16] = {};
+        tm_store16(tm_o + u * N + k0, zero);
+      }
+    if (tid == 0) ctl.o_begun = 1;
+  }
+  named_sync(1, kSoftThreads);
+  for (int r = 0; r < kTile; ++r) {
+    if (!(ctl.odd[r >> 5] >> (r & 31) & 1)) continue;
+    if (warp == r >> 5) {
+      for (int k0 = 0; k0 < N; k0 += 16) {
+        float v[16];
+        load_scores(k0, v);
+        if (lane == (r & 31)) {
+          for (int k = 0; k < 16; ++k) ctl.part[0][k0 + k] = exp2_fast(v[k] - ctl.base[k0 + k]);
+        }
+      }
+      if (lane == (r & 31)) ctl.odd_row = row + c.val_off + (int64_t)s.g * c.val_stride;
+      __syncwarp();
+    }
+    named_sync(1, kSoftThreads);
+    const uint8_t* y = ctl.odd_row;
+    for (int u = 0; u < pl.units; ++u) {
+      const int d = u * 128 + tid;
+      float x = 0.f;
+      if (d < c.dv)
+        x = c.f16 ? __half2float(*reinterpret_cast<const __half*>(y + 2 * d))
+                  : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(y + 2 * d));
+      for (int k0 = 0; k0 < N; k0 += 16) {
+        float v[16];
+        tm_load16(tm_o + u * N + k0, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (ctl.part[0][k0 + k] != 0.f) v[k] += ctl.part[0][k0 + k] * x;
+        tm_store16(tm_o + u * N + k0, v);
+      }
+    }
+    named_sync(1, kSoftThreads);
+  }
+  for (int u = 0; u < pl.units; ++u) {
+    warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
+    if (odd) {
+      uint8_t* at = sm + pl.off_v + vr.slot * kUnit + tid * 128;
+      for (int k = 0; k < 8; ++k) {
+        *reinterpret_cast<uint4*>(at + 16 * k) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(at + kChunk + 16 * k) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    vr.next(pl.vslots);
+  }
+}
+
+// Softmax warps: thread = row of the tile; then the segment's output.
+template <int N, int MAXI>
+__device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid,
+                             int32_t tb, int32_t te, float* parts) {
+  const AttendCommon& c = P.c;
+  const Plan& pl = P.plan;
+  const int warp = tid >> 5, lane = tid & 31;
+  const uint32_t tm_s = ctl.tmem + ((uint32_t)(warp * 32) << 16), tm_o = tm_s + N;
+  const float scale = c.scale * 1.44269504088896341f;  // log2 e
+  uint8_t* weights = sm + (pl.alias ? pl.off_k : pl.off_p);
+  Ring rr, vr;
+  uint32_t sphase = 0, ophase = 0;
+  for (int32_t t = tb; t < te;) {
+    const Segment s = segment_at<N>(P, t, te);
+    t += s.t1 - s.t0;
+    const AttendItem& it = *s.it;
+    named_sync(1, kSoftThreads);  // the previous segment's column tables are read
+    if (tid == 0) ctl.o_begun = 0;
+    if (tid < N) {
+      const bool on = tid < s.cols;
+      const int qc = s.col0 + min(tid, s.cols - 1);
+      const int qi = it.loc ? s.qbase : qc / c.group;
+      const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
+      ctl.out_off[tid] = qi * c.o_qs + h * c.o_hs;
+      ctl.lse_at[tid] = on ? qi * c.heads + h : -1;
+      int64_t lo = 0, hi = it.len;
+      if (!it.loc) query_rows(it, qi, lo, hi);
+      ctl.col_lo[tid] = (int32_t)min(lo, (int64_t)INT32_MAX);
+      ctl.col_hi[tid] = (int32_t)max(hi, (int64_t)INT32_MIN);
+      ctl.m[tid] = -INFINITY;
+      ctl.base[tid] = 0.f;
+    }
+    named_sync(1, kSoftThreads);
+    // rows [all_lo, all_hi) are visible to every column
+    int32_t all_lo = 0, all_hi = INT32_MAX;
+    if (!it.loc) {
+      for (int k = 0; k < s.cols; ++k) {
+        all_lo = max(all_lo, ctl.col_lo[k]);
+        all_hi = min(all_hi, ctl.col_hi[k]);
+      }
+    }
+    float l[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) l[k] = 0.f;
+
+    for (int tile = s.v0; tile < s.v1; ++tile) {
+      const int32_t j = tile * kTile + tid;
+      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, &ctl.gave_up);
+      const uint8_t* row = ctl.row[rr.slot][tid];
+      const bool live = row != nullptr;
+      bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
+      rr.next(2);
+      const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
+      warp_wait(smem_u32(&ctl.sfull), sphase, &ctl.gave_up);
+      sphase ^= 1;
+      tc_after();
+      auto load_scores = [&](int k0, float (&v)[16]) {
+        tm_load16(tm_s + k0, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          v[k] *= scale;
+          if (!live || (ragged && (j < ctl.col_lo[k0 + k] || j >= ctl.col_hi[k0 + k])))
+            v[k] = -INFINITY;
+        }
+      };
+      bool move = tile == s.v0;
+      if (!move) {
+        float over = -INFINITY;
+#pragma unroll
+        for (int k0 = 0; k0 < N; k0 += 16) {
+          float v[16];
+          load_scores(k0, v);
+          // an unset reference (-inf) gives +inf, or NaN for a score of -inf
+#pragma unroll
+          for (int k = 0; k < 16; ++k) over = fmaxf(over, v[k] - ctl.m[k0 + k]);
+        }
+        move = named_or(1, kSoftThreads, over > kSlack);
+      }
+      if (move) {  // new references: the maxima so far
+#pragma unroll
+        for (int k0 = 0; k0 < N; k0 += 16) {
+          float v[16];
+          load_scores(k0, v);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float x = v[k];
+            for (int w = 16; w; w >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, w));
+            if (lane == k) ctl.part[warp][k0 + k] = x;
+          }
+        }
+        named_sync(1, kSoftThreads);
+        if (tid < N) {
+          const float old = ctl.base[tid];
+          const float m = fmaxf(fmaxf(fmaxf(ctl.part[0][tid], ctl.part[1][tid]),
+                                      fmaxf(ctl.part[2][tid], ctl.part[3][tid])), ctl.m[tid]);
+          const float b = m == -INFINITY ? 0.f : m;
+          ctl.fac[tid] = ctl.m[tid] == -INFINITY ? 0.f : exp2_fast(old - b);
+          ctl.m[tid] = m;
+          ctl.base[tid] = b;
+        }
+        named_sync(1, kSoftThreads);
+        if (tile > s.v0) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) l[k] *= ctl.fac[k];
+          // products of the tiles before are complete: they were issued
+          // before this tile's scores
+          for (int u = 0; u < pl.units; ++u)
+#pragma unroll
+            for (int k0 = 0; k0 < N; k0 += 16) {
+              float v[16];
+              tm_load16(tm_o + u * N + k0, v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] *= ctl.fac[k0 + k];
+              tm_store16(tm_o + u * N + k0, v);
+            }
+        }
+      }
+      // A row that only some of the columns see would reach the others too
+      // if its value is not finite (0 x inf): such rows leave the tile, and
+      // their products are added by hand to the columns that see them.
+      bool odd = false;
+      __syncwarp();
+      if (ragged) {
+        if (live && (j < all_lo || j >= all_hi))
+          odd = !finite_row(row + c.val_off + (int64_t)s.g * c.val_stride, c.dv, c.f16);
+        if (named_or(1, kSoftThreads, odd)) {
+          odd_rows<N>(P, s, sm, ctl, tid, odd, row, vr, tile == s.v0, load_scores);
+        }
+      }
+      for (int u = 0; u < pl.units; ++u) vr.next(pl.vslots);
+      // weights: one row of N in the swizzled layout
+#pragma unroll
+      for (int k0 = 0; k0 < N; k0 += 16) {
+        float v[16];
+        load_scores(k0, v);
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const float x = exp2_fast(v[k] - ctl.base[k0 + k]);
+          const float y = exp2_fast(v[k + 1] - ctl.base[k0 + k + 1]);
+          l[k0 + k] += x;
+          l[k0 + k + 1] += y;
+          if (c.f16) {
+            const __half2 z = __floats2half2_rn(x, y);
+            w[k / 2] = *reinterpret_cast<const uint32_t*>(&z);
+          } else {
+            const __nv_bfloat162 z = __floats2bfloat162_rn(x, y);
+            w[k / 2] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          if (odd) w[k / 2] = 0;
+        }
+        constexpr int row_b = weight_row(N);
+        const int turn = row_b == 32 ? (tid >> 2) & 1 : row_b == 64 ? (tid >> 1) & 3 : tid & 7;
+        uint8_t* to = weights + tid * row_b;
+        *reinterpret_cast<uint4*>(to + (((k0 / 8) ^ turn) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(to + (((k0 / 8 + 1) ^ turn) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      fence_async();
+      tc_before();
+      bar_arrive(smem_u32(&ctl.pfull));
+    }
+
+    // l over the rows: 16 columns at a time, lane k (and k + 16) ends with column k
+    named_sync(1, kSoftThreads);
+#pragma unroll
+    for (int k0 = 0; k0 < N; k0 += 16) {
+      float v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = l[k0 + k] + __shfl_xor_sync(~0u, l[k0 + k], 16);
+#pragma unroll
+      for (int w = 8; w; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int k = 0; k < w; ++k) {
+          const float send = up ? v[k] : v[k + w], keep = up ? v[k + w] : v[k];
+          v[k] = keep + __shfl_xor_sync(~0u, send, w);
+        }
+      }
+      if (lane < 16) ctl.part[warp][k0 + lane] = v[0];
+    }
+    named_sync(1, kSoftThreads);
+    const bool none = s.v0 >= s.v1, whole = s.whole();
+    float* part = nullptr;
+    if (!whole) {
+      // a block leaves at most two parts: of the job it begins inside of,
+      // and of the job that it ends inside of
+      const int slot = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
+      part = parts + (size_t)slot * N * (c.dv + 2);
+    }
+    if (tid < N) {
+      const float z = ctl.part[0][tid] + ctl.part[1][tid] + ctl.part[2][tid] + ctl.part[3][tid];
+      if (whole) {
+        ctl.fac[tid] = z == 0.f ? 0.f : 1.f / z;
+        if (it.lse && ctl.lse_at[tid] >= 0)
+          it.lse[ctl.lse_at[tid]] =
+              z == 0.f ? -INFINITY : (ctl.base[tid] + log2f(z)) * 0.693147180559945309f;
+      } else {
+        ctl.fac[tid] = 1.f;
+        part[(size_t)N * c.dv + tid] = z == 0.f ? -INFINITY : ctl.base[tid];
+        part[(size_t)N * c.dv + N + tid] = z;
+      }
+    }
+    named_sync(1, kSoftThreads);
+    if (!none) {
+      warp_wait(smem_u32(&ctl.ofull), ophase, &ctl.gave_up);
+      ophase ^= 1;
+      tc_after();
+    }
+    for (int u = 0; u < pl.units; ++u) {
+      const int d = u * 128 + tid;
+#pragma unroll
+      for (int k0 = 0; k0 < N; k0 += 16) {
+        float v[16];
+        if (none) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = 0.f;
+        } else {
+          tm_load16(tm_o + u * N + k0, v);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          // a weight sum of zero leaves products of zero: the output is zero
+          const float x = ctl.fac[k0 + k] == 0.f ? 0.f : v[k] * ctl.fac[k0 + k];
+          if (d >= c.dv || k0 + k >= s.cols) {
+          } else if (!whole) {
+            part[(size_t)(k0 + k) * c.dv + d] = x;
+          } else if (c.f16) {
+            *reinterpret_cast<__half*>(it.out + ctl.out_off[k0 + k] + 2 * d) = __float2half_rn(x);
+          } else {
+            *reinterpret_cast<__nv_bfloat16*>(it.out + ctl.out_off[k0 + k] + 2 * d) =
+                __float2bfloat16_rn(x);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!none) {
+      tc_before();
+      bar_arrive(smem_u32(&ctl.oempty));
+    }
+  }
+}
+
+template <int N, int MAXI>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ AttendParams<MAXI> P, float* parts) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
+  Control& ctl = *reinterpret_cast<Control*>(sm);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == kThreads / 32 - 1) {
+#pragma unroll
+    for (int k = 0; k < kBarriers; k += 32) {
+      const int i = k + (tid & 31);
+      const bool full = i < kMaxK || (i >= 2 * kMaxK && i < 2 * kMaxK + kMaxV) || i == kBarQfull;
+      const bool soft = i == kBarPfull || i == kBarOempty || i == kBarRempty || i == kBarRempty + 1;
+      const bool rows = i == kBarRfull || i == kBarRfull + 1;
+      bar_init(smem_u32(&ctl.kfull[0]) + 8 * i,
+               full ? kLoadThreads : soft ? kSoftThreads : rows ? kTile : 1);
+    }
+    ctl.gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&ctl.tmem)),
+                 "r"(tmem_columns(N))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const int32_t tb = first_tile(P.c.n_tiles, gridDim.x, blockIdx.x);
+  const int32_t te = first_tile(P.c.n_tiles, gridDim.x, blockIdx.x + 1);
+  if (warp < kSoftThreads / 32) {
+    softmax_rows<N>(P, sm, ctl, tid, tb, te, parts);
+  } else if (warp < (kSoftThreads + kLoadThreads) / 32) {
+    load_rows<N>(P, sm, ctl, tid - kSoftThreads, tb, te);
+  } else {
+    issue_products<N>(P, sm, ctl, tid & 31, tb, te);
+  }
+  __syncwarp();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == kThreads / 32 - 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl.tmem),
+                 "r"(tmem_columns(N))
+                 : "memory");
+  if (tid == 0 && ctl.gave_up) atomicOr(P.c.status, kStatusEtimeout);
+}
+
+// ------------------------------------------------------------------ merge
+
+constexpr int kMergeThreads = 128;
+
+// One block per (split job, column): the job's parts, in block order.
+template <int N, int MAXI>
+__global__ void __launch_bounds__(kMergeThreads)
+    merge_kernel(const __grid_constant__ AttendParams<MAXI> P, const float* parts, int blocks) {
+  const AttendCommon& c = P.c;
+  __shared__ float weight[kAttendMaxBlocks];
+  __shared__ float total;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // block i's first tile cuts a job when it lies inside it; the first such
+  // block of a job joins its parts
+  const int b1 = blockIdx.x + 1;
+  const int32_t t = first_tile(c.n_tiles, blocks, b1);
+  const Segment s = segment_at<N>(P, t, t + 1);
+  const int32_t t_job = t - s.t0;  // the job's first tile
+  if (s.t0 == 0 || first_tile(c.n_tiles, blocks, b1 - 1) > t_job) return;
+  const int col = blockIdx.y;
+  if (col >= s.cols) return;
+  const int b0 = b1 - 1;
+  int b2 = b1 + 1;  // past the last block with tiles of the job
+  while (b2 < blocks && first_tile(c.n_tiles, blocks, b2) < t_job + s.tiles) ++b2;
+  const int n = b2 - b0;
+  const size_t stride = (size_t)N * (c.dv + 2);
+  auto part = [&](int i) { return parts + (size_t)(2 * (b0 + i) + (i == 0)) * stride; };
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[(size_t)N * c.dv + col]);
+    for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
+    const float base = m == -INFINITY ? 0.f : m;
+    float z = 0.f;
+    for (int i = lane; i < n; i += 32) {
+      const float* p = part(i) + (size_t)N * c.dv;
+      const float w = exp2f(p[col] - base);
+      weight[i] = w;
+      z += w * p[N + col];
+    }
+    for (int w = 16; w; w >>= 1) z += __shfl_xor_sync(~0u, z, w);
+    if (lane == 0) {
+      total = z;
+      const AttendItem& it = *s.it;
+      if (it.lse) {
+        const int qc = s.col0 + col;
+        const int qi = it.loc ? s.qbase : qc / c.group;
+        const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
+        it.lse[(size_t)qi * c.heads + h] =
+            z == 0.f ? -INFINITY : (base + log2f(z)) * 0.693147180559945309f;
+      }
+    }
+  }
+  __syncthreads();
+  const AttendItem& it = *s.it;
+  const int qc = s.col0 + col;
+  const int qi = it.loc ? s.qbase : qc / c.group;
+  const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
+  uint8_t* out = it.out + qi * c.o_qs + h * c.o_hs;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  for (int d = tid; d < c.dv; d += kMergeThreads) {
+    float x = 0.f;
+    for (int i = 0; i < n; ++i) {
+      // a part without weight may hold sums that were never written
+      if (weight[i] != 0.f) x += weight[i] * part(i)[(size_t)col * c.dv + d];
+    }
+    x = inv == 0.f ? 0.f : x * inv;
+    if (c.f16) *reinterpret_cast<__half*>(out + 2 * d) = __float2half_rn(x);
+    else *reinterpret_cast<__nv_bfloat16*>(out + 2 * d) = __float2bfloat16_rn(x);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr uint32_t kSmemLimit = 232448;  // opt-in shared memory of a block
+
+uint32_t round_up(uint32_t x, uint32_t to) { return (x + to - 1) / to * to; }
+
+// Ring sizes that fit shared memory: what a tile needs at once, then one
+// value unit and one key chunk more in turn while there is room.
+Plan make_plan(const AttendCommon& c, int n) {
+  Plan p{};
+  p.key_chunks = (c.dk + 63) / 64;
+  p.units = (c.dv + 127) / 128;
+  p.shared = c.val_off == c.key_off && c.dv <= c.dk &&
+             (c.heads == c.group || c.val_stride == c.key_stride);
+  p.only_chunks = p.shared ? std::max(0, p.key_chunks - 2 * p.units) : p.key_chunks;
+  const uint32_t q = round_up((uint32_t)p.key_chunks * n * 128, 1024);
+  const uint32_t w = (uint32_t)kTile * weight_row(n);
+  p.kslots = p.only_chunks ? 1 : 0;
+  p.vslots = p.units;
+  auto bytes = [&](int k, int v, bool alias) {
+    return 1024 + kControlBytes + q + (alias ? 0 : w) + (uint32_t)k * kChunk + (uint32_t)v * kUnit;
+  };
+  // the weights can take the place of a key chunk that is done with by then
+  p.alias = bytes(p.kslots, p.vslots, false) > kSmemLimit && p.only_chunks == 1;
+  for (bool more = true; more;) {
+    more = false;
+    if (p.vslots < std::min(kMaxV, 2 * p.units) && bytes(p.kslots, p.vslots + 1, p.alias) <= kSmemLimit) {
+      ++p.vslots;
+      more = true;
+    }
+    if (!p.alias && p.only_chunks && p.kslots < std::min(kMaxK, 2 * p.only_chunks) &&
+        bytes(p.kslots + 1, p.vslots, false) <= kSmemLimit) {
+      ++p.kslots;
+      more = true;
+    }
+  }
+  p.off_q = kControlBytes;
+  p.off_p = p.off_q + q;
+  p.off_k = round_up(p.off_p + (p.alias ? 0 : w), 1024);
+  p.off_v = p.off_k + (uint32_t)p.kslots * kChunk;
+  p.smem = 1024 + p.off_v + (uint32_t)p.vslots * kUnit;
+  return p;
+}
+
+// The widest block of columns whose queries leave room for a tile: 64, or 48
+// for the largest keys and values that are not the same bytes.
+int widest_block(const AttendCommon& c) {
+  int n = 64;
+  while (n > 16 && make_plan(c, n).smem > kSmemLimit) n -= 16;
+  return n;
+}
+
+struct Shape {
+  int n;            // columns of a block
+  int64_t tiles;
+  int blocks;
+  bool split;       // some job is cut by a block's boundary
+};
+
+int columns_of(const AttendCommon& c, const AttendItem& it, int most) {
+  const int all = it.loc ? c.group : it.Q * c.group;
+  const int blk = (all + most - 1) / most;
+  return (all + blk - 1) / blk;
+}
+
+// Fills in every item's tiles.
+Shape shape_of(const AttendCommon& c, AttendItem* items, int n_items, int sms) {
+  Shape s{};
+  const int most = widest_block(c);
+  int widest = 1;
+  for (int i = 0; i < n_items; ++i) widest = std::max(widest, columns_of(c, items[i], most));
+  s.n = (widest + 15) / 16 * 16;
+  const int kv = c.heads / c.group;
+  for (int i = 0; i < n_items; ++i) {
+    AttendItem& it = items[i];
+    it.tile0 = (int32_t)std::min<int64_t>(s.tiles, INT32_MAX);
+    // an item without rows still has one tile, that writes its empty outputs
+    it.tiles = (int32_t)std::max<int64_t>(1, (it.len + kTile - 1) / kTile);
+    const int64_t all = it.loc ? c.group : (int64_t)it.Q * c.group;
+    const int64_t jobs = (it.loc ? it.Q : 1) * (int64_t)kv * ((all + s.n - 1) / s.n);
+    s.tiles += jobs * it.tiles;
+  }
+  s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kAttendMaxBlocks), s.tiles));
+  if (s.tiles <= INT32_MAX) {
+    int k = 0;
+    for (int b = 1; b < s.blocks && !s.split; ++b) {
+      const int32_t t = first_tile(s.tiles, s.blocks, b);
+      while (k + 1 < n_items && items[k + 1].tile0 <= t) ++k;
+      s.split = (t - items[k].tile0) % items[k].tiles != 0;
+    }
+  }
+  return s;
+}
+
+template <int N, int MAXI>
+cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
+  attend_kernel<N, MAXI><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !s.split) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(s.blocks - 1, N);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel<N, MAXI>, P, (const float*)parts, s.blocks);
 }
 
 template <int MAXI>
-cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items,
-                     cudaStream_t stream) {
+cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items, const Shape& s,
+                     float* parts, cudaStream_t stream) {
   AttendParams<MAXI> P;
   P.c = c;
   P.c.n_items = n_items;
-  int64_t jobs = 0;
-  for (int i = 0; i < n_items; ++i) {
-    P.items[i] = items[i];
-    P.items[i].job0 = (int32_t)jobs;
-    jobs += (int64_t)items[i].Q * c.heads;
-    if (jobs > INT32_MAX) return cudaErrorInvalidValue;
+  P.c.n_tiles = (int32_t)s.tiles;
+  P.plan = make_plan(c, s.n);
+  for (int i = 0; i < n_items; ++i) P.items[i] = items[i];
+  switch (s.n) {
+    case 16: return launch_n<16, MAXI>(P, s, parts, stream);
+    case 32: return launch_n<32, MAXI>(P, s, parts, stream);
+    case 48: return launch_n<48, MAXI>(P, s, parts, stream);
+    default: return launch_n<64, MAXI>(P, s, parts, stream);
   }
-  P.c.n_jobs = (int32_t)jobs;
-  attend_kernel<MAXI><<<(int)jobs, kThreads, 0, stream>>>(P);
-  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attend(const AttendCommon& c, const AttendItem* items, int n_items,
-                          cudaStream_t stream) {
+cudaError_t attend_set_smem_limit() {
+  for (const void* k : {(const void*)attend_kernel<16, kAttendItemsSmall>,
+                        (const void*)attend_kernel<32, kAttendItemsSmall>,
+                        (const void*)attend_kernel<48, kAttendItemsSmall>,
+                        (const void*)attend_kernel<64, kAttendItemsSmall>,
+                        (const void*)attend_kernel<16, kAttendItemsLarge>,
+                        (const void*)attend_kernel<32, kAttendItemsLarge>,
+                        (const void*)attend_kernel<48, kAttendItemsLarge>,
+                        (const void*)attend_kernel<64, kAttendItemsLarge>}) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+bool attend_shape(const AttendCommon& c, AttendItem* items, int n_items, int sms, size_t* bytes) {
+  const Shape s = shape_of(c, items, n_items, sms);
+  *bytes = s.split ? (size_t)2 * s.blocks * s.n * (c.dv + 2) * sizeof(float) : 0;
+  return s.tiles <= INT32_MAX;
+}
+
+cudaError_t launch_attend(const AttendCommon& c, AttendItem* items, int n_items, int sms,
+                          void* work, cudaStream_t stream) {
   if (n_items <= 0) return cudaSuccess;
   if (n_items > kAttendItemsLarge) return cudaErrorInvalidValue;
-  return n_items <= kAttendItemsSmall ? launch_t<kAttendItemsSmall>(c, items, n_items, stream)
-                                      : launch_t<kAttendItemsLarge>(c, items, n_items, stream);
+  const Shape s = shape_of(c, items, n_items, sms);
+  if (s.tiles > INT32_MAX) return cudaErrorInvalidValue;
+  float* parts = static_cast<float*>(work);
+  return n_items <= kAttendItemsSmall
+             ? launch_t<kAttendItemsSmall>(c, items, n_items, s, parts, stream)
+             : launch_t<kAttendItemsLarge>(c, items, n_items, s, parts, stream);
 }
 
 }  // namespace dhs

@@ -303,7 +303,8 @@ struct AttendItem {
   int32_t pair;
   int32_t complete;       // history items: complete imported pages
   int32_t Q;
-  int32_t job0;           // first job of this item in the launch
+  int32_t tiles;          // tiles of each of its jobs
+  int32_t tile0;          // first tile of this item in the launch
 };
 
 struct AttendCommon {
@@ -314,7 +315,7 @@ struct AttendCommon {
   uint32_t tail_rows, opt_rows, hot_rows;  // arena sizes in rows
   int32_t row_bytes, T, Pmax, page_shift;
   uint32_t* status;
-  int32_t n_items, n_jobs;
+  int32_t n_items, n_tiles;
   int32_t f16;            // rows are f16, else bf16
   int32_t heads, group;   // query heads, query heads per kv head
   int32_t dk, dv;         // elements of a key and of a value
@@ -323,8 +324,14 @@ struct AttendCommon {
   int64_t q_qs, q_hs, o_qs, o_hs;  // bytes
 };
 
-cudaError_t launch_attend(const AttendCommon& c, const AttendItem* items, int n_items,
-                          cudaStream_t stream);
+constexpr int kAttendMaxBlocks = 256;
+
+// Once per device: let the attention's blocks use all of an SM's shared memory.
+cudaError_t attend_set_smem_limit();
+// Workspace of a launch; fills in the items' tiles.  False: too many tiles.
+bool attend_shape(const AttendCommon& c, AttendItem* items, int n_items, int sms, size_t* bytes);
+cudaError_t launch_attend(const AttendCommon& c, AttendItem* items, int n_items, int sms,
+                          void* work, cudaStream_t stream);
 
 // ------------------------------------------------------------ forks
 constexpr int kForkSourcesMax = 256;

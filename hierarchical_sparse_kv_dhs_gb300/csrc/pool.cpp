@@ -678,7 +678,8 @@ int dhs_pool_create(const dhs_pool_config* cfg, dhs_pool** out) {
   }
   if (dhs::resolve_set_carveout() != cudaSuccess ||
       dhs::hostcopy_set_carveout(copy_hold_limit(optin)) != cudaSuccess ||
-      dhs::gather_set_carveout() != cudaSuccess || dhs::append_set_carveout() != cudaSuccess) {
+      dhs::gather_set_carveout() != cudaSuccess || dhs::append_set_carveout() != cudaSuccess ||
+      dhs::attend_set_smem_limit() != cudaSuccess) {
     delete p;
     return DHS_ECUDA;
   }
@@ -1719,6 +1720,8 @@ int dhs_read_state(dhs_pool* p, int32_t req, int32_t src, int32_t* tags, uint32_
 // ---------------------------------------------------------------------------
 // Attention over located rows and histories (attend.cu).
 
+}  // extern "C"
+
 static int validate_attend(dhs_pool* p, const dhs_attend_step* st) {
   if (!p || !st || st->n_items < 0 || (st->n_items > 0 && !st->items)) return DHS_EINVAL;
   const dhs_pool_config& c = p->cfg;
@@ -1757,14 +1760,8 @@ static int validate_attend(dhs_pool* p, const dhs_attend_step* st) {
   return DHS_OK;
 }
 
-int dhs_attend_bytes(dhs_pool* p, const dhs_attend_step* st, size_t* bytes) {
-  if (bytes) *bytes = 0;
-  if (!bytes) return DHS_EINVAL;
-  return validate_attend(p, st);
-}
-
-// Launch the attention of every item of a validated, flushed step.
-static int launch_attends(dhs_pool* p, const dhs_attend_step* st) {
+// The common parameters and the item table (p->titems) of a validated step.
+static int attend_tables(dhs_pool* p, const dhs_attend_step* st, dhs::AttendCommon* out) {
   const dhs_pool_config& c = p->cfg;
   dhs::AttendCommon a{};
   a.tail = (const uint8_t*)c.tail_dev;
@@ -1786,13 +1783,14 @@ static int launch_attends(dhs_pool* p, const dhs_attend_step* st) {
   a.dv = st->value_elems;
   a.key_off = st->key_offset * 2;
   a.val_off = st->value_offset * 2;
-  a.key_stride = st->key_stride * 2;
-  a.val_stride = st->value_stride * 2;
+  a.key_stride = st->kv_heads > 1 ? st->key_stride * 2 : 0;
+  a.val_stride = st->kv_heads > 1 ? st->value_stride * 2 : 0;
   a.scale = st->scale;
   a.q_qs = st->q_query_stride * 2;
   a.q_hs = st->q_head_stride * 2;
   a.o_qs = st->out_query_stride * 2;
   a.o_hs = st->out_head_stride * 2;
+  *out = a;
   try {
     p->titems.clear();
     for (int32_t i = 0; i < st->n_items; ++i) {
@@ -1822,12 +1820,59 @@ static int launch_attends(dhs_pool* p, const dhs_attend_step* st) {
   } catch (...) {
     return DHS_ENOMEM;
   }
+  return DHS_OK;
+}
+
+// Calls f(items, n) for every launch's share of the item table.
+template <class F>
+static int each_attend_launch(dhs_pool* p, F f) {
   for (size_t b = 0; b < p->titems.size(); b += dhs::kAttendItemsLarge) {
     const int n = (int)std::min<size_t>(dhs::kAttendItemsLarge, p->titems.size() - b);
-    if (dhs::launch_attend(a, p->titems.data() + b, n, p->stream) != cudaSuccess)
-      return DHS_ECUDA;
+    const int rc = f(p->titems.data() + b, n);
+    if (rc) return rc;
   }
   return DHS_OK;
+}
+
+// Workspace bytes of a step whose tables are made.
+static int attend_work(dhs_pool* p, const dhs::AttendCommon& a, size_t* bytes) {
+  *bytes = 0;
+  return each_attend_launch(p, [&](dhs::AttendItem* items, int n) {
+    size_t need = 0;
+    if (!dhs::attend_shape(a, items, n, std::max(1, p->sm_count), &need)) return DHS_EINVAL;
+    *bytes = std::max(*bytes, need);
+    return DHS_OK;
+  });
+}
+
+// Validation, tables and the check of the workspace.
+static int prepare_attend(dhs_pool* p, const dhs_attend_step* st, dhs::AttendCommon* a) {
+  int rc = validate_attend(p, st);
+  if (rc) return rc;
+  if ((rc = attend_tables(p, st, a))) return rc;
+  size_t need = 0;
+  if ((rc = attend_work(p, *a, &need))) return rc;
+  if (need && (!st->work_dev || (uintptr_t)st->work_dev % kAlign || st->work_bytes < need))
+    return DHS_EINVAL;
+  return DHS_OK;
+}
+
+static int launch_attends(dhs_pool* p, const dhs_attend_step* st, const dhs::AttendCommon& a) {
+  return each_attend_launch(p, [&](dhs::AttendItem* items, int n) {
+    return cuda_rc(dhs::launch_attend(a, items, n, std::max(1, p->sm_count), st->work_dev, p->stream));
+  });
+}
+
+extern "C" {
+
+int dhs_attend_bytes(dhs_pool* p, const dhs_attend_step* st, size_t* bytes) {
+  if (bytes) *bytes = 0;
+  if (!bytes) return DHS_EINVAL;
+  dhs::AttendCommon a;
+  int rc = validate_attend(p, st);
+  if (rc) return rc;
+  if ((rc = attend_tables(p, st, &a))) return rc;
+  return attend_work(p, a, bytes);
 }
 
 // Attention only reads rows: gathers and attentions still running on other
@@ -1841,20 +1886,22 @@ static int enter_attend(dhs_pool* p) {
 }
 
 int dhs_attend(dhs_pool* p, const dhs_attend_step* st) {
-  int rc = validate_attend(p, st);
+  dhs::AttendCommon a;
+  int rc = prepare_attend(p, st, &a);
   if (rc) return rc;
   if ((rc = enter_attend(p))) return rc;
   if ((rc = flush(p))) return rc;
-  return launch_attends(p, st);
+  return launch_attends(p, st, a);
 }
 
 int dhs_attend_on(dhs_pool* p, const dhs_attend_step* st, void* stream) {
   if (!stream) return DHS_EINVAL;
-  int rc = validate_attend(p, st);
+  dhs::AttendCommon a;
+  int rc = prepare_attend(p, st, &a);
   if (rc) return rc;
   if ((rc = enter_attend(p))) return rc;
   if ((rc = flush(p))) return rc;
-  return on_stream(p, stream, [&] { return launch_attends(p, st); });
+  return on_stream(p, stream, [&] { return launch_attends(p, st, a); });
 }
 
 // ---------------------------------------------------------------------------
