@@ -20,7 +20,7 @@
 // stay in tensor memory; a thread owns one row of S^T, so weights need no
 // shuffles, and the maximum is only reduced across rows when m moves.
 //
-// A block has 4 softmax warps, 8 loading warps and 1 issuing warp, joined by
+// A block has 8 softmax warps, 4 loading warps and 1 issuing warp, joined by
 // mbarriers.  Rows lie at arbitrary addresses of four memories, so loads are
 // 16-byte asynchronous copies into the swizzled layout.  The launch is one
 // block per SM; all tiles of all jobs (a job: one item, kv head and block of
@@ -38,14 +38,14 @@ namespace dhs {
 namespace {
 
 constexpr int kTile = 128;                 // rows per tile
-constexpr int kSoftThreads = 128, kLoadThreads = 256;
+constexpr int kSoftThreads = 256, kLoadThreads = 128;
 constexpr int kThreads = kSoftThreads + kLoadThreads + 32;
 constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk of a tile
 constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
 constexpr float kSlack = 8.f;              // log2 units
 constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
-constexpr int kLag = 3;                    // copy groups in flight per loading thread
+constexpr int kLag = 3;                    // copy groups in flight per loading thread (see drain)
 
 // How a launch's row slices are staged.
 struct Plan {
@@ -121,11 +121,24 @@ __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// One of the warp's threads, the same one each time.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(p)::"memory");
+  return p != 0;
+}
+
+// D += A B (D = A B unless add) with operand descriptors given as halves: the
+// high one is fixed for a kind of operand, the low one moves with the address.
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t ahi, uint32_t b, uint32_t bhi,
+                                    uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 x, y;\n"
+      "mov.b64 x, {%1, %2};\nmov.b64 y, {%3, %4};\nsetp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(ahi), "r"(b), "r"(bhi), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
 
@@ -136,34 +149,42 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       : "memory");
 }
 
-__device__ __forceinline__ void tm_load16(uint32_t addr, float (&v)[16]) {
-  uint32_t r[16];
-  __syncwarp();
+// Eight columns of the warp's 32 lanes.  The values may be used only behind
+// tm_wait, which every later use depends on.
+__device__ __forceinline__ void tm_load8(uint32_t addr, float* v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"  // with the load: no use of it may move ahead
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7])
       : "r"(addr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tm_store16(uint32_t addr, const float (&v)[16]) {
+template <int C>
+__device__ __forceinline__ void tm_wait(float (&v)[C]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < C; ++k) asm volatile("" : "+f"(v[k]));
+}
+
+template <int C>
+__device__ __forceinline__ void tm_load(uint32_t addr, float (&v)[C]) {
   __syncwarp();
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(__float_as_uint(v[0])),
-      "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
-      "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])),
-      "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])),
-      "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])),
-      "r"(addr)
-      : "memory");
+#pragma unroll
+  for (int k = 0; k < C; k += 8) tm_load8(addr + k, v + k);
+  tm_wait(v);
+}
+
+template <int C>
+__device__ __forceinline__ void tm_store(uint32_t addr, const float (&v)[C]) {
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < C; k += 8)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(v[k]),
+        "f"(v[k + 1]), "f"(v[k + 2]), "f"(v[k + 3]), "f"(v[k + 4]), "f"(v[k + 5]), "f"(v[k + 6]),
+        "f"(v[k + 7]), "r"(addr + k)
+        : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
@@ -190,11 +211,34 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Shared-memory operand descriptor: start, the two strides (bytes), swizzle
-// (2 = 128 B, 4 = 64 B, 6 = 32 B rows).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t sw) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lbo >> 4) << 16 |
-         (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)sw << 61;
+// Shared-memory operand descriptor.  Low half: start and leading stride
+// (bytes); high half: 8-row stride, format version, swizzle (2 = 128 B, 4 =
+// 64 B, 6 = 32 B rows).
+__device__ __forceinline__ uint32_t operand_lo(uint32_t addr, uint32_t lead) {
+  return (addr & 0x3FFFF) >> 4 | (lead >> 4) << 16;
+}
+__host__ __device__ constexpr uint32_t operand_hi(uint32_t eight, uint32_t swizzle) {
+  return eight >> 4 | 1u << 14 | swizzle << 29;
+}
+
+// Eight values of each lane reduced over the warp: lane i gets the result of
+// value i & 7.
+template <class F>
+__device__ __forceinline__ float fold8(const float* in, int lane, F f) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = in[k];
+#pragma unroll
+  for (int w = 4; w; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int k = 0; k < w; ++k) {
+      const float send = up ? v[k] : v[k + w], keep = up ? v[k + w] : v[k];
+      v[k] = f(keep, __shfl_xor_sync(~0u, send, w));
+    }
+  }
+  v[0] = f(v[0], __shfl_xor_sync(~0u, v[0], 8));
+  return f(v[0], __shfl_xor_sync(~0u, v[0], 16));
 }
 
 // ------------------------------------------------------------------ jobs
@@ -327,7 +371,7 @@ struct Control {
   int64_t out_off[64];
   int32_t lse_at[64];
   int32_t col_lo[64], col_hi[64];
-  float m[64], base[64], fac[64];
+  alignas(16) float m[64], base[64], fac[64];
   float part[4][64];
   uint32_t odd[4];    // rows of the tile whose products are taken by hand
   const uint8_t* odd_row;
@@ -379,10 +423,19 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     fifo >>= 8;
     --flying;
   };
-  auto drain = [&] {
-    if (!flying) return;
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    while (flying) land();
+  auto drain = [&] {  // oldest first, so that the products start with it
+    if (flying == 3) {
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      land();
+    }
+    if (flying == 2) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      land();
+    }
+    if (flying == 1) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      land();
+    }
   };
   // wait for a slot, handing over what is in flight first: the consumer may
   // need it before it frees the slot
@@ -401,7 +454,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
       land();
     }
   };
-  const int piece = tid & 7, r0 = tid >> 3;  // rows r0 + 32 i
+  const int piece = tid & 7, r0 = tid >> 3;  // rows r0 + 16 i
   bool first = true;
   for (int32_t t = tb; t < te;) {
     const Segment s = segment_at<N>(P, t, te);
@@ -442,29 +495,26 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
 
     const uint32_t key_at = c.key_off + s.g * c.key_stride;
     const uint32_t val_at = c.val_off + s.g * c.val_stride;
-    const uint8_t* ahead = tid < kTile ? row_of(c, s, (int64_t)s.v0 * kTile + tid) : nullptr;
+    static_assert(kLoadThreads == kTile, "one row address per loading thread");
+    const uint8_t* ahead = row_of(c, s, (int64_t)s.v0 * kTile + tid);
     for (int tile = s.v0; tile < s.v1; ++tile) {
-      // The tile's row addresses, to every loading thread and the softmax.
-      // Only the threads whose arrivals fill the slot wait for it: another
-      // could come late and find the phase it waits for already gone.
-      if (tid < kTile) {
-        wait_empty(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1);
-        ctl.row[rr.slot][tid] = ahead;
-        bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
-      }
+      // the tile's row addresses, to every loading thread and the softmax
+      wait_empty(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1);
+      ctl.row[rr.slot][tid] = ahead;
+      bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
       named_sync(2, kLoadThreads);
-      const uint8_t* row[4];
+      const uint8_t* row[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) row[i] = ctl.row[rr.slot][r0 + 32 * i];
+      for (int i = 0; i < 8; ++i) row[i] = ctl.row[rr.slot][r0 + 16 * i];
       rr.next(2);
-      if (tid < kTile && tile + 1 < s.v1) ahead = row_of(c, s, (int64_t)(tile + 1) * kTile + tid);
+      if (tile + 1 < s.v1) ahead = row_of(c, s, (int64_t)(tile + 1) * kTile + tid);
       // one 64-element chunk of the 128 rows: element el.. of a slice of
       // `n` elements at byte `at` of each row
       auto chunk = [&](uint32_t dst, uint32_t at, int el, int n) {
         const int e = el + piece * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + 32 * i;
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 16 * i;
           const bool on = row[i] && e < n;
           const uint8_t* src = on ? row[i] + at + 2 * e : c.tail;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -494,10 +544,10 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
   drain();
 }
 
-// Issuing warp.
+// Issuing warp: all its lanes walk the same path, one of them issues.
 template <int N, int MAXI>
-__device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int lane,
-                               int32_t tb, int32_t te) {
+__device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int32_t tb,
+                               int32_t te) {
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
   const uint32_t base = smem_u32(sm);
@@ -507,82 +557,92 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
   // operands are both M/N-major
   const uint32_t id1 = 1u << 4 | type << 7 | type << 10 | (uint32_t)(N >> 3) << 17 | 8u << 24;
   const uint32_t id2 = id1 | 1u << 15 | 1u << 16;
-  constexpr uint32_t psbo = 8 * weight_row(N), psw = weight_swizzle(N);
-  const uint32_t p_at = base + (pl.alias ? pl.off_k : pl.off_p);
+  constexpr uint32_t psbo = 8 * weight_row(N);
+  constexpr uint32_t hi = operand_hi(1024, 2), hi_p = operand_hi(psbo, weight_swizzle(N));
+  const uint32_t q_lo = operand_lo(base + pl.off_q, 16);
+  const uint32_t p_lo = operand_lo(base + (pl.alias ? pl.off_k : pl.off_p), 16);
+  const uint32_t k_lo = operand_lo(base + pl.off_k, 16);
+  const uint32_t v_lo = operand_lo(base + pl.off_v, 16), vt_lo = operand_lo(base + pl.off_v, kChunk);
+  const bool lead = elected();
+  const int c0 = pl.key_chunks - pl.only_chunks;
+  const int last_steps = (c.dk - (pl.key_chunks - 1) * 64 + 15) / 16;
   Ring kr, vr;
   uint32_t qphase = 0, pphase = 0, ophase = 0;
   bool first = true;
+  // the products of key chunk `ch` staged at `at`
+  auto scores = [&](uint32_t at, int ch, bool add) {
+    const uint32_t b = q_lo + ch * (N * 128 >> 4);
+    const int steps = ch + 1 < pl.key_chunks ? 4 : last_steps;
+    if (!lead) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < steps) mma(tm_s, at + 2 * k, hi, b + 2 * k, hi, id1, add || k > 0);
+  };
   for (int32_t t = tb; t < te;) {
     const Segment s = segment_at<N>(P, t, te);
     t += s.t1 - s.t0;
     if (s.v0 >= s.v1) continue;
-    if (lane == 0) {
-      bar_wait(smem_u32(&ctl.qfull), qphase, &ctl.gave_up);
-      for (int tile = s.v0; tile < s.v1; ++tile) {
-        bool add = false;
-        auto scores = [&](uint32_t at, int ch) {  // chunk ch of the keys staged at `at`
-          const int steps = (min(64, c.dk - ch * 64) + 15) / 16;
-          for (int k = 0; k < steps; ++k) {
-            mma(tm_s, operand(at + k * 32, 16, 1024, 2),
-                operand(base + pl.off_q + ch * N * 128 + k * 32, 16, 1024, 2), id1, add);
-            add = true;
-          }
-        };
-        const int c0 = pl.key_chunks - pl.only_chunks;
-        const int kslot = kr.slot;
-        for (int k = 0; k < pl.only_chunks; ++k) {
-          bar_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
+    warp_wait(smem_u32(&ctl.qfull), qphase, &ctl.gave_up);
+    qphase ^= 1;
+    for (int tile = s.v0; tile < s.v1; ++tile) {
+      const int kslot = kr.slot;
+      for (int k = 0; k < pl.only_chunks; ++k) {
+        warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
+        tc_after();
+        scores(k_lo + kr.slot * (kChunk >> 4), c0 + k, k > 0);
+        if (lead && !pl.alias) commit(smem_u32(&ctl.kempty[kr.slot]));
+        kr.next(pl.kslots);
+      }
+      Ring v = vr;
+      if (pl.shared) {
+        for (int u = 0; u < pl.units; ++u) {
+          warp_wait(smem_u32(&ctl.vfull[v.slot]), v.phase, &ctl.gave_up);
           tc_after();
-          scores(base + pl.off_k + kr.slot * kChunk, c0 + k);
-          if (!pl.alias) commit(smem_u32(&ctl.kempty[kr.slot]));
-          kr.next(pl.kslots);
+          const uint32_t at = v_lo + v.slot * (kUnit >> 4);
+          scores(at, 2 * u, pl.only_chunks > 0 || u > 0);
+          if (2 * u + 1 < pl.key_chunks) scores(at + (kChunk >> 4), 2 * u + 1, true);
+          v.next(pl.vslots);
         }
-        Ring v = vr;
-        if (pl.shared) {
-          for (int u = 0; u < pl.units; ++u) {
-            bar_wait(smem_u32(&ctl.vfull[v.slot]), v.phase, &ctl.gave_up);
-            tc_after();
-            const uint32_t at = base + pl.off_v + v.slot * kUnit;
-            scores(at, 2 * u);
-            if (2 * u + 1 < pl.key_chunks) scores(at + kChunk, 2 * u + 1);
-            v.next(pl.vslots);
-          }
-        }
+      }
+      if (lead) {
         commit(smem_u32(&ctl.sfull));
         if (tile + 1 == s.v1) commit(smem_u32(&ctl.qempty));
-        bar_wait(smem_u32(&ctl.pfull), pphase, &ctl.gave_up);
-        pphase ^= 1;
-        if (tile == s.v0 && !first) {  // the previous segment's sums are read
-          bar_wait(smem_u32(&ctl.oempty), ophase, &ctl.gave_up);
-          ophase ^= 1;
-        }
-        tc_after();
-        const bool begun = *(volatile uint32_t*)&ctl.o_begun;
-        for (int u = 0; u < pl.units; ++u) {
-          if (!pl.shared) {
-            bar_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
-            tc_after();
-          }
-          const uint32_t at = base + pl.off_v + vr.slot * kUnit;
-          for (int k = 0; k < kTile / 16; ++k)
-            mma(tm_o + u * N, operand(at + k * 2048, kChunk, 1024, 2),
-                operand(p_at + k * 2 * psbo, 16, psbo, psw), id2, tile > s.v0 || k > 0 || begun);
-          commit(smem_u32(&ctl.vempty[vr.slot]));
-          vr.next(pl.vslots);
-        }
-        if (pl.alias) commit(smem_u32(&ctl.kempty[kslot]));
       }
-      commit(smem_u32(&ctl.ofull));
+      warp_wait(smem_u32(&ctl.pfull), pphase, &ctl.gave_up);
+      pphase ^= 1;
+      if (tile == s.v0 && !first) {  // the previous segment's sums are read
+        warp_wait(smem_u32(&ctl.oempty), ophase, &ctl.gave_up);
+        ophase ^= 1;
+      }
+      tc_after();
+      const bool begun = tile > s.v0 || *(volatile uint32_t*)&ctl.o_begun;
+      for (int u = 0; u < pl.units; ++u) {
+        if (!pl.shared) {
+          warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
+          tc_after();
+        }
+        if (lead) {
+          const uint32_t at = vt_lo + vr.slot * (kUnit >> 4);
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma(tm_o + u * N, at + k * (2048 >> 4), hi, p_lo + k * (2 * psbo >> 4), hi_p, id2,
+                begun || k > 0);
+          commit(smem_u32(&ctl.vempty[vr.slot]));
+        }
+        vr.next(pl.vslots);
+      }
+      if (lead) {
+        if (pl.alias) commit(smem_u32(&ctl.kempty[kslot]));
+        if (tile + 1 == s.v1) commit(smem_u32(&ctl.ofull));
+      }
     }
-    qphase ^= 1;
     first = false;
-    __syncwarp();
   }
-  if (lane == 0) {  // nothing of ours is in flight when tensor memory goes back
-    commit(smem_u32(&ctl.drain));
-    for (uint32_t n = 0; n < kWaitPolls && !bar_try(smem_u32(&ctl.drain), 0); ++n) {
-    }
+  // nothing of ours is in flight when tensor memory goes back
+  if (lead) commit(smem_u32(&ctl.drain));
+  for (uint32_t n = 0; n < kWaitPolls && !bar_try(smem_u32(&ctl.drain), 0); ++n) {
   }
+  __syncwarp();
 }
 
 // Whether none of the n elements at `p` is an infinity or NaN.
@@ -597,64 +657,65 @@ __device__ bool finite_row(const uint8_t* p, int n, int f16) {
   return ok;
 }
 
-// The products of the tile's rows marked `odd` (a thread's own row), added to
-// the sums of the columns that see them; their staged values become zeros.
-// Runs while no product is in flight: those of the tiles before are complete.
-template <int N, int MAXI, class F>
-__device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, const Segment& s, uint8_t* sm,
-                                      Control& ctl, int tid, bool odd, const uint8_t* row, Ring vr,
-                                      bool first, F load_scores) {
+// The products of the tile's rows marked `odd` (thread = row and half of the
+// columns), added to the sums of the columns that see them; their staged
+// values become zeros.  Runs while no product is in flight: those of the
+// tiles before are complete.
+template <int N, int MAXI>
+__device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl,
+                                      int tid, bool odd, const uint8_t* value, Ring vr,
+                                      int32_t tile0, bool first) {
+  constexpr int C = N / 2;
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
-  const int warp = tid >> 5, lane = tid & 31;
-  const uint32_t tm_o = ctl.tmem + ((uint32_t)(warp * 32) << 16) + N;
+  const int r = tid & (kTile - 1), k0 = tid / kTile * C;
+  const uint32_t tm_s = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0, tm_o = tm_s + N;
+  const float scale = c.scale * 1.44269504088896341f;
   const uint32_t marked = __ballot_sync(~0u, odd);
-  if (lane == 0) ctl.odd[warp] = marked;
+  if ((tid & 31) == 0 && tid < kTile) ctl.odd[tid >> 5] = marked;
+  float v[8];
   if (first) {
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
     for (int u = 0; u < pl.units; ++u)
-      for (int k0 = 0; k0 < N; k0 += 16) {
-        const float zero[16] = {};
-        tm_store16(tm_o + u * N + k0, zero);
-      }
+      for (int k = 0; k < C; k += 8) tm_store(tm_o + u * N + k, v);
     if (tid == 0) ctl.o_begun = 1;
   }
   named_sync(1, kSoftThreads);
-  for (int r = 0; r < kTile; ++r) {
-    if (!(ctl.odd[r >> 5] >> (r & 31) & 1)) continue;
-    if (warp == r >> 5) {
-      for (int k0 = 0; k0 < N; k0 += 16) {
-        float v[16];
-        load_scores(k0, v);
-        if (lane == (r & 31)) {
-          for (int k = 0; k < 16; ++k) ctl.part[0][k0 + k] = exp2_fast(v[k] - ctl.base[k0 + k]);
-        }
+  for (int i = 0; i < kTile; ++i) {
+    if (!(ctl.odd[i >> 5] >> (i & 31) & 1)) continue;
+    if ((r >> 5) == (i >> 5)) {  // the warps that own the row
+      for (int k = 0; k < C; k += 8) {
+        tm_load(tm_s + k, v);
+        if (r == i)
+          for (int n = 0; n < 8; ++n) {
+            const int col = k0 + k + n;
+            const bool seen = tile0 + i >= ctl.col_lo[col] && tile0 + i < ctl.col_hi[col];
+            ctl.part[0][col] = seen ? exp2_fast(v[n] * scale - ctl.base[col]) : 0.f;
+          }
       }
-      if (lane == (r & 31)) ctl.odd_row = row + c.val_off + (int64_t)s.g * c.val_stride;
-      __syncwarp();
+      if (r == i) ctl.odd_row = value;
     }
     named_sync(1, kSoftThreads);
     const uint8_t* y = ctl.odd_row;
     for (int u = 0; u < pl.units; ++u) {
-      const int d = u * 128 + tid;
-      float x = 0.f;
+      const int d = u * 128 + r;
+      float e = 0.f;
       if (d < c.dv)
-        x = c.f16 ? __half2float(*reinterpret_cast<const __half*>(y + 2 * d))
+        e = c.f16 ? __half2float(*reinterpret_cast<const __half*>(y + 2 * d))
                   : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(y + 2 * d));
-      for (int k0 = 0; k0 < N; k0 += 16) {
-        float v[16];
-        tm_load16(tm_o + u * N + k0, v);
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (ctl.part[0][k0 + k] != 0.f) v[k] += ctl.part[0][k0 + k] * x;
-        tm_store16(tm_o + u * N + k0, v);
+      for (int k = 0; k < C; k += 8) {
+        tm_load(tm_o + u * N + k, v);
+        for (int n = 0; n < 8; ++n)
+          if (ctl.part[0][k0 + k + n] != 0.f) v[n] += ctl.part[0][k0 + k + n] * e;
+        tm_store(tm_o + u * N + k, v);
       }
     }
     named_sync(1, kSoftThreads);
   }
   for (int u = 0; u < pl.units; ++u) {
     warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
-    if (odd) {
-      uint8_t* at = sm + pl.off_v + vr.slot * kUnit + tid * 128;
+    if (odd && tid < kTile) {
+      uint8_t* at = sm + pl.off_v + vr.slot * kUnit + r * 128;
       for (int k = 0; k < 8; ++k) {
         *reinterpret_cast<uint4*>(at + 16 * k) = make_uint4(0, 0, 0, 0);
         *reinterpret_cast<uint4*>(at + kChunk + 16 * k) = make_uint4(0, 0, 0, 0);
@@ -664,18 +725,23 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, const Segment
   }
 }
 
-// Softmax warps: thread = row of the tile; then the segment's output.
+// Softmax warps: a thread has one row of the tile and half of the columns;
+// then the segment's output.
 template <int N, int MAXI>
 __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid,
                              int32_t tb, int32_t te, float* parts) {
+  constexpr int C = N / 2;
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
-  const int warp = tid >> 5, lane = tid & 31;
-  const uint32_t tm_s = ctl.tmem + ((uint32_t)(warp * 32) << 16), tm_o = tm_s + N;
+  const int lane = tid & 31, r = tid & (kTile - 1), quarter = r >> 5, k0 = tid / kTile * C;
+  const uint32_t tm_s = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0, tm_o = tm_s + N;
   const float scale = c.scale * 1.44269504088896341f;  // log2 e
-  uint8_t* weights = sm + (pl.alias ? pl.off_k : pl.off_p);
+  uint8_t* const weights = sm + (pl.alias ? pl.off_k : pl.off_p) + r * weight_row(N);
+  const int turn = weight_row(N) == 32 ? (r >> 2) & 1 : weight_row(N) == 64 ? (r >> 1) & 3 : r & 7;
   Ring rr, vr;
   uint32_t sphase = 0, ophase = 0;
+  auto larger = [](float a, float b) { return fmaxf(a, b); };
+  auto sum = [](float a, float b) { return a + b; };
   for (int32_t t = tb; t < te;) {
     const Segment s = segment_at<N>(P, t, te);
     t += s.t1 - s.t0;
@@ -705,79 +771,70 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
         all_hi = min(all_hi, ctl.col_hi[k]);
       }
     }
-    float l[N];
+    float l[C];
 #pragma unroll
-    for (int k = 0; k < N; ++k) l[k] = 0.f;
+    for (int k = 0; k < C; ++k) l[k] = 0.f;
 
     for (int tile = s.v0; tile < s.v1; ++tile) {
-      const int32_t j = tile * kTile + tid;
+      const int32_t j = tile * kTile + r;
       warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, &ctl.gave_up);
-      const uint8_t* row = ctl.row[rr.slot][tid];
-      const bool live = row != nullptr;
+      const uint8_t* row = ctl.row[rr.slot][r];
       bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
       rr.next(2);
       const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
       warp_wait(smem_u32(&ctl.sfull), sphase, &ctl.gave_up);
       sphase ^= 1;
       tc_after();
-      auto load_scores = [&](int k0, float (&v)[16]) {
-        tm_load16(tm_s + k0, v);
+      float x[C];  // scores in log2 units
+      tm_load(tm_s, x);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          v[k] *= scale;
-          if (!live || (ragged && (j < ctl.col_lo[k0 + k] || j >= ctl.col_hi[k0 + k])))
-            v[k] = -INFINITY;
-        }
-      };
+      for (int k = 0; k < C; ++k) x[k] = row ? x[k] * scale : -INFINITY;
+      if (ragged) {
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+          if (j < ctl.col_lo[k0 + k] || j >= ctl.col_hi[k0 + k]) x[k] = -INFINITY;
+      }
       bool move = tile == s.v0;
       if (!move) {
+        // an unset reference (-inf) gives +inf, or NaN for a score of -inf
         float over = -INFINITY;
 #pragma unroll
-        for (int k0 = 0; k0 < N; k0 += 16) {
-          float v[16];
-          load_scores(k0, v);
-          // an unset reference (-inf) gives +inf, or NaN for a score of -inf
-#pragma unroll
-          for (int k = 0; k < 16; ++k) over = fmaxf(over, v[k] - ctl.m[k0 + k]);
+        for (int k = 0; k < C; k += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&ctl.m[k0 + k]);
+          over = fmaxf(fmaxf(fmaxf(over, x[k] - m.x), x[k + 1] - m.y),
+                       fmaxf(x[k + 2] - m.z, x[k + 3] - m.w));
         }
         move = named_or(1, kSoftThreads, over > kSlack);
       }
       if (move) {  // new references: the maxima so far
 #pragma unroll
-        for (int k0 = 0; k0 < N; k0 += 16) {
-          float v[16];
-          load_scores(k0, v);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x = v[k];
-            for (int w = 16; w; w >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, w));
-            if (lane == k) ctl.part[warp][k0 + k] = x;
-          }
+        for (int k = 0; k < C; k += 8) {
+          const float y = fold8(x + k, lane, larger);
+          if (lane < 8) ctl.part[quarter][k0 + k + lane] = y;
         }
         named_sync(1, kSoftThreads);
         if (tid < N) {
-          const float old = ctl.base[tid];
+          const float old = ctl.m[tid];
           const float m = fmaxf(fmaxf(fmaxf(ctl.part[0][tid], ctl.part[1][tid]),
-                                      fmaxf(ctl.part[2][tid], ctl.part[3][tid])), ctl.m[tid]);
+                                      fmaxf(ctl.part[2][tid], ctl.part[3][tid])), old);
           const float b = m == -INFINITY ? 0.f : m;
-          ctl.fac[tid] = ctl.m[tid] == -INFINITY ? 0.f : exp2_fast(old - b);
+          ctl.fac[tid] = old == -INFINITY ? 0.f : exp2_fast(old - b);
           ctl.m[tid] = m;
           ctl.base[tid] = b;
         }
         named_sync(1, kSoftThreads);
         if (tile > s.v0) {
 #pragma unroll
-          for (int k = 0; k < N; ++k) l[k] *= ctl.fac[k];
+          for (int k = 0; k < C; ++k) l[k] *= ctl.fac[k0 + k];
           // products of the tiles before are complete: they were issued
           // before this tile's scores
           for (int u = 0; u < pl.units; ++u)
+            for (int k = 0; k < C; k += 8) {
+              float v[8];
+              tm_load(tm_o + u * N + k, v);
 #pragma unroll
-            for (int k0 = 0; k0 < N; k0 += 16) {
-              float v[16];
-              tm_load16(tm_o + u * N + k0, v);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] *= ctl.fac[k0 + k];
-              tm_store16(tm_o + u * N + k0, v);
+              for (int i = 0; i < 8; ++i) v[i] *= ctl.fac[k0 + k + i];
+              tm_store(tm_o + u * N + k, v);
             }
         }
       }
@@ -785,64 +842,50 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       // if its value is not finite (0 x inf): such rows leave the tile, and
       // their products are added by hand to the columns that see them.
       bool odd = false;
-      __syncwarp();
       if (ragged) {
-        if (live && (j < all_lo || j >= all_hi))
-          odd = !finite_row(row + c.val_off + (int64_t)s.g * c.val_stride, c.dv, c.f16);
-        if (named_or(1, kSoftThreads, odd)) {
-          odd_rows<N>(P, s, sm, ctl, tid, odd, row, vr, tile == s.v0, load_scores);
-        }
+        const uint8_t* value = row + c.val_off + (int64_t)s.g * c.val_stride;
+        if (row && (j < all_lo || j >= all_hi)) odd = !finite_row(value, c.dv, c.f16);
+        if (named_or(1, kSoftThreads, odd))
+          odd_rows<N>(P, sm, ctl, tid, odd, value, vr, tile * kTile, tile == s.v0);
       }
       for (int u = 0; u < pl.units; ++u) vr.next(pl.vslots);
-      // weights: one row of N in the swizzled layout
+      // weights: half of a row of N in the swizzled layout
 #pragma unroll
-      for (int k0 = 0; k0 < N; k0 += 16) {
-        float v[16];
-        load_scores(k0, v);
-        uint32_t w[8];
+      for (int k = 0; k < C; k += 8) {
+        const float4 b0 = *reinterpret_cast<const float4*>(&ctl.base[k0 + k]);
+        const float4 b1 = *reinterpret_cast<const float4*>(&ctl.base[k0 + k + 4]);
+        const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+        float p[8];
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const float x = exp2_fast(v[k] - ctl.base[k0 + k]);
-          const float y = exp2_fast(v[k + 1] - ctl.base[k0 + k + 1]);
-          l[k0 + k] += x;
-          l[k0 + k + 1] += y;
-          if (c.f16) {
-            const __half2 z = __floats2half2_rn(x, y);
-            w[k / 2] = *reinterpret_cast<const uint32_t*>(&z);
-          } else {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(x, y);
-            w[k / 2] = *reinterpret_cast<const uint32_t*>(&z);
-          }
-          if (odd) w[k / 2] = 0;
+        for (int i = 0; i < 8; ++i) {
+          p[i] = exp2_fast(x[k + i] - b[i]);
+          l[k + i] += p[i];
         }
-        constexpr int row_b = weight_row(N);
-        const int turn = row_b == 32 ? (tid >> 2) & 1 : row_b == 64 ? (tid >> 1) & 3 : tid & 7;
-        uint8_t* to = weights + tid * row_b;
-        *reinterpret_cast<uint4*>(to + (((k0 / 8) ^ turn) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(to + (((k0 / 8 + 1) ^ turn) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (c.f16) {
+            const __half2 z = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&z);
+          } else {
+            const __nv_bfloat162 z = __floats2bfloat162_rn(p[2 * i], p[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          if (odd) w[i] = 0;
+        }
+        *reinterpret_cast<uint4*>(weights + ((((k0 + k) / 8) ^ turn) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_async();
       tc_before();
       bar_arrive(smem_u32(&ctl.pfull));
     }
 
-    // l over the rows: 16 columns at a time, lane k (and k + 16) ends with column k
     named_sync(1, kSoftThreads);
 #pragma unroll
-    for (int k0 = 0; k0 < N; k0 += 16) {
-      float v[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = l[k0 + k] + __shfl_xor_sync(~0u, l[k0 + k], 16);
-#pragma unroll
-      for (int w = 8; w; w >>= 1) {
-        const bool up = lane & w;
-#pragma unroll
-        for (int k = 0; k < w; ++k) {
-          const float send = up ? v[k] : v[k + w], keep = up ? v[k + w] : v[k];
-          v[k] = keep + __shfl_xor_sync(~0u, send, w);
-        }
-      }
-      if (lane < 16) ctl.part[warp][k0 + lane] = v[0];
+    for (int k = 0; k < C; k += 8) {
+      const float y = fold8(l + k, lane, sum);
+      if (lane < 8) ctl.part[quarter][k0 + k + lane] = y;
     }
     named_sync(1, kSoftThreads);
     const bool none = s.v0 >= s.v1, whole = s.whole();
@@ -873,31 +916,27 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       tc_after();
     }
     for (int u = 0; u < pl.units; ++u) {
-      const int d = u * 128 + tid;
+      const int d = u * 128 + r;
+      float v[C];
+      if (none) {
 #pragma unroll
-      for (int k0 = 0; k0 < N; k0 += 16) {
-        float v[16];
-        if (none) {
+        for (int k = 0; k < C; ++k) v[k] = 0.f;
+      } else {
+        tm_load(tm_o + u * N, v);
+      }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = 0.f;
+      for (int k = 0; k < C; ++k) {
+        // a weight sum of zero leaves products of zero: the output is zero
+        const float y = ctl.fac[k0 + k] == 0.f ? 0.f : v[k] * ctl.fac[k0 + k];
+        if (d >= c.dv || k0 + k >= s.cols) {
+        } else if (!whole) {
+          part[(size_t)(k0 + k) * c.dv + d] = y;
+        } else if (c.f16) {
+          *reinterpret_cast<__half*>(it.out + ctl.out_off[k0 + k] + 2 * d) = __float2half_rn(y);
         } else {
-          tm_load16(tm_o + u * N + k0, v);
+          *reinterpret_cast<__nv_bfloat16*>(it.out + ctl.out_off[k0 + k] + 2 * d) =
+              __float2bfloat16_rn(y);
         }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          // a weight sum of zero leaves products of zero: the output is zero
-          const float x = ctl.fac[k0 + k] == 0.f ? 0.f : v[k] * ctl.fac[k0 + k];
-          if (d >= c.dv || k0 + k >= s.cols) {
-          } else if (!whole) {
-            part[(size_t)(k0 + k) * c.dv + d] = x;
-          } else if (c.f16) {
-            *reinterpret_cast<__half*>(it.out + ctl.out_off[k0 + k] + 2 * d) = __float2half_rn(x);
-          } else {
-            *reinterpret_cast<__nv_bfloat16*>(it.out + ctl.out_off[k0 + k] + 2 * d) =
-                __float2bfloat16_rn(x);
-          }
-        }
-        __syncwarp();
       }
     }
     if (!none) {
@@ -944,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < (kSoftThreads + kLoadThreads) / 32) {
     load_rows<N>(P, sm, ctl, tid - kSoftThreads, tb, te);
   } else {
-    issue_products<N>(P, sm, ctl, tid & 31, tb, te);
+    issue_products<N>(P, sm, ctl, tb, te);
   }
   __syncwarp();
   tc_before();

@@ -641,3 +641,65 @@ def test_refusals(dhs):
         st.work_dev = buf.data_ptr()
         assert env.pool.attend(st) == 0
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", ["latent", "latent_100", "grouped", "odd", "largest"])
+@pytest.mark.parametrize("L", [3, 128, 130, 389])
+def test_history_row_that_is_not_finite(dhs, name, L):
+    """A row with NaN that only the block's later queries see leaves the
+    earlier ones untouched."""
+    lay, Q = LAYOUTS[name], 5
+    env = History(dhs, lay, [L], T=24, seed=11)
+    for back in (1, 2, 3):  # the last rows, the third from the end by query 2 on
+        if L < back:
+            continue
+        rows = torch.full((1, lay.elems), NAN, device="cuda").to(env.rows.dtype)
+        env.rows[0, L - back] = rows
+    # a pool of its own whose ring holds the damaged rows
+    pool = dhs.Pool(max_requests=1, sources=1, row_bytes=lay.elems * 2, page_rows=PAGE, tail_rows=24,
+                    hot_rows=16, max_queries=8, max_topk=16, max_rows_per_request=L + 1,
+                    optional_pages=L // PAGE + 1)
+    host = torch.zeros((L + 1) * lay.elems * 2, dtype=torch.uint8).pin_memory()
+    assert pool.admit_device(0, 0, env.rows[0].data_ptr(), host.data_ptr(), L)[0] == 0
+    env.pool = pool
+    (it, (q, o, lse, _)), = env.items(Q)
+    run(dhs, pool, lay, [it])
+    torch.cuda.synchronize()
+    first_bad = max(0, L - 3)
+    for i in range(Q):
+        end = max(0, L - Q + 1 + i)
+        if end > first_bad:
+            assert bool(o[i].isnan().all()) and bool(lse[i].isnan().all()), i
+        else:
+            keep = torch.arange(L, device="cuda")[None] < end
+            compare(lay, q[i:i + 1], env.rows[0, :L][None], keep, o[i:i + 1], lse[i:i + 1])
+
+
+@pytest.mark.parametrize("name", ["grouped", "grouped_f16", "interleaved", "largest"])
+def test_history_value_that_is_infinite(dhs, name):
+    """An infinite value element reaches that element of the queries that see
+    its row, and nothing else."""
+    lay, Q, L = LAYOUTS[name], 4, 150
+    env = History(dhs, lay, [L], T=24, seed=12, appended=0)
+    g = lay.kv - 1
+    at = lay.value_offset + g * lay.value_stride + 3
+    clean = env.rows.clone()
+    env.rows[0, L - 2, at] = math.inf
+    pool = dhs.Pool(max_requests=1, sources=1, row_bytes=lay.elems * 2, page_rows=PAGE, tail_rows=24,
+                    hot_rows=16, max_queries=8, max_topk=16, max_rows_per_request=L + 1,
+                    optional_pages=L // PAGE + 1)
+    host = torch.zeros((L + 1) * lay.elems * 2, dtype=torch.uint8).pin_memory()
+    assert pool.admit_device(0, 0, env.rows[0].data_ptr(), host.data_ptr(), L)[0] == 0
+    env.pool = pool
+    (it, (q, o, lse, _)), = env.items(Q)
+    run(dhs, pool, lay, [it])
+    torch.cuda.synchronize()
+    heads = slice(g * (lay.heads // lay.kv), lay.heads)
+    sees = torch.arange(Q, device="cuda") >= 2  # rows below L - 3 + i include L - 2
+    assert bool((o[sees][:, heads, 3] == math.inf).all())
+    o[sees, heads, 3] = 0
+    keep = torch.arange(L, device="cuda")[None] < (L - Q + 1 + torch.arange(Q, device="cuda"))[:, None]
+    ro, rl, tol, ltol = reference(lay, q, clean[0, :L][None], keep)
+    ro[sees, heads, 3] = 0
+    assert bool(((o.double() - ro).abs() <= tol).all())
+    assert bool(((lse.double() - rl).abs() <= ltol).all())
