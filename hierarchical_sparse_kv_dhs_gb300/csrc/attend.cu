@@ -45,7 +45,6 @@ constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
 constexpr float kSlack = 8.f;              // log2 units
 constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
-constexpr int kLag = 3;                    // copy groups in flight per loading thread (see drain)
 
 // How a launch's row slices are staged.
 struct Plan {
@@ -412,47 +411,12 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
   const uint32_t base = smem_u32(sm);
   Ring kr, vr, rr;
   uint32_t qphase = 0;
-  uint64_t fifo = 0;  // full barriers of the copy groups in flight, oldest in the low byte
-  int flying = 0;
-  auto full_bar = [&](uint32_t id) {
-    return id < kMaxK ? smem_u32(&ctl.kfull[id]) : smem_u32(&ctl.vfull[id - kMaxK]);
-  };
-  auto land = [&] {  // the oldest group has landed
-    fence_async();
-    bar_arrive(full_bar(fifo & 255));
-    fifo >>= 8;
-    --flying;
-  };
-  auto drain = [&] {  // oldest first, so that the products start with it
-    if (flying == 3) {
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-      land();
-    }
-    if (flying == 2) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      land();
-    }
-    if (flying == 1) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      land();
-    }
-  };
-  // wait for a slot, handing over what is in flight first: the consumer may
-  // need it before it frees the slot
-  auto wait_empty = [&](uint32_t bar, uint32_t parity) {
-    if (!bar_try(bar, parity)) {
-      drain();
-      bar_wait(bar, parity, &ctl.gave_up);
-    }
-    __syncwarp();
-  };
-  auto launch = [&](uint32_t id) {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    fifo |= (uint64_t)id << (8 * flying);
-    if (++flying > kLag) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-      land();
-    }
+  auto wait_empty = [&](uint32_t bar, uint32_t parity) { warp_wait(bar, parity, &ctl.gave_up); };
+  // The slot's barrier gets this thread's arrival when its copies so far have
+  // landed.  The issuing warp makes them visible to the tensor cores: a proxy
+  // fence here would wait for every copy in flight.
+  auto launch = [&](uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
   };
   const int piece = tid & 7, r0 = tid >> 3;  // rows r0 + 16 i
   bool first = true;
@@ -463,7 +427,6 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     const AttendItem& it = *s.it;
     // queries: [chunk][column][128 B], zeros past the key and the columns
     if (!first) {
-      drain();
       warp_wait(smem_u32(&ctl.qempty), qphase, &ctl.gave_up);
       qphase ^= 1;
     }
@@ -527,7 +490,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
       for (int k = 0; k < pl.only_chunks; ++k) {
         wait_empty(smem_u32(&ctl.kempty[kr.slot]), kr.phase ^ 1);
         chunk(base + pl.off_k + kr.slot * kChunk, key_at, (c0 + k) * 64, c.dk);
-        launch(kr.slot);
+        launch(smem_u32(&ctl.kfull[kr.slot]));
         kr.next(pl.kslots);
       }
       const int n = pl.shared ? c.dk : c.dv;
@@ -536,12 +499,12 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
         const uint32_t dst = base + pl.off_v + vr.slot * kUnit;
         chunk(dst, pl.shared ? key_at : val_at, u * 128, n);
         if (u * 128 + 64 < n) chunk(dst + kChunk, pl.shared ? key_at : val_at, u * 128 + 64, n);
-        launch(kMaxK + vr.slot);
+        launch(smem_u32(&ctl.vfull[vr.slot]));
         vr.next(pl.vslots);
       }
     }
   }
-  drain();
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Issuing warp: all its lanes walk the same path, one of them issues.
@@ -588,6 +551,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
       const int kslot = kr.slot;
       for (int k = 0; k < pl.only_chunks; ++k) {
         warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
+        fence_async();
         tc_after();
         scores(k_lo + kr.slot * (kChunk >> 4), c0 + k, k > 0);
         if (lead && !pl.alias) commit(smem_u32(&ctl.kempty[kr.slot]));
@@ -597,6 +561,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
       if (pl.shared) {
         for (int u = 0; u < pl.units; ++u) {
           warp_wait(smem_u32(&ctl.vfull[v.slot]), v.phase, &ctl.gave_up);
+          fence_async();
           tc_after();
           const uint32_t at = v_lo + v.slot * (kUnit >> 4);
           scores(at, 2 * u, pl.only_chunks > 0 || u > 0);
@@ -619,6 +584,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
       for (int u = 0; u < pl.units; ++u) {
         if (!pl.shared) {
           warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
+          fence_async();
           tc_after();
         }
         if (lead) {
