@@ -964,49 +964,55 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ merge
 
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 512, kMergeGroups = 4;  // groups of 128 threads
 
-// One block per (split job, column): the job's parts, in block order.
+// Joins the parts of the jobs that a block's boundary cuts, in block order.
+// Block (x, y): the job that boundary x + 1 is the first to cut, if any.  A
+// few parts: each group of threads takes a column of its own.  Many: the
+// groups share one column's parts.  (152 parts of 16 columns, 5 MB: see the
+// design notes for the time beside the attention's.)
 template <int N, int MAXI>
 __global__ void __launch_bounds__(kMergeThreads)
-    merge_kernel(const __grid_constant__ AttendParams<MAXI> P, const float* parts, int blocks) {
+    merge_kernel(const __grid_constant__ AttendParams<MAXI> P, const float* parts, int blocks,
+                 int share) {
   const AttendCommon& c = P.c;
-  __shared__ float weight[kAttendMaxBlocks];
-  __shared__ float total;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // block i's first tile cuts a job when it lies inside it; the first such
-  // block of a job joins its parts
+  __shared__ float weight[kMergeGroups][kAttendMaxBlocks];
+  __shared__ float total[kMergeGroups];
+  __shared__ float4 sums[kMergeGroups][kAttendMaxValue / 4];
   const int b1 = blockIdx.x + 1;
   const int32_t t = first_tile(c.n_tiles, blocks, b1);
   const Segment s = segment_at<N>(P, t, t + 1);
   const int32_t t_job = t - s.t0;  // the job's first tile
   if (s.t0 == 0 || first_tile(c.n_tiles, blocks, b1 - 1) > t_job) return;
-  const int col = blockIdx.y;
-  if (col >= s.cols) return;
   const int b0 = b1 - 1;
-  int b2 = b1 + 1;  // past the last block with tiles of the job
-  while (b2 < blocks && first_tile(c.n_tiles, blocks, b2) < t_job + s.tiles) ++b2;
-  const int n = b2 - b0;
+  // the block that holds the job's last tile: the largest b with
+  // first_tile(b) <= last
+  const int64_t last = (int64_t)t_job + s.tiles - 1;
+  const int n = (int)(((last + 1) * blocks - 1) / c.n_tiles) - b0 + 1;
+  const int tid = threadIdx.x, lane = tid & 31, group = tid >> 7, g_tid = tid & 127;
+  const int col = share ? (int)blockIdx.y : (int)blockIdx.y * kMergeGroups + group;
+  const bool on = col < s.cols;
   const size_t stride = (size_t)N * (c.dv + 2);
   auto part = [&](int i) { return parts + (size_t)(2 * (b0 + i) + (i == 0)) * stride; };
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < 32) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (on && g_tid < 32) {
+    const float* ml = parts + (size_t)N * c.dv + col;
     float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[(size_t)N * c.dv + col]);
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, (part(i) - parts + ml)[0]);
     for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
     const float base = m == -INFINITY ? 0.f : m;
     float z = 0.f;
     for (int i = lane; i < n; i += 32) {
-      const float* p = part(i) + (size_t)N * c.dv;
-      const float w = exp2f(p[col] - base);
-      weight[i] = w;
-      z += w * p[N + col];
+      const float* p = part(i) - parts + ml;
+      const float w = exp2f(p[0] - base);
+      weight[group][i] = w;
+      z += w * p[N];
     }
     for (int w = 16; w; w >>= 1) z += __shfl_xor_sync(~0u, z, w);
     if (lane == 0) {
-      total = z;
+      total[group] = z;
       const AttendItem& it = *s.it;
-      if (it.lse) {
+      if (it.lse && (!share || group == 0)) {
         const int qc = s.col0 + col;
         const int qi = it.loc ? s.qbase : qc / c.group;
         const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
@@ -1016,21 +1022,57 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
   }
   __syncthreads();
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool mine = on && g_tid * 4 < c.dv;
+  if (mine) {
+    // a part without weight may hold sums that are not finite
+    auto add = [&](float w, const float4& y) {
+      if (w != 0.f) {
+        x.x += w * y.x;
+        x.y += w * y.y;
+        x.z += w * y.z;
+        x.w += w * y.w;
+      }
+    };
+    const int step = share ? kMergeGroups : 1;
+    const size_t at = (size_t)col * c.dv + g_tid * 4;
+    int i = share ? group : 0;
+    for (; i + 7 * step < n; i += 8 * step) {
+      float4 y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = *reinterpret_cast<const float4*>(part(i + k * step) + at);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add(weight[group][i + k * step], y[k]);
+    }
+    for (; i < n; i += step) add(weight[group][i], *reinterpret_cast<const float4*>(part(i) + at));
+  }
+  if (share) {
+    if (mine) sums[group][g_tid] = x;
+    __syncthreads();
+    if (group) return;
+    if (mine)
+      for (int k = 1; k < kMergeGroups; ++k) {
+        const float4 y = sums[k][g_tid];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+  }
+  if (!mine) return;
   const AttendItem& it = *s.it;
   const int qc = s.col0 + col;
   const int qi = it.loc ? s.qbase : qc / c.group;
   const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
-  uint8_t* out = it.out + qi * c.o_qs + h * c.o_hs;
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  for (int d = tid; d < c.dv; d += kMergeThreads) {
-    float x = 0.f;
-    for (int i = 0; i < n; ++i) {
-      // a part without weight may hold sums that were never written
-      if (weight[i] != 0.f) x += weight[i] * part(i)[(size_t)col * c.dv + d];
-    }
-    x = inv == 0.f ? 0.f : x * inv;
-    if (c.f16) *reinterpret_cast<__half*>(out + 2 * d) = __float2half_rn(x);
-    else *reinterpret_cast<__nv_bfloat16*>(out + 2 * d) = __float2bfloat16_rn(x);
+  uint8_t* out = it.out + qi * c.o_qs + h * c.o_hs + 8 * g_tid;
+  const float z = total[group];
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float v = inv == 0.f ? 0.f : y[k] * inv;
+    if (c.f16) reinterpret_cast<__half*>(out)[k] = __float2half_rn(v);
+    else reinterpret_cast<__nv_bfloat16*>(out)[k] = __float2bfloat16_rn(v);
   }
 }
 
@@ -1091,6 +1133,7 @@ struct Shape {
   int64_t tiles;
   int blocks;
   bool split;       // some job is cut by a block's boundary
+  int parts;        // of the longest job, at most
 };
 
 int columns_of(const AttendCommon& c, const AttendItem& it, int most) {
@@ -1104,6 +1147,7 @@ Shape shape_of(const AttendCommon& c, AttendItem* items, int n_items, int sms) {
   Shape s{};
   const int most = widest_block(c);
   int widest = 1;
+  int64_t n_jobs = 0, longest = 0, shortest = INT64_MAX;
   for (int i = 0; i < n_items; ++i) widest = std::max(widest, columns_of(c, items[i], most));
   s.n = (widest + 15) / 16 * 16;
   const int kv = c.heads / c.group;
@@ -1115,8 +1159,19 @@ Shape shape_of(const AttendCommon& c, AttendItem* items, int n_items, int sms) {
     const int64_t all = it.loc ? c.group : (int64_t)it.Q * c.group;
     const int64_t jobs = (it.loc ? it.Q : 1) * (int64_t)kv * ((all + s.n - 1) / s.n);
     s.tiles += jobs * it.tiles;
+    n_jobs += jobs;
+    longest = std::max<int64_t>(longest, it.tiles);
+    shortest = std::min<int64_t>(shortest, it.tiles);
   }
-  s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kAttendMaxBlocks), s.tiles));
+  sms = std::min(sms, kAttendMaxBlocks);
+  s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(sms, s.tiles));
+  // Whole jobs per block where that makes no block's share longer: nothing to
+  // join then.
+  const int64_t each = (n_jobs + sms - 1) / sms;
+  if (longest == shortest && n_jobs % each == 0 &&
+      each * longest <= (s.tiles + s.blocks - 1) / s.blocks)
+    s.blocks = (int)(n_jobs / each);
+  s.parts = (int)std::min<int64_t>(s.blocks, longest * s.blocks / s.tiles + 2);
   if (s.tiles <= INT32_MAX) {
     int k = 0;
     for (int b = 1; b < s.blocks && !s.split; ++b) {
@@ -1134,7 +1189,10 @@ cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, 
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !s.split) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(s.blocks - 1, N);
+  // groups share a column's parts where those are many: 8 loads in flight a
+  // thread are then enough for each
+  const int share = s.parts > 8;
+  cfg.gridDim = dim3(s.blocks - 1, share ? N : N / kMergeGroups);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -1142,7 +1200,7 @@ cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<N, MAXI>, P, (const float*)parts, s.blocks);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<N, MAXI>, P, (const float*)parts, s.blocks, share);
 }
 
 template <int MAXI>

@@ -26,7 +26,6 @@
 #include <cstring>
 #include <functional>
 #include <new>
-#include <set>
 #include <vector>
 
 #include "dhs.h"
@@ -186,7 +185,13 @@ struct dhs_pool {
   int fresh_list = -1;          // DHS_OPT_FRESH_LIST: -1 auto, 0 off, 1 on
   int64_t complete_pages = 0;   // complete imported pages of admitted pairs
   uint64_t bseq = 0;            // pages put in backup order so far
-  std::set<std::pair<uint64_t, int64_t>> backup_order;  // (order, pair * pmax + page)
+  // Pages whose host backup is deferred, in order: (order, pair * pmax + page).
+  // An entry counts while its page's PairState::backup holds its order; the
+  // others are skipped, and swept out once they outnumber the live ones
+  // (a fork queues and a release drops thousands of pages at a time).
+  std::vector<std::pair<uint64_t, int64_t>> backup_queue;
+  size_t backup_head = 0;       // entries before it are done with
+  int64_t backup_live = 0;
   int32_t rr = 0;               // refill cursor: the next request visited
   int sm_count = 0;
   int smem_optin = 0;           // opt-in shared memory per block
@@ -484,6 +489,37 @@ int flush(dhs_pool* p) {
   return DHS_OK;
 }
 
+bool backup_waits(const dhs_pool* p, const std::pair<uint64_t, int64_t>& e) {
+  const std::vector<uint64_t>& b = p->ps[e.second / p->pmax].backup;
+  return !b.empty() && b[e.second % p->pmax] == e.first;
+}
+
+// Make room for n more entries (may throw; queue_backup then does not).
+void reserve_backup(dhs_pool* p, size_t n) {
+  auto& q = p->backup_queue;
+  if (q.size() + n > q.capacity() || q.size() > 2 * (size_t)p->backup_live + 4096) {
+    size_t to = 0;
+    for (size_t i = p->backup_head; i < q.size(); ++i)
+      if (backup_waits(p, q[i])) q[to++] = q[i];
+    q.resize(to);
+    p->backup_head = 0;
+    if (q.size() + n > q.capacity()) q.reserve(std::max(2 * q.capacity(), q.size() + n));
+  }
+}
+
+// Defer the host backup of page `q` of `pair` (PairState::backup is sized).
+void queue_backup(dhs_pool* p, int64_t pair, int64_t q) {
+  p->backup_queue.push_back({++p->bseq, pair * p->pmax + q});
+  p->ps[pair].backup[q] = p->bseq;
+  ++p->backup_live;
+}
+
+// The page is backed up, or needs no backup any more.
+void unqueue_backup(dhs_pool* p, int64_t pair, int64_t q) {
+  p->ps[pair].backup[q] = 0;
+  --p->backup_live;
+}
+
 void free_slot(dhs_pool* p, int64_t slot) {
   p->slot_pair[slot] = -1;
   p->slot_page[slot] = -1;
@@ -515,8 +551,7 @@ int backup_page(dhs_pool* p, int64_t pair, int64_t q) {
                              cudaMemcpyDeviceToHost, p->stream) != cudaSuccess) {
     return DHS_ECUDA;
   }
-  p->backup_order.erase({s.backup[q], pair * p->pmax + q});
-  s.backup[q] = 0;
+  unqueue_backup(p, pair, q);
   return DHS_OK;
 }
 
@@ -545,8 +580,7 @@ int64_t drop_pages(dhs_pool* p, int64_t pair, bool backup) {
         const int rc = backup_page(p, pair, q);
         if (rc) return rc;
       } else {
-        p->backup_order.erase({s.backup[q], pair * p->pmax + q});
-        s.backup[q] = 0;
+        unqueue_backup(p, pair, q);
       }
     }
     free_slot(p, pm[q]);
@@ -920,6 +954,7 @@ int dhs_admit_device(dhs_pool* p, int32_t req, int32_t src, const void* dev_rows
     row += run;
   }
   int32_t* pm = p->map_host.data() + pair * p->pmax;
+  reserve_backup(p, (size_t)want);
   s.backup.assign((size_t)p->pmax, 0);
   for (int64_t q = 0; q < complete; ++q) {
     if (mask && !mask[q]) continue;
@@ -928,8 +963,7 @@ int dhs_admit_device(dhs_pool* p, int32_t req, int32_t src, const void* dev_rows
     p->slot_page[slot] = (int32_t)q;
     p->used += 1;
     pm[q] = (int32_t)slot;
-    s.backup[q] = ++p->bseq;
-    p->backup_order.insert({s.backup[q], pair * p->pmax + q});
+    queue_backup(p, pair, q);
   }
   // resident pages: device to device, runs of consecutive pages and slots;
   // every other imported row: device to host now, runs of consecutive rows
@@ -969,8 +1003,10 @@ int dhs_backup(dhs_pool* p, int64_t max_pages, int64_t* done) {
   if (rc) return rc;
   p->moves.clear();
   int64_t n = 0;
-  while (n < max_pages && !p->backup_order.empty()) {
-    const int64_t key = p->backup_order.begin()->second;
+  while (n < max_pages && p->backup_live > 0) {
+    const std::pair<uint64_t, int64_t> e = p->backup_queue[p->backup_head++];
+    if (!backup_waits(p, e)) continue;
+    const int64_t key = e.second;
     if ((rc = backup_page(p, key / p->pmax, key % p->pmax))) return rc;
     ++n;
   }
@@ -1011,7 +1047,7 @@ int dhs_admit_window(dhs_pool* p, int32_t req, int32_t src, const void* dev_rows
 }
 
 int64_t dhs_pending_backup(const dhs_pool* p) {
-  return p ? (int64_t)p->backup_order.size() : -1;
+  return p ? p->backup_live : -1;
 }
 
 int dhs_refill(dhs_pool* p, int64_t max_pages, int64_t* filled) {
@@ -1973,6 +2009,7 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
       if (deficit) *deficit = p->used + want - usable;
       return DHS_EWOULDWAIT;
     }
+    reserve_backup(p, (size_t)want);
     for (const dhs::ForkSource& k : src) {
       const int32_t s = (int32_t)(k.to - to0);
       const PairState& f = p->ps[k.from];
@@ -1991,8 +2028,7 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
       mark_dirty(p, k.to);
       for (int64_t q = 0; q < k.complete; ++q) {
         if (mask ? !mask[q] : pm[q] < 0) continue;
-        p->backup_order.insert({++p->bseq, (int64_t)k.to * p->pmax + q});
-        t.backup[q] = p->bseq;
+        queue_backup(p, k.to, q);
         const int64_t slot = lowest_free_slot(p);
         p->slot_pair[slot] = k.to;
         p->slot_page[slot] = (int32_t)q;
