@@ -964,108 +964,101 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ merge
 
-constexpr int kMergeThreads = 512, kMergeGroups = 4;  // groups of 128 threads
+constexpr int kMergeWarps = 16;
+constexpr int kMergeElems = 128;  // value elements of a warp: a float4 a lane
 
-// Joins the parts of the jobs that a block's boundary cuts, in block order.
-// Block (x, y): the job that boundary x + 1 is the first to cut, if any.  A
-// few parts: each group of threads takes a column of its own.  Many: the
-// groups share one column's parts.  (152 parts of 16 columns, 5 MB: see the
-// design notes for the time beside the attention's.)
+struct MergeParams {
+  int32_t blocks;     // of the attention's grid
+  int32_t groups;     // warps that share one column's parts: 1, 4 or 16
+  uint8_t cut[kAttendMaxBlocks];  // per split job: the first block that begins inside it
+};
+
+// Joins the parts of the split jobs in block order.  A warp has 128 value
+// elements of one column and every `groups`-th part; the groups' sums meet in
+// shared memory.
 template <int N, int MAXI>
-__global__ void __launch_bounds__(kMergeThreads)
-    merge_kernel(const __grid_constant__ AttendParams<MAXI> P, const float* parts, int blocks,
-                 int share) {
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    merge_kernel(const __grid_constant__ AttendParams<MAXI> P, const __grid_constant__ MergeParams M,
+                 const float* parts) {
   const AttendCommon& c = P.c;
-  __shared__ float weight[kMergeGroups][kAttendMaxBlocks];
-  __shared__ float total[kMergeGroups];
-  __shared__ float4 sums[kMergeGroups][kAttendMaxValue / 4];
-  const int b1 = blockIdx.x + 1;
-  const int32_t t = first_tile(c.n_tiles, blocks, b1);
+  __shared__ float weight[kMergeWarps][kAttendMaxBlocks];
+  __shared__ float4 sums[kMergeWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b0 = M.cut[blockIdx.x] - 1;
+  const int32_t t = first_tile(c.n_tiles, M.blocks, b0 + 1);
   const Segment s = segment_at<N>(P, t, t + 1);
-  const int32_t t_job = t - s.t0;  // the job's first tile
-  if (s.t0 == 0 || first_tile(c.n_tiles, blocks, b1 - 1) > t_job) return;
-  const int b0 = b1 - 1;
   // the block that holds the job's last tile: the largest b with
   // first_tile(b) <= last
-  const int64_t last = (int64_t)t_job + s.tiles - 1;
-  const int n = (int)(((last + 1) * blocks - 1) / c.n_tiles) - b0 + 1;
-  const int tid = threadIdx.x, lane = tid & 31, group = tid >> 7, g_tid = tid & 127;
-  const int col = share ? (int)blockIdx.y : (int)blockIdx.y * kMergeGroups + group;
+  const int64_t last = (int64_t)(t - s.t0) + s.tiles - 1;
+  const int n = (int)(((last + 1) * M.blocks - 1) / c.n_tiles) - b0 + 1;
+  const int spans = (c.dv + kMergeElems - 1) / kMergeElems;
+  const int pair = blockIdx.y * (kMergeWarps / M.groups) + warp / M.groups;
+  const int col = pair / spans, d = pair % spans * kMergeElems + lane * 4;
+  const int group = warp % M.groups;
   const bool on = col < s.cols;
   const size_t stride = (size_t)N * (c.dv + 2);
   auto part = [&](int i) { return parts + (size_t)(2 * (b0 + i) + (i == 0)) * stride; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (on && g_tid < 32) {
-    const float* ml = parts + (size_t)N * c.dv + col;
+  const AttendItem& it = *s.it;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float base = 0.f, z = 0.f;
+  if (on) {
+    const size_t ml = (size_t)N * c.dv + col;
     float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, (part(i) - parts + ml)[0]);
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ml]);
     for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
-    const float base = m == -INFINITY ? 0.f : m;
-    float z = 0.f;
+    base = m == -INFINITY ? 0.f : m;
     for (int i = lane; i < n; i += 32) {
-      const float* p = part(i) - parts + ml;
-      const float w = exp2f(p[0] - base);
-      weight[group][i] = w;
-      z += w * p[N];
+      const float w = exp2f(part(i)[ml] - base);
+      weight[warp][i] = w;
+      z += w * part(i)[ml + N];
     }
     for (int w = 16; w; w >>= 1) z += __shfl_xor_sync(~0u, z, w);
-    if (lane == 0) {
-      total[group] = z;
-      const AttendItem& it = *s.it;
-      if (it.lse && (!share || group == 0)) {
-        const int qc = s.col0 + col;
-        const int qi = it.loc ? s.qbase : qc / c.group;
-        const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
-        it.lse[(size_t)qi * c.heads + h] =
-            z == 0.f ? -INFINITY : (base + log2f(z)) * 0.693147180559945309f;
+    __syncwarp();
+    if (d < c.dv) {
+      const size_t at = (size_t)col * c.dv + d;
+      auto add = [&](float w, const float4& y) {
+        if (w != 0.f) {  // a part without weight may hold sums that are not finite
+          x.x += w * y.x;
+          x.y += w * y.y;
+          x.z += w * y.z;
+          x.w += w * y.w;
+        }
+      };
+      int i = group;
+      for (; i + 3 * M.groups < n; i += 4 * M.groups) {
+        float4 y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          y[k] = *reinterpret_cast<const float4*>(part(i + k * M.groups) + at);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) add(weight[warp][i + k * M.groups], y[k]);
       }
+      for (; i < n; i += M.groups)
+        add(weight[warp][i], *reinterpret_cast<const float4*>(part(i) + at));
     }
   }
-  __syncthreads();
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  const bool mine = on && g_tid * 4 < c.dv;
-  if (mine) {
-    // a part without weight may hold sums that are not finite
-    auto add = [&](float w, const float4& y) {
-      if (w != 0.f) {
-        x.x += w * y.x;
-        x.y += w * y.y;
-        x.z += w * y.z;
-        x.w += w * y.w;
-      }
-    };
-    const int step = share ? kMergeGroups : 1;
-    const size_t at = (size_t)col * c.dv + g_tid * 4;
-    int i = share ? group : 0;
-    for (; i + 7 * step < n; i += 8 * step) {
-      float4 y[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = *reinterpret_cast<const float4*>(part(i + k * step) + at);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) add(weight[group][i + k * step], y[k]);
-    }
-    for (; i < n; i += step) add(weight[group][i], *reinterpret_cast<const float4*>(part(i) + at));
-  }
-  if (share) {
-    if (mine) sums[group][g_tid] = x;
+  if (M.groups > 1) {
+    sums[warp][lane] = x;
     __syncthreads();
     if (group) return;
-    if (mine)
-      for (int k = 1; k < kMergeGroups; ++k) {
-        const float4 y = sums[k][g_tid];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-      }
+    for (int k = 1; k < M.groups; ++k) {
+      const float4 y = sums[warp + k][lane];
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+    }
   }
-  if (!mine) return;
-  const AttendItem& it = *s.it;
+  if (!on) return;
   const int qc = s.col0 + col;
   const int qi = it.loc ? s.qbase : qc / c.group;
   const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
-  uint8_t* out = it.out + qi * c.o_qs + h * c.o_hs + 8 * g_tid;
-  const float z = total[group];
+  if (it.lse && lane == 0 && d == 0)
+    it.lse[(size_t)qi * c.heads + h] =
+        z == 0.f ? -INFINITY : (base + log2f(z)) * 0.693147180559945309f;
+  if (d >= c.dv) return;
+  uint8_t* out = it.out + qi * c.o_qs + h * c.o_hs + 2 * d;
   const float inv = z == 0.f ? 0.f : 1.f / z;
   const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -1132,8 +1125,9 @@ struct Shape {
   int n;            // columns of a block
   int64_t tiles;
   int blocks;
-  bool split;       // some job is cut by a block's boundary
-  int parts;        // of the longest job, at most
+  int n_cut;        // jobs cut by a block's boundary
+  int parts;        // of the longest job, about
+  MergeParams merge;
 };
 
 int columns_of(const AttendCommon& c, const AttendItem& it, int most) {
@@ -1172,12 +1166,18 @@ Shape shape_of(const AttendCommon& c, AttendItem* items, int n_items, int sms) {
       each * longest <= (s.tiles + s.blocks - 1) / s.blocks)
     s.blocks = (int)(n_jobs / each);
   s.parts = (int)std::min<int64_t>(s.blocks, longest * s.blocks / s.tiles + 2);
+  s.merge.blocks = s.blocks;
+  s.merge.groups = s.parts > 24 ? 16 : s.parts > 4 ? 4 : 1;
   if (s.tiles <= INT32_MAX) {
     int k = 0;
-    for (int b = 1; b < s.blocks && !s.split; ++b) {
+    int64_t cut_job = -1;  // first tile of the job cut last
+    for (int b = 1; b < s.blocks; ++b) {
       const int32_t t = first_tile(s.tiles, s.blocks, b);
       while (k + 1 < n_items && items[k + 1].tile0 <= t) ++k;
-      s.split = (t - items[k].tile0) % items[k].tiles != 0;
+      const int32_t in = (t - items[k].tile0) % items[k].tiles;
+      if (in == 0 || t - in == cut_job) continue;
+      cut_job = t - in;
+      s.merge.cut[s.n_cut++] = (uint8_t)b;
     }
   }
   return s;
@@ -1187,20 +1187,19 @@ template <int N, int MAXI>
 cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
   attend_kernel<N, MAXI><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !s.split) return e;
+  if (e != cudaSuccess || !s.n_cut) return e;
   cudaLaunchConfig_t cfg{};
-  // groups share a column's parts where those are many: 8 loads in flight a
-  // thread are then enough for each
-  const int share = s.parts > 8;
-  cfg.gridDim = dim3(s.blocks - 1, share ? N : N / kMergeGroups);
-  cfg.blockDim = dim3(kMergeThreads);
+  const int per = kMergeWarps / s.merge.groups;
+  const int pairs = N * ((P.c.dv + kMergeElems - 1) / kMergeElems);
+  cfg.gridDim = dim3(s.n_cut, (pairs + per - 1) / per);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<N, MAXI>, P, (const float*)parts, s.blocks, share);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<N, MAXI>, P, s.merge, (const float*)parts);
 }
 
 template <int MAXI>
@@ -1239,7 +1238,7 @@ cudaError_t attend_set_smem_limit() {
 
 bool attend_shape(const AttendCommon& c, AttendItem* items, int n_items, int sms, size_t* bytes) {
   const Shape s = shape_of(c, items, n_items, sms);
-  *bytes = s.split ? (size_t)2 * s.blocks * s.n * (c.dv + 2) * sizeof(float) : 0;
+  *bytes = s.n_cut ? (size_t)2 * s.blocks * s.n * (c.dv + 2) * sizeof(float) : 0;
   return s.tiles <= INT32_MAX;
 }
 
