@@ -425,36 +425,45 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     t += s.t1 - s.t0;
     if (s.v0 >= s.v1) continue;
     const AttendItem& it = *s.it;
-    // queries: [chunk][column][128 B], zeros past the key and the columns
-    if (!first) {
-      warp_wait(smem_u32(&ctl.qempty), qphase, &ctl.gave_up);
-      qphase ^= 1;
-    }
-    first = false;
-    const bool aligned = !(((uintptr_t)it.q | c.q_qs | c.q_hs) & 15);
-    for (int e = tid; e < pl.key_chunks * N * 8; e += kLoadThreads) {
-      const int ch = e / (N * 8), col = e / 8 % N, pc = e & 7;
-      const int el = ch * 64 + pc * 8;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (el < c.dk && col < s.cols) {
-        const int qc = s.col0 + col;
+    // Queries: [chunk][column][128 B], zeros past the key and the columns.
+    // Loaded behind the first tile's key chunks: the segment before may still
+    // hold the buffer, and does so about as long as the slots of its rows.
+    auto load_queries = [&] {
+      if (!first) {
+        warp_wait(smem_u32(&ctl.qempty), qphase, &ctl.gave_up);
+        qphase ^= 1;
+      }
+      first = false;
+      const bool aligned = !(((uintptr_t)it.q | c.q_qs | c.q_hs) & 15);
+      for (int col = tid >> 3; col < N; col += kLoadThreads / 8) {
+        const bool on = col < s.cols;
+        const int qc = s.col0 + min(col, s.cols - 1);
         const int qi = it.loc ? s.qbase : qc / c.group;
         const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
-        const uint8_t* src = it.q + qi * c.q_qs + h * c.q_hs + 2 * el;
-        if (aligned) {
-          v = __ldg(reinterpret_cast<const uint4*>(src));
-        } else {
-          const uint16_t* s2 = reinterpret_cast<const uint16_t*>(src);
-          uint32_t w[4];
+        const uint8_t* src = it.q + qi * c.q_qs + h * c.q_hs;
+        const uint32_t dst = pl.off_q + col * 128 + ((piece ^ (col & 7)) << 4);
+        for (int ch = 0; ch < pl.key_chunks; ++ch) {
+          const int el = ch * 64 + piece * 8;
+          const bool in = on && el < c.dk;
+          if (aligned) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             base + dst + ch * (N * 128)),
+                         "l"(in ? src + 2 * el : c.tail), "r"(in ? 16 : 0)
+                         : "memory");
+          } else {
+            const uint16_t* s2 = reinterpret_cast<const uint16_t*>(src + 2 * el);
+            uint32_t w[4] = {};
+            if (in)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = s2[2 * k] | (uint32_t)s2[2 * k + 1] << 16;
-          v = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 4; ++k) w[k] = s2[2 * k] | (uint32_t)s2[2 * k + 1] << 16;
+            *reinterpret_cast<uint4*>(sm + dst + ch * (N * 128)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
       }
-      *reinterpret_cast<uint4*>(sm + pl.off_q + (ch * N + col) * 128 + ((pc ^ (col & 7)) << 4)) = v;
-    }
-    fence_async();
-    bar_arrive(smem_u32(&ctl.qfull));
+      if (aligned) launch(smem_u32(&ctl.qfull));
+      else bar_arrive(smem_u32(&ctl.qfull));
+    };
 
     const uint32_t key_at = c.key_off + s.g * c.key_stride;
     const uint32_t val_at = c.val_off + s.g * c.val_stride;
@@ -488,11 +497,14 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
       };
       const int c0 = pl.key_chunks - pl.only_chunks;
       for (int k = 0; k < pl.only_chunks; ++k) {
+        // a slot that this tile itself has to free needs the queries
+        if (tile == s.v0 && k == pl.kslots) load_queries();
         wait_empty(smem_u32(&ctl.kempty[kr.slot]), kr.phase ^ 1);
         chunk(base + pl.off_k + kr.slot * kChunk, key_at, (c0 + k) * 64, c.dk);
         launch(smem_u32(&ctl.kfull[kr.slot]));
         kr.next(pl.kslots);
       }
+      if (tile == s.v0 && pl.only_chunks <= pl.kslots) load_queries();
       const int n = pl.shared ? c.dk : c.dv;
       for (int u = 0; u < pl.units; ++u) {
         wait_empty(smem_u32(&ctl.vempty[vr.slot]), vr.phase ^ 1);
@@ -546,6 +558,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
     t += s.t1 - s.t0;
     if (s.v0 >= s.v1) continue;
     warp_wait(smem_u32(&ctl.qfull), qphase, &ctl.gave_up);
+    fence_async();
     qphase ^= 1;
     for (int tile = s.v0; tile < s.v1; ++tile) {
       const int kslot = kr.slot;
