@@ -44,7 +44,9 @@ constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk
 constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
 constexpr float kSlack = 8.f;              // log2 units
-constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
+// A wait sleeps up to kWaitNs at a time (polling would take shared-memory
+// cycles from the copies) and gives up after kWaitPolls times.
+constexpr uint32_t kWaitNs = 20000, kWaitPolls = 1u << 17;
 
 // How a launch's row slices are staged.
 struct Plan {
@@ -84,10 +86,10 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kWaitNs)
       : "memory");
   return ok != 0;
 }
@@ -98,7 +100,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
   for (uint32_t n = 0; n < kWaitPolls; ++n) {
     if (bar_try(bar, parity)) return;
-    if ((n & 255) == 255 && *gave_up) return;
+    if ((n & 15) == 15 && *gave_up) return;
   }
   *gave_up = 1;
 }
@@ -246,7 +248,7 @@ __device__ __forceinline__ float fold8(const float* in, int lane, F f) {
 // col0 + cols) of kv head g (column = query * group + head within the group
 // for a history; located items: query qbase, column = head).
 struct Segment {
-  const AttendItem* it;
+  AttendItem it;     // a copy: the table is indexed constant memory, slow to read
   int32_t tiles;     // of the whole job
   int32_t t0, t1;    // the segment's tiles before clipping to visible rows
   int32_t g, qbase, col0, cols;
@@ -275,8 +277,8 @@ __device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te
     else b = m;
   }
   Segment s;
-  s.it = &P.items[a];
-  const AttendItem& it = *s.it;
+  s.it = P.items[a];
+  const AttendItem& it = s.it;
   const bool located = it.loc != nullptr;
   s.tiles = it.tiles;
   int32_t job = (t - it.tile0) / it.tiles;
@@ -320,26 +322,38 @@ __host__ __device__ __forceinline__ int32_t first_tile(int64_t total, int blocks
   return (int32_t)(total * b / blocks);
 }
 
+// Finding row j of a job takes up to two dependent loads: a list position
+// (union items), then the location or (histories) the page's slot.  They are
+// split so that a loading thread can keep them in flight: `row_index` two
+// tiles ahead, `row_word` one tile ahead, `row_of` when the tile is loaded.
+__device__ __forceinline__ int32_t row_index(const Segment& s, int64_t j) {
+  const AttendItem& it = s.it;
+  if (!it.index || j < s.lo || j >= s.hi) return -1;
+  return __ldg(it.index + (int64_t)s.qbase * it.len + j);
+}
+
+__device__ __forceinline__ uint32_t row_word(const AttendCommon& c, const Segment& s, int64_t j,
+                                             int32_t index) {
+  const AttendItem& it = s.it;
+  if (j < s.lo || j >= s.hi) return kNoLoc;
+  if (it.loc) {
+    if (!it.index) return __ldg(it.loc + (int64_t)s.qbase * it.len + j);
+    if (index < 0) return kNoLoc;
+    // a position past the list: a location of no tier
+    return index < (int64_t)it.Q * it.len ? __ldg(it.loc + index) : 3u << 30;
+  }
+  const int64_t page = (it.first + j) >> c.page_shift;
+  return page < it.complete ? (uint32_t)__ldg(c.map + (size_t)it.pair * c.Pmax + page) : kNoLoc;
+}
+
 // Address of row j of the job, or null when there is none.
-__device__ __forceinline__ const uint8_t* row_of(const AttendCommon& c, const Segment& s, int64_t j) {
-  const AttendItem& it = *s.it;
+__device__ __forceinline__ const uint8_t* row_of(const AttendCommon& c, const Segment& s, int64_t j,
+                                                 uint32_t word) {
+  const AttendItem& it = s.it;
   if (j < s.lo || j >= s.hi) return nullptr;
   if (it.loc) {
-    const int64_t e = (int64_t)s.qbase * it.len + j;
-    uint32_t loc;
-    if (it.index) {
-      const int32_t u = it.index[e];
-      if (u < 0) return nullptr;
-      if (u >= (int64_t)it.Q * it.len) {
-        atomicOr(c.status, kStatusEloc);
-        return nullptr;
-      }
-      loc = it.loc[u];
-    } else {
-      loc = it.loc[e];
-    }
-    if (loc >= kEndLoc) return nullptr;
-    const uint32_t tier = loc >> 30, x = loc & 0x3FFFFFFFu;
+    if (word >= kEndLoc) return nullptr;
+    const uint32_t tier = word >> 30, x = word & 0x3FFFFFFFu;
     const uint32_t rows = tier == kTierTail ? c.tail_rows : tier == kTierOpt ? c.opt_rows
                           : tier == kTierHot ? c.hot_rows : 0;
     if (x >= rows) {
@@ -349,14 +363,11 @@ __device__ __forceinline__ const uint8_t* row_of(const AttendCommon& c, const Se
     const uint8_t* base = tier == kTierTail ? c.tail : tier == kTierOpt ? c.opt : c.hot;
     return base + (size_t)x * c.row_bytes;
   }
-  const int64_t r = it.first + j, L = it.first + it.len;
-  if (r >= L - c.T) return c.tail + ((size_t)it.pair * c.T + (size_t)(r % c.T)) * c.row_bytes;
-  const int64_t page = r >> c.page_shift;
-  if (page < it.complete) {
-    const int32_t slot = c.map[(size_t)it.pair * c.Pmax + page];
-    if (slot >= 0)
-      return c.opt + (((size_t)slot << c.page_shift) + (r & ((1 << c.page_shift) - 1))) * c.row_bytes;
-  }
+  const int64_t r = it.first + j;
+  if (r >= it.first + it.len - c.T)
+    return c.tail + ((size_t)it.pair * c.T + (uint32_t)r % (uint32_t)c.T) * c.row_bytes;
+  if ((int32_t)word >= 0)
+    return c.opt + (((size_t)word << c.page_shift) + (r & ((1 << c.page_shift) - 1))) * c.row_bytes;
   return it.host + (size_t)r * c.row_bytes;
 }
 
@@ -424,7 +435,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     const Segment s = segment_at<N>(P, t, te);
     t += s.t1 - s.t0;
     if (s.v0 >= s.v1) continue;
-    const AttendItem& it = *s.it;
+    const AttendItem& it = s.it;
     // Queries: [chunk][column][128 B], zeros past the key and the columns.
     // Loaded behind the first tile's key chunks: the segment before may still
     // hold the buffer, and does so about as long as the slots of its rows.
@@ -468,18 +479,22 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     const uint32_t key_at = c.key_off + s.g * c.key_stride;
     const uint32_t val_at = c.val_off + s.g * c.val_stride;
     static_assert(kLoadThreads == kTile, "one row address per loading thread");
-    const uint8_t* ahead = row_of(c, s, (int64_t)s.v0 * kTile + tid);
+    int64_t j = (int64_t)s.v0 * kTile + tid;  // this thread's row of the tile
+    uint32_t word = row_word(c, s, j, row_index(s, j));
+    int32_t index = row_index(s, j + kTile);
     for (int tile = s.v0; tile < s.v1; ++tile) {
       // the tile's row addresses, to every loading thread and the softmax
       wait_empty(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1);
-      ctl.row[rr.slot][tid] = ahead;
+      ctl.row[rr.slot][tid] = row_of(c, s, j, word);
+      j += kTile;
+      word = row_word(c, s, j, index);
+      index = row_index(s, j + kTile);
       bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
       named_sync(2, kLoadThreads);
       const uint8_t* row[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = ctl.row[rr.slot][r0 + 16 * i];
       rr.next(2);
-      if (tile + 1 < s.v1) ahead = row_of(c, s, (int64_t)(tile + 1) * kTile + tid);
       // one 64-element chunk of the 128 rows: element el.. of a slice of
       // `n` elements at byte `at` of each row
       auto chunk = [&](uint32_t dst, uint32_t at, int el, int n) {
@@ -495,24 +510,28 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
                        : "memory");
         }
       };
-      const int c0 = pl.key_chunks - pl.only_chunks;
-      for (int k = 0; k < pl.only_chunks; ++k) {
+      // Key chunks, then value units; where the weights take the key chunk's
+      // slot, which is then free last, the units first.
+      const int c0 = pl.key_chunks - pl.only_chunks, items = pl.only_chunks + pl.units;
+#pragma unroll 1
+      for (int i = 0; i < items; ++i) {
+        const bool key = pl.alias ? i >= pl.units : i < pl.only_chunks;
         // a slot that this tile itself has to free needs the queries
-        if (tile == s.v0 && k == pl.kslots) load_queries();
-        wait_empty(smem_u32(&ctl.kempty[kr.slot]), kr.phase ^ 1);
-        chunk(base + pl.off_k + kr.slot * kChunk, key_at, (c0 + k) * 64, c.dk);
-        launch(smem_u32(&ctl.kfull[kr.slot]));
-        kr.next(pl.kslots);
-      }
-      if (tile == s.v0 && pl.only_chunks <= pl.kslots) load_queries();
-      const int n = pl.shared ? c.dk : c.dv;
-      for (int u = 0; u < pl.units; ++u) {
-        wait_empty(smem_u32(&ctl.vempty[vr.slot]), vr.phase ^ 1);
-        const uint32_t dst = base + pl.off_v + vr.slot * kUnit;
-        chunk(dst, pl.shared ? key_at : val_at, u * 128, n);
-        if (u * 128 + 64 < n) chunk(dst + kChunk, pl.shared ? key_at : val_at, u * 128 + 64, n);
-        launch(smem_u32(&ctl.vfull[vr.slot]));
-        vr.next(pl.vslots);
+        if (tile == s.v0 && i == (pl.alias ? 0 : min(pl.kslots, pl.only_chunks))) load_queries();
+        if (key) {
+          wait_empty(smem_u32(&ctl.kempty[kr.slot]), kr.phase ^ 1);
+          chunk(base + pl.off_k + kr.slot * kChunk, key_at, (c0 + (pl.alias ? 0 : i)) * 64, c.dk);
+          launch(smem_u32(&ctl.kfull[kr.slot]));
+          kr.next(pl.kslots);
+        } else {
+          const int el = (pl.alias ? i : i - pl.only_chunks) * 128, n = pl.shared ? c.dk : c.dv;
+          const uint32_t at = pl.shared ? key_at : val_at, dst = base + pl.off_v + vr.slot * kUnit;
+          wait_empty(smem_u32(&ctl.vempty[vr.slot]), vr.phase ^ 1);
+          chunk(dst, at, el, n);
+          if (el + 64 < n) chunk(dst + kChunk, at, el + 64, n);
+          launch(smem_u32(&ctl.vfull[vr.slot]));
+          vr.next(pl.vslots);
+        }
       }
     }
   }
@@ -562,14 +581,17 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
     qphase ^= 1;
     for (int tile = s.v0; tile < s.v1; ++tile) {
       const int kslot = kr.slot;
-      for (int k = 0; k < pl.only_chunks; ++k) {
-        warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
-        fence_async();
-        tc_after();
-        scores(k_lo + kr.slot * (kChunk >> 4), c0 + k, k > 0);
-        if (lead && !pl.alias) commit(smem_u32(&ctl.kempty[kr.slot]));
-        kr.next(pl.kslots);
-      }
+      auto keys = [&](bool add) {
+        for (int k = 0; k < pl.only_chunks; ++k) {
+          warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
+          fence_async();
+          tc_after();
+          scores(k_lo + kr.slot * (kChunk >> 4), c0 + k, add || k > 0);
+          if (lead && !pl.alias) commit(smem_u32(&ctl.kempty[kr.slot]));
+          kr.next(pl.kslots);
+        }
+      };
+      if (!pl.alias) keys(false);
       Ring v = vr;
       if (pl.shared) {
         for (int u = 0; u < pl.units; ++u) {
@@ -577,11 +599,12 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
           fence_async();
           tc_after();
           const uint32_t at = v_lo + v.slot * (kUnit >> 4);
-          scores(at, 2 * u, pl.only_chunks > 0 || u > 0);
+          scores(at, 2 * u, (pl.only_chunks > 0 && !pl.alias) || u > 0);
           if (2 * u + 1 < pl.key_chunks) scores(at + (kChunk >> 4), 2 * u + 1, true);
           v.next(pl.vslots);
         }
       }
+      if (pl.alias) keys(true);
       if (lead) {
         commit(smem_u32(&ctl.sfull));
         if (tile + 1 == s.v1) commit(smem_u32(&ctl.qempty));
@@ -704,6 +727,33 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
   }
 }
 
+// 4 x 4 values of four neighbouring lanes transposed: lane i (mod 4) gets
+// value i of lanes 0..3.
+__device__ __forceinline__ void transpose4(float* v, int lane) {
+  const bool a = lane & 1, b = lane & 2;
+  float s0 = a ? v[0] : v[1], s1 = a ? v[2] : v[3];
+  s0 = __shfl_xor_sync(~0u, s0, 1);
+  s1 = __shfl_xor_sync(~0u, s1, 1);
+  if (a) {
+    v[0] = s0;
+    v[2] = s1;
+  } else {
+    v[1] = s0;
+    v[3] = s1;
+  }
+  s0 = b ? v[0] : v[2];
+  s1 = b ? v[1] : v[3];
+  s0 = __shfl_xor_sync(~0u, s0, 2);
+  s1 = __shfl_xor_sync(~0u, s1, 2);
+  if (b) {
+    v[0] = s0;
+    v[1] = s1;
+  } else {
+    v[2] = s0;
+    v[3] = s1;
+  }
+}
+
 // Softmax warps: a thread has one row of the tile and half of the columns;
 // then the segment's output.
 template <int N, int MAXI>
@@ -716,6 +766,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
   const uint32_t tm_s = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0, tm_o = tm_s + N;
   const float scale = c.scale * 1.44269504088896341f;  // log2 e
   uint8_t* const weights = sm + (pl.alias ? pl.off_k : pl.off_p) + r * weight_row(N);
+  const bool wide = !(((uintptr_t)c.o_qs | c.o_hs) & 7);  // outputs store four elements at once
   const int turn = weight_row(N) == 32 ? (r >> 2) & 1 : weight_row(N) == 64 ? (r >> 1) & 3 : r & 7;
   Ring rr, vr;
   uint32_t sphase = 0, ophase = 0;
@@ -724,7 +775,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
   for (int32_t t = tb; t < te;) {
     const Segment s = segment_at<N>(P, t, te);
     t += s.t1 - s.t0;
-    const AttendItem& it = *s.it;
+    const AttendItem& it = s.it;
     named_sync(1, kSoftThreads);  // the previous segment's column tables are read
     if (tid == 0) ctl.o_begun = 0;
     if (tid < N) {
@@ -758,7 +809,8 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       const int32_t j = tile * kTile + r;
       warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, &ctl.gave_up);
       const uint8_t* row = ctl.row[rr.slot][r];
-      bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
       rr.next(2);
       const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
       warp_wait(smem_u32(&ctl.sfull), sphase, &ctl.gave_up);
@@ -857,7 +909,8 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       }
       fence_async();
       tc_before();
-      bar_arrive(smem_u32(&ctl.pfull));
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_u32(&ctl.pfull));
     }
 
     named_sync(1, kSoftThreads);
@@ -894,8 +947,10 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       ophase ^= 1;
       tc_after();
     }
+    const bool quads = wide && !((uintptr_t)it.out & 7);
     for (int u = 0; u < pl.units; ++u) {
-      const int d = u * 128 + r;
+      // after the exchange lane i of four has column k + i of four elements
+      const int d = u * 128 + quarter * 32 + (lane & ~3);
       float v[C];
       if (none) {
 #pragma unroll
@@ -904,23 +959,50 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
         tm_load(tm_o + u * N, v);
       }
 #pragma unroll
-      for (int k = 0; k < C; ++k) {
+      for (int k = 0; k < C; k += 4) {
+        transpose4(v + k, lane);
+        const int col = k0 + k + (lane & 3);
+        const float f = ctl.fac[col];
+        const bool on = d < c.dv && col < s.cols;
+        float y[4];
         // a weight sum of zero leaves products of zero: the output is zero
-        const float y = ctl.fac[k0 + k] == 0.f ? 0.f : v[k] * ctl.fac[k0 + k];
-        if (d >= c.dv || k0 + k >= s.cols) {
-        } else if (!whole) {
-          part[(size_t)(k0 + k) * c.dv + d] = y;
-        } else if (c.f16) {
-          *reinterpret_cast<__half*>(it.out + ctl.out_off[k0 + k] + 2 * d) = __float2half_rn(y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = f == 0.f ? 0.f : v[k + i] * f;
+        if (!whole) {
+          if (on)
+            *reinterpret_cast<float4*>(part + (size_t)col * c.dv + d) =
+                make_float4(y[0], y[1], y[2], y[3]);
+          continue;
+        }
+        uint32_t w[2];
+        if (c.f16) {
+          const __half2 a = __floats2half2_rn(y[0], y[1]), b = __floats2half2_rn(y[2], y[3]);
+          w[0] = *reinterpret_cast<const uint32_t*>(&a);
+          w[1] = *reinterpret_cast<const uint32_t*>(&b);
         } else {
-          *reinterpret_cast<__nv_bfloat16*>(it.out + ctl.out_off[k0 + k] + 2 * d) =
-              __float2bfloat16_rn(y);
+          const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(y[2], y[3]);
+          w[0] = *reinterpret_cast<const uint32_t*>(&a);
+          w[1] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        uint8_t* out = it.out + ctl.out_off[col] + 2 * d;
+        if (!on) {
+        } else if (quads) {
+          *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+        } else {
+          uint16_t* o = reinterpret_cast<uint16_t*>(out);
+          o[0] = (uint16_t)w[0];
+          o[1] = (uint16_t)(w[0] >> 16);
+          o[2] = (uint16_t)w[1];
+          o[3] = (uint16_t)(w[1] >> 16);
         }
       }
+      __syncwarp();
     }
     if (!none) {
       tc_before();
-      bar_arrive(smem_u32(&ctl.oempty));
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_u32(&ctl.oempty));
     }
   }
 }
@@ -941,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool soft = i == kBarPfull || i == kBarOempty || i == kBarRempty || i == kBarRempty + 1;
       const bool rows = i == kBarRfull || i == kBarRfull + 1;
       bar_init(smem_u32(&ctl.kfull[0]) + 8 * i,
-               full ? kLoadThreads : soft ? kSoftThreads : rows ? kTile : 1);
+               full ? kLoadThreads : soft ? kSoftThreads / 32 : rows ? kTile : 1);
     }
     ctl.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1012,7 +1094,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const size_t stride = (size_t)N * (c.dv + 2);
   auto part = [&](int i) { return parts + (size_t)(2 * (b0 + i) + (i == 0)) * stride; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const AttendItem& it = *s.it;
+  const AttendItem& it = s.it;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   float base = 0.f, z = 0.f;
   if (on) {
