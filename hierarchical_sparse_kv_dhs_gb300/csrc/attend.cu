@@ -318,8 +318,40 @@ __device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te
   return s;
 }
 
-__host__ __device__ __forceinline__ int32_t first_tile(int64_t total, int blocks, int b) {
-  return (int32_t)(total * b / blocks);
+// First tile of block b's share of what the waves leave.
+__host__ __device__ __forceinline__ int32_t first_tile(int64_t total, int32_t waved, int blocks,
+                                                       int b) {
+  return waved + (int32_t)((total - waved) * b / blocks);
+}
+
+// A block's segments: first a whole job of each wave (jobs of equal length go
+// to the blocks in order, so that blocks running side by side work on
+// neighbouring jobs, which read the same rows), then its even share of the
+// tiles that are left.
+struct Walk {
+  int32_t wave, t, te;
+};
+template <int MAXI>
+__device__ __forceinline__ Walk first_of(const AttendParams<MAXI>& P) {
+  const AttendCommon& c = P.c;
+  return {0, first_tile(c.n_tiles, c.waved, gridDim.x, blockIdx.x),
+          first_tile(c.n_tiles, c.waved, gridDim.x, blockIdx.x + 1)};
+}
+template <int N, int MAXI>
+__device__ bool next_segment(const AttendParams<MAXI>& P, Walk& w, Segment& s) {
+  const AttendCommon& c = P.c;
+  int32_t t = w.t, te = w.te;
+  if (w.wave < c.waves) {
+    t = (int32_t)((w.wave * gridDim.x + blockIdx.x) * c.job_tiles);
+    te = t + c.job_tiles;
+    ++w.wave;
+    s = segment_at<N>(P, t, te);
+    return true;
+  }
+  if (t >= te) return false;
+  s = segment_at<N>(P, t, te);
+  w.t += s.t1 - s.t0;
+  return true;
 }
 
 // Finding row j of a job takes up to two dependent loads: a list position
@@ -415,8 +447,7 @@ __host__ __device__ constexpr uint32_t weight_swizzle(int n) { return n <= 16 ? 
 
 // Loading warps: queries once per segment, rows tile by tile.
 template <int N, int MAXI>
-__device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid,
-                          int32_t tb, int32_t te) {
+__device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid) {
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
   const uint32_t base = smem_u32(sm);
@@ -431,9 +462,8 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
   };
   const int piece = tid & 7, r0 = tid >> 3;  // rows r0 + 16 i
   bool first = true;
-  for (int32_t t = tb; t < te;) {
-    const Segment s = segment_at<N>(P, t, te);
-    t += s.t1 - s.t0;
+  Segment s;
+  for (Walk w = first_of(P); next_segment<N>(P, w, s);) {
     if (s.v0 >= s.v1) continue;
     const AttendItem& it = s.it;
     // Queries: [chunk][column][128 B], zeros past the key and the columns.
@@ -540,8 +570,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
 
 // Issuing warp: all its lanes walk the same path, one of them issues.
 template <int N, int MAXI>
-__device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int32_t tb,
-                               int32_t te) {
+__device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl) {
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
   const uint32_t base = smem_u32(sm);
@@ -572,9 +601,8 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
     for (int k = 0; k < 4; ++k)
       if (k < steps) mma(tm_s, at + 2 * k, hi, b + 2 * k, hi, id1, add || k > 0);
   };
-  for (int32_t t = tb; t < te;) {
-    const Segment s = segment_at<N>(P, t, te);
-    t += s.t1 - s.t0;
+  Segment s;
+  for (Walk w = first_of(P); next_segment<N>(P, w, s);) {
     if (s.v0 >= s.v1) continue;
     warp_wait(smem_u32(&ctl.qfull), qphase, &ctl.gave_up);
     fence_async();
@@ -758,7 +786,7 @@ __device__ __forceinline__ void transpose4(float* v, int lane) {
 // then the segment's output.
 template <int N, int MAXI>
 __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid,
-                             int32_t tb, int32_t te, float* parts) {
+                             float* parts) {
   constexpr int C = N / 2;
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
@@ -772,9 +800,8 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
   uint32_t sphase = 0, ophase = 0;
   auto larger = [](float a, float b) { return fmaxf(a, b); };
   auto sum = [](float a, float b) { return a + b; };
-  for (int32_t t = tb; t < te;) {
-    const Segment s = segment_at<N>(P, t, te);
-    t += s.t1 - s.t0;
+  Segment s;
+  for (Walk w = first_of(P); next_segment<N>(P, w, s);) {
     const AttendItem& it = s.it;
     named_sync(1, kSoftThreads);  // the previous segment's column tables are read
     if (tid == 0) ctl.o_begun = 0;
@@ -1037,14 +1064,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  const int32_t tb = first_tile(P.c.n_tiles, gridDim.x, blockIdx.x);
-  const int32_t te = first_tile(P.c.n_tiles, gridDim.x, blockIdx.x + 1);
   if (warp < kSoftThreads / 32) {
-    softmax_rows<N>(P, sm, ctl, tid, tb, te, parts);
+    softmax_rows<N>(P, sm, ctl, tid, parts);
   } else if (warp < (kSoftThreads + kLoadThreads) / 32) {
-    load_rows<N>(P, sm, ctl, tid - kSoftThreads, tb, te);
+    load_rows<N>(P, sm, ctl, tid - kSoftThreads);
   } else {
-    issue_products<N>(P, sm, ctl, tb, te);
+    issue_products<N>(P, sm, ctl);
   }
   __syncwarp();
   tc_before();
@@ -1080,12 +1105,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   __shared__ float4 sums[kMergeWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b0 = M.cut[blockIdx.x] - 1;
-  const int32_t t = first_tile(c.n_tiles, M.blocks, b0 + 1);
+  const int32_t t = first_tile(c.n_tiles, c.waved, M.blocks, b0 + 1);
   const Segment s = segment_at<N>(P, t, t + 1);
   // the block that holds the job's last tile: the largest b with
   // first_tile(b) <= last
   const int64_t last = (int64_t)(t - s.t0) + s.tiles - 1;
-  const int n = (int)(((last + 1) * M.blocks - 1) / c.n_tiles) - b0 + 1;
+  const int n = (int)(((last + 1 - c.waved) * M.blocks - 1) / (c.n_tiles - c.waved)) - b0 + 1;
   const int spans = (c.dv + kMergeElems - 1) / kMergeElems;
   const int pair = blockIdx.y * (kMergeWarps / M.groups) + warp / M.groups;
   const int col = pair / spans, d = pair % spans * kMergeElems + lane * 4;
@@ -1220,6 +1245,9 @@ struct Shape {
   int n;            // columns of a block
   int64_t tiles;
   int blocks;
+  int waves;        // whole jobs that every block takes first, one at a time
+  int64_t waved;    // tiles of them all
+  int64_t job_tiles;
   int n_cut;        // jobs cut by a block's boundary
   int parts;        // of the longest job, about
   MergeParams merge;
@@ -1254,23 +1282,29 @@ Shape shape_of(const AttendCommon& c, AttendItem* items, int n_items, int sms) {
   }
   sms = std::min(sms, kAttendMaxBlocks);
   s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(sms, s.tiles));
-  // Whole jobs per block where that makes no block's share longer: nothing to
-  // join then.
-  const int64_t each = (n_jobs + sms - 1) / sms;
-  if (longest == shortest && n_jobs % each == 0 &&
-      each * longest <= (s.tiles + s.blocks - 1) / s.blocks)
-    s.blocks = (int)(n_jobs / each);
-  s.parts = (int)std::min<int64_t>(s.blocks, longest * s.blocks / s.tiles + 2);
+  // Jobs of equal length: whole ones in waves over the blocks (64 verify
+  // blocks of 8 queries, whose rows are mostly the same: XXX), fewer blocks if
+  // that leaves nothing to split and no block with more to do.
+  if (longest == shortest) {
+    const int64_t each = (n_jobs + sms - 1) / sms;
+    if (n_jobs % each == 0 && each * longest <= (s.tiles + s.blocks - 1) / s.blocks)
+      s.blocks = (int)(n_jobs / each);
+    s.waves = (int)(n_jobs / s.blocks);
+    s.job_tiles = longest;
+    s.waved = s.waves * s.blocks * longest;
+  }
+  const int64_t rest = s.tiles - s.waved;  // dealt out evenly, cut where it falls
+  s.parts = rest ? (int)std::min<int64_t>(s.blocks, longest * s.blocks / rest + 2) : 0;
   s.merge.blocks = s.blocks;
   s.merge.groups = s.parts > 24 ? 16 : s.parts > 4 ? 4 : 1;
-  if (s.tiles <= INT32_MAX) {
+  if (s.tiles <= INT32_MAX && rest) {
     int k = 0;
     int64_t cut_job = -1;  // first tile of the job cut last
     for (int b = 1; b < s.blocks; ++b) {
-      const int32_t t = first_tile(s.tiles, s.blocks, b);
+      const int32_t t = first_tile(s.tiles, (int32_t)s.waved, s.blocks, b);
       while (k + 1 < n_items && items[k + 1].tile0 <= t) ++k;
       const int32_t in = (t - items[k].tile0) % items[k].tiles;
-      if (in == 0 || t - in == cut_job) continue;
+      if (in == 0 || t - in == cut_job || t >= s.tiles) continue;
       cut_job = t - in;
       s.merge.cut[s.n_cut++] = (uint8_t)b;
     }
@@ -1304,6 +1338,9 @@ cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items
   P.c = c;
   P.c.n_items = n_items;
   P.c.n_tiles = (int32_t)s.tiles;
+  P.c.waves = s.waves;
+  P.c.waved = (int32_t)s.waved;
+  P.c.job_tiles = (int32_t)s.job_tiles;
   P.plan = make_plan(c, s.n);
   for (int i = 0; i < n_items; ++i) P.items[i] = items[i];
   switch (s.n) {

@@ -316,6 +316,7 @@ struct AttendCommon {
   int32_t row_bytes, T, Pmax, page_shift;
   uint32_t* status;
   int32_t n_items, n_tiles;
+  int32_t waves, waved, job_tiles;  // whole jobs dealt out first (launch_attend)
   int32_t f16;            // rows are f16, else bf16
   int32_t heads, group;   // query heads, query heads per kv head
   int32_t dk, dv;         // elements of a key and of a value
