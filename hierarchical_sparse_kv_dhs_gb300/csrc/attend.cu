@@ -44,9 +44,7 @@ constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk
 constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
 constexpr float kSlack = 8.f;              // log2 units
-// A wait sleeps up to kWaitNs at a time (polling would take shared-memory
-// cycles from the copies) and gives up after kWaitPolls times.
-constexpr uint32_t kWaitNs = 20000, kWaitPolls = 1u << 17;
+constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
 
 // How a launch's row slices are staged.
 struct Plan {
@@ -86,10 +84,10 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kWaitNs)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -100,7 +98,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
   for (uint32_t n = 0; n < kWaitPolls; ++n) {
     if (bar_try(bar, parity)) return;
-    if ((n & 15) == 15 && *gave_up) return;
+    if ((n & 255) == 255 && *gave_up) return;
   }
   *gave_up = 1;
 }
@@ -534,7 +532,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
           const int r = r0 + 16 * i;
           const bool on = row[i] && e < n;
           const uint8_t* src = on ? row[i] + at + 2 * e : c.tail;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+          asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(
                            dst + r * 128 + ((piece ^ (r & 7)) << 4)),
                        "l"(src), "r"(on ? 16 : 0)
                        : "memory");

@@ -336,14 +336,18 @@ cudaError_t launch_attend(const AttendCommon& c, AttendItem* items, int n_items,
 
 // ------------------------------------------------------------ forks
 constexpr int kForkSourcesMax = 256;
+// Sources and page slots that travel with a launch; beyond them the child's
+// slots go through the device's page map.
+constexpr int kForkSourcesSome = 64, kForkSlotsMax = 6656;
 
 struct ForkSource {
   const uint8_t* host_from;  // device-visible host rows (null: a window source)
   uint8_t* host_to;
   int64_t L;
+  int64_t unit0;             // first work unit of this source in the launch
   int32_t from, to;          // pairs
   int32_t complete;          // complete imported pages
-  int32_t unit0;             // first work unit of this source in the launch
+  int32_t slot0;             // first of the child's page slots in the launch's table
 };
 
 struct ForkCommon {
@@ -352,13 +356,27 @@ struct ForkCommon {
   uint8_t* hot;
   int32_t* tags;
   uint32_t* stamps;
-  const int32_t* map;
+  int32_t* map;
+  int64_t n_units;
   int32_t row_bytes, T, B, Pmax, page_shift;
-  int32_t n_sources, n_units;
+  int32_t n_sources;
 };
 
-cudaError_t launch_fork(const ForkCommon& c, const ForkSource* sources, int n_sources, int sms,
-                        cudaStream_t stream);
+// slots: the child's slot of each complete page (-1: not resident), source by
+// source; null: they are in c.map.
+cudaError_t launch_fork(const ForkCommon& c, const ForkSource* sources, int n_sources,
+                        const int32_t* slots, int n_slots, int sms, cudaStream_t stream);
+
+// Consecutive pages of one map, in consecutive slots, to consecutive slots.
+struct PageRun {
+  int64_t map;    // map entry of the first page
+  int32_t from, to, pages;
+};
+cudaError_t launch_page_runs(uint8_t* opt, int32_t* map, int row_bytes, int page_shift,
+                             const PageRun* runs, int64_t n_runs, int sms, cudaStream_t stream);
+
+// Empty hot caches: tags -1, stamps 0.
+cudaError_t launch_clear_hot(int32_t* tags, uint32_t* stamps, int64_t n, cudaStream_t stream);
 
 // ------------------------------------------------------------ append (A0)
 constexpr int kAppendThreads = 256;

@@ -141,6 +141,11 @@ struct PairState {
                                  // deferred, 0 = backed (empty: all backed)
 };
 
+struct BackupRun {
+  uint64_t order;  // of the first page
+  int32_t pair, page, pages;
+};
+
 }  // namespace
 
 struct dhs_pool {
@@ -185,12 +190,12 @@ struct dhs_pool {
   int fresh_list = -1;          // DHS_OPT_FRESH_LIST: -1 auto, 0 off, 1 on
   int64_t complete_pages = 0;   // complete imported pages of admitted pairs
   uint64_t bseq = 0;            // pages put in backup order so far
-  // Pages whose host backup is deferred, in order: (order, pair * pmax + page).
-  // An entry counts while its page's PairState::backup holds its order; the
-  // others are skipped, and swept out once they outnumber the live ones
-  // (a fork queues and a release drops thousands of pages at a time).
-  std::vector<std::pair<uint64_t, int64_t>> backup_queue;
-  size_t backup_head = 0;       // entries before it are done with
+  // Pages whose host backup is deferred, in order, as runs of consecutive
+  // pages and orders (a fork or an admission queues thousands at a time).  A
+  // page of a run counts while its PairState::backup holds its order; the
+  // others are skipped, and runs without any swept out now and then.
+  std::vector<BackupRun> backup_queue;
+  size_t backup_head = 0;       // runs before it are done with
   int64_t backup_live = 0;
   int32_t rr = 0;               // refill cursor: the next request visited
   int sm_count = 0;
@@ -226,6 +231,7 @@ struct dhs_pool {
   std::vector<LocKey> loc_keys;
   std::vector<dhs::AppendItem> aitems;
   std::vector<dhs::AttendItem> titems;
+  std::vector<dhs::PageRun> runs;      // page runs of a compaction
   std::vector<uint8_t> seen;
   std::vector<int32_t> app_of_pair;  // decode step: append item of each pair, -1 = none
   std::vector<int64_t> l0_of_pair;   // length of each resolved pair before this step's append
@@ -489,28 +495,36 @@ int flush(dhs_pool* p) {
   return DHS_OK;
 }
 
-bool backup_waits(const dhs_pool* p, const std::pair<uint64_t, int64_t>& e) {
-  const std::vector<uint64_t>& b = p->ps[e.second / p->pmax].backup;
-  return !b.empty() && b[e.second % p->pmax] == e.first;
+bool backup_waits(const dhs_pool* p, const BackupRun& r, int32_t i) {
+  const std::vector<uint64_t>& b = p->ps[r.pair].backup;
+  return !b.empty() && b[r.page + i] == r.order + i;
 }
 
-// Make room for n more entries (may throw; queue_backup then does not).
+// Make room for n more pages (may throw; queue_backup then does not).
 void reserve_backup(dhs_pool* p, size_t n) {
   auto& q = p->backup_queue;
-  if (q.size() + n > q.capacity() || q.size() > 2 * (size_t)p->backup_live + 4096) {
+  if (q.size() > (size_t)p->backup_live + 1024) {
     size_t to = 0;
-    for (size_t i = p->backup_head; i < q.size(); ++i)
-      if (backup_waits(p, q[i])) q[to++] = q[i];
+    for (size_t i = p->backup_head; i < q.size(); ++i) {
+      int32_t k = 0;
+      while (k < q[i].pages && !backup_waits(p, q[i], k)) ++k;
+      if (k < q[i].pages) q[to++] = q[i];
+    }
     q.resize(to);
     p->backup_head = 0;
-    if (q.size() + n > q.capacity()) q.reserve(std::max(2 * q.capacity(), q.size() + n));
   }
+  if (q.size() + n > q.capacity()) q.reserve(std::max(2 * q.capacity(), q.size() + n));
 }
 
 // Defer the host backup of page `q` of `pair` (PairState::backup is sized).
 void queue_backup(dhs_pool* p, int64_t pair, int64_t q) {
-  p->backup_queue.push_back({++p->bseq, pair * p->pmax + q});
-  p->ps[pair].backup[q] = p->bseq;
+  const uint64_t order = ++p->bseq;
+  BackupRun* r = p->backup_queue.size() > p->backup_head ? &p->backup_queue.back() : nullptr;
+  if (r && r->pair == pair && r->page + r->pages == q && r->order + r->pages == order)
+    ++r->pages;
+  else
+    p->backup_queue.push_back({order, (int32_t)pair, (int32_t)q, 1});
+  p->ps[pair].backup[q] = order;
   ++p->backup_live;
 }
 
@@ -1004,11 +1018,14 @@ int dhs_backup(dhs_pool* p, int64_t max_pages, int64_t* done) {
   p->moves.clear();
   int64_t n = 0;
   while (n < max_pages && p->backup_live > 0) {
-    const std::pair<uint64_t, int64_t> e = p->backup_queue[p->backup_head++];
-    if (!backup_waits(p, e)) continue;
-    const int64_t key = e.second;
-    if ((rc = backup_page(p, key / p->pmax, key % p->pmax))) return rc;
-    ++n;
+    BackupRun& r = p->backup_queue[p->backup_head];
+    if (backup_waits(p, r, 0)) {
+      if ((rc = backup_page(p, r.pair, r.page))) return rc;
+      ++n;
+    }
+    ++r.order;
+    ++r.page;
+    if (--r.pages == 0) ++p->backup_head;
   }
   if ((rc = run_moves(p))) return rc;
   if (done) *done = n;
@@ -1131,10 +1148,8 @@ int dhs_release(dhs_pool* p, int32_t req) {
     p->ps[pair] = PairState();
   }
   const int64_t pair0 = (int64_t)req * p->cfg.sources;
-  cudaError_t e = cudaMemsetAsync(p->tags + pair0 * B, 0xFF, p->cfg.sources * B * 4, p->stream);
-  if (e == cudaSuccess)
-    e = cudaMemsetAsync(p->stamps + pair0 * B, 0, p->cfg.sources * B * 4, p->stream);
-  return cuda_rc(e);
+  return cuda_rc(dhs::launch_clear_hot(p->tags + pair0 * B, p->stamps + pair0 * B,
+                                       p->cfg.sources * B, p->stream));
 }
 
 int dhs_flush(dhs_pool* p) {
@@ -1949,6 +1964,7 @@ static void undo_fork(dhs_pool* p, int32_t child) {
     const int64_t pair = (int64_t)child * p->cfg.sources + s;
     if (!p->ps[pair].admitted) continue;
     drop_pages(p, pair, false);
+    mark_dirty(p, pair);
     p->complete_pages -= p->ps[pair].N >> p->page_shift;
     p->ps[pair] = PairState();
   }
@@ -1982,8 +1998,11 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
   int rc = enter(p);
   if (rc) return rc;
   std::vector<dhs::ForkSource> src;
+  std::vector<int32_t> slots;  // the child's, where they travel with the launch
+  bool direct = false;
   try {
     src.reserve(c.sources);
+    int64_t pages = 0;
     for (int32_t s = 0; s < c.sources; ++s) {
       const PairState& f = p->ps[from0 + s];
       if (!f.admitted) continue;
@@ -2002,14 +2021,26 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
         k.host_to = (uint8_t*)hdev;
         k.complete = (int32_t)(f.N >> p->page_shift);
       }
+      k.slot0 = (int32_t)std::min<int64_t>(pages, INT32_MAX);
+      pages += k.complete;
       src.push_back(k);
     }
+    direct = pages <= dhs::kForkSlotsMax && src.size() <= (size_t)dhs::kForkSourcesSome;
+    if (direct) slots.assign((size_t)pages + 1, -1);
     const int64_t usable = p->capacity - c.admission_reserve_pages;
     if (p->used + want > usable) {
       if (deficit) *deficit = p->used + want - usable;
       return DHS_EWOULDWAIT;
     }
     reserve_backup(p, (size_t)want);
+    // The parent's pending pages and the maps, before the copy reads them.  If
+    // only the child's map awaits an upload (its release, mostly), none is
+    // needed: the copy writes that map itself.
+    if (direct && !p->any_pending && p->dirty_lo >= to0 && p->dirty_hi < to0 + c.sources) {
+      p->dirty_lo = INT64_MAX;
+      p->dirty_hi = -1;
+    }
+    if (direct && (rc = flush(p))) return rc;
     for (const dhs::ForkSource& k : src) {
       const int32_t s = (int32_t)(k.to - to0);
       const PairState& f = p->ps[k.from];
@@ -2025,7 +2056,7 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
       const uint8_t* mask = masks && !f.window ? masks[s] : nullptr;
       const int32_t* pm = p->map_host.data() + (int64_t)k.from * p->pmax;
       int32_t* to = p->map_host.data() + (int64_t)k.to * p->pmax;
-      mark_dirty(p, k.to);
+      if (!direct) mark_dirty(p, k.to);
       for (int64_t q = 0; q < k.complete; ++q) {
         if (mask ? !mask[q] : pm[q] < 0) continue;
         queue_backup(p, k.to, q);
@@ -2034,10 +2065,10 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
         p->slot_page[slot] = (int32_t)q;
         p->used += 1;
         to[q] = (int32_t)slot;
+        if (direct) slots[k.slot0 + q] = (int32_t)slot;
       }
     }
-    // the parent's pending pages and both page maps, before the copy reads them
-    rc = flush(p);
+    if (!direct) rc = flush(p);
   } catch (...) {
     rc = DHS_ENOMEM;
   }
@@ -2059,7 +2090,8 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
   f.page_shift = p->page_shift;
   for (size_t b = 0; b < src.size(); b += dhs::kForkSourcesMax) {
     const int n = (int)std::min<size_t>(dhs::kForkSourcesMax, src.size() - b);
-    if (dhs::launch_fork(f, src.data() + b, n, std::max(1, p->sm_count), p->stream) !=
+    if (dhs::launch_fork(f, src.data() + b, n, direct ? slots.data() : nullptr,
+                         (int)slots.size(), std::max(1, p->sm_count), p->stream) !=
         cudaSuccess) {
       undo_fork(p, child);
       return DHS_ECUDA;
@@ -2075,14 +2107,12 @@ int dhs_compact(dhs_pool* p, int64_t capacity, int64_t* moved) {
   int rc = enter(p);
   if (rc) return rc;
   // pages still to be filled are filled where they are, then moved
-  if ((rc = flush(p))) return rc;
-  const int64_t pb = (int64_t)p->cfg.page_rows * p->cfg.row_bytes;
-  uint8_t* opt = (uint8_t*)p->cfg.opt_dev;
+  if (p->any_pending && (rc = flush(p))) return rc;
   int64_t n = 0;
   for (int64_t i = capacity; i < p->capacity; ++i) n += p->slot_pair[i] >= 0;
-  p->moves.clear();
+  p->runs.clear();
   try {
-    p->moves.reserve(n);
+    p->runs.reserve(n);
   } catch (...) {
     return DHS_ENOMEM;
   }
@@ -2090,24 +2120,24 @@ int dhs_compact(dhs_pool* p, int64_t capacity, int64_t* moved) {
   for (int64_t i = capacity; i < p->capacity; ++i) {
     if (p->slot_pair[i] < 0) continue;
     while (p->slot_pair[to] >= 0) ++to;
-    p->moves.push_back({opt + i * pb, opt + to * pb});
+    const int64_t at = p->slot_pair[i] * p->pmax + p->slot_page[i];
+    dhs::PageRun* r = p->runs.empty() ? nullptr : &p->runs.back();
+    if (r && at == r->map + r->pages && i == r->from + r->pages && to == r->to + r->pages)
+      ++r->pages;
+    else
+      p->runs.push_back({at, (int32_t)i, (int32_t)to, 1});
     p->slot_pair[to] = p->slot_pair[i];
     p->slot_page[to] = p->slot_page[i];
     p->slot_pair[i] = p->slot_page[i] = -1;
-    p->map_host[p->slot_pair[to] * p->pmax + p->slot_page[to]] = (int32_t)to;
-    mark_dirty(p, p->slot_pair[to]);
+    // the copy writes the device's entry; an upload still to come agrees
+    p->map_host[at] = (int32_t)to;
   }
   p->first_free = to;
   p->capacity = capacity;
   if (moved) *moved = n;
-  if (!small_pages(p)) {  // pages too large for the page kernel
-    for (const dhs::PageMove& m : p->moves)
-      if (cudaMemcpyAsync(m.dst, m.src, pb, cudaMemcpyDeviceToDevice, p->stream) != cudaSuccess)
-        return DHS_ECUDA;
-    p->moves.clear();
-  }
-  if ((rc = run_moves(p))) return rc;
-  return flush(p);
+  return cuda_rc(dhs::launch_page_runs((uint8_t*)p->cfg.opt_dev, p->map, p->cfg.row_bytes,
+                                       p->page_shift, p->runs.data(), (int64_t)p->runs.size(),
+                                       std::max(1, p->sm_count), p->stream));
 }
 
 int64_t dhs_pool_capacity(const dhs_pool* p) { return p ? p->capacity : -1; }
