@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cstddef>
 
 #include "dhs_internal.h"
 
@@ -43,6 +44,7 @@ constexpr int kThreads = kSoftThreads + kLoadThreads + 32;
 constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk of a tile
 constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
+constexpr int kSegments = 4;               // segments from the loading warps to the others
 constexpr float kSlack = 8.f;              // log2 units
 constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
 
@@ -62,6 +64,7 @@ template <int MAXI>
 struct AttendParams {
   AttendCommon c;
   Plan plan;
+  int32_t first[MAXI];   // first tile of each item, past the last one INT32_MAX
   AttendItem items[MAXI];
 };
 static_assert(sizeof(AttendParams<kAttendItemsLarge>) <= 32764, "attend item table too large");
@@ -96,6 +99,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // the block then falls through, so that all its warps still reach their end
 // (on wrong data: the launch's status says so).
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+#pragma unroll 1
   for (uint32_t n = 0; n < kWaitPolls; ++n) {
     if (bar_try(bar, parity)) return;
     if ((n & 255) == 255 && *gave_up) return;
@@ -262,40 +266,64 @@ __device__ __forceinline__ void query_rows(const AttendItem& it, int i, int64_t&
   hi = (it.range ? min((int64_t)it.range[2 * i + 1], L) : L - it.Q + 1 + i) - it.first;
 }
 
+// Launch parameters through memory: lanes read different ones, and many at a
+// time, where constant memory answers one miss after the other (~500 cycles
+// each, after every launch).
+template <class T>
+__device__ __forceinline__ T fetch(const T* p) {
+  union {
+    T t;
+    uint4 q[sizeof(T) / 16];
+  } u;
+  static_assert(sizeof(T) % 16 == 0, "whole 16-byte words");
+  const uint4* a = reinterpret_cast<const uint4*>(p);
+  asm volatile("" : "+l"(a));  // no longer known to be a parameter
+#pragma unroll
+  for (int k = 0; k < (int)(sizeof(T) / 16); ++k) u.q[k] = a[k];
+  return u.t;
+}
+
+// The last item whose first tile is <= t (an item without jobs has none).
+template <int MAXI>
+__device__ __forceinline__ int item_at(const AttendParams<MAXI>& P, int32_t t) {
+  const int32_t* first = P.first + (threadIdx.x & 31);
+  asm volatile("" : "+l"(first));
+  int32_t x[(MAXI + 31) / 32];
+#pragma unroll
+  for (int k = 0; k < (MAXI + 31) / 32; ++k)
+    x[k] = 32 * k + (threadIdx.x & 31) < MAXI ? first[32 * k] : INT32_MAX;
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < (MAXI + 31) / 32; ++k) n += __popc(__ballot_sync(~0u, x[k] <= t));
+  return n - 1;
+}
+
 // The segment that begins at tile `t` of the launch and ends before `te`.
 // Called by whole warps.
 template <int N, int MAXI>
 __device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te) {
   const AttendCommon& c = P.c;
   __syncwarp();
-  int a = 0, b = c.n_items;  // last item whose first tile is <= t (empty items have no tiles)
-  while (b - a > 1) {
-    const int m = (a + b) >> 1;
-    if (P.items[m].tile0 <= t) a = m;
-    else b = m;
-  }
   Segment s;
-  s.it = P.items[a];
+  s.it = fetch(&P.items[item_at(P, t)]);
   const AttendItem& it = s.it;
   const bool located = it.loc != nullptr;
   s.tiles = it.tiles;
-  int32_t job = (t - it.tile0) / it.tiles;
+  const int32_t job = (t - it.tile0) / it.tiles;
   s.t0 = (t - it.tile0) - job * it.tiles;
   s.t1 = min(it.tiles, s.t0 + (te - t));
   const int32_t columns = located ? c.group : it.Q * c.group;
-  const int32_t nblk = (columns + N - 1) / N, width = (columns + nblk - 1) / nblk;
-  const int32_t blk = job % nblk;
-  job /= nblk;
-  const int32_t kv = c.heads / c.group;
-  s.g = job % kv;
-  s.qbase = job / kv;
-  s.col0 = blk * width;
-  s.cols = min(width, columns - s.col0);
+  const int32_t query = job / it.blocks;
+  s.col0 = (job - query * it.blocks) * it.width;
+  s.cols = min(it.width, columns - s.col0);
+  s.qbase = query / c.kv;
+  s.g = query - s.qbase * c.kv;
   s.lo = 0;
   s.hi = it.len;
   if (!located) {
     const int q0 = s.col0 / c.group, q1 = (s.col0 + s.cols - 1) / c.group;
     int64_t lo = it.len, hi = 0;
+#pragma unroll 1
     for (int i = q0 + (threadIdx.x & 31); i <= q1; i += 32) {
       int64_t x, y;
       query_rows(it, i, x, y);
@@ -304,6 +332,7 @@ __device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te
         hi = max(hi, y);
       }
     }
+#pragma unroll 1
     for (int w = 16; w; w >>= 1) {
       lo = min(lo, (int64_t)__shfl_xor_sync(~0u, (long long)lo, w));
       hi = max(hi, (int64_t)__shfl_xor_sync(~0u, (long long)hi, w));
@@ -317,9 +346,8 @@ __device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te
 }
 
 // First tile of block b's share of what the waves leave.
-__host__ __device__ __forceinline__ int32_t first_tile(int64_t total, int32_t waved, int blocks,
-                                                       int b) {
-  return waved + (int32_t)((total - waved) * b / blocks);
+__host__ __device__ __forceinline__ int32_t first_tile(const AttendCommon& c, int32_t b) {
+  return c.waved + b * c.share + min(b, c.extra);
 }
 
 // A block's segments: first a whole job of each wave (jobs of equal length go
@@ -332,23 +360,22 @@ struct Walk {
 template <int MAXI>
 __device__ __forceinline__ Walk first_of(const AttendParams<MAXI>& P) {
   const AttendCommon& c = P.c;
-  return {0, first_tile(c.n_tiles, c.waved, gridDim.x, blockIdx.x),
-          first_tile(c.n_tiles, c.waved, gridDim.x, blockIdx.x + 1)};
+  return {0, first_tile(c, blockIdx.x), first_tile(c, blockIdx.x + 1)};
 }
 template <int N, int MAXI>
 __device__ bool next_segment(const AttendParams<MAXI>& P, Walk& w, Segment& s) {
   const AttendCommon& c = P.c;
   int32_t t = w.t, te = w.te;
-  if (w.wave < c.waves) {
+  const bool wave = w.wave < c.waves;
+  if (wave) {
     t = (int32_t)((w.wave * gridDim.x + blockIdx.x) * c.job_tiles);
     te = t + c.job_tiles;
     ++w.wave;
-    s = segment_at<N>(P, t, te);
-    return true;
+  } else if (t >= te) {
+    return false;
   }
-  if (t >= te) return false;
   s = segment_at<N>(P, t, te);
-  w.t += s.t1 - s.t0;
+  if (!wave) w.t += s.t1 - s.t0;
   return true;
 }
 
@@ -406,7 +433,9 @@ __device__ __forceinline__ const uint8_t* row_of(const AttendCommon& c, const Se
 struct Control {
   uint64_t kfull[kMaxK], kempty[kMaxK], vfull[kMaxV], vempty[kMaxV];
   uint64_t qfull, qempty, sfull, pfull, ofull, oempty, rfull[2], rempty[2], drain;
-  uint64_t unused[13];  // to 64: two barriers a lane
+  uint64_t segfull[kSegments], segempty[kSegments];
+  uint64_t unused[5];  // to 64: two barriers a lane
+  Segment seg[kSegments];  // found by the loading warps, for the others
   const uint8_t* row[2][kTile];
   int64_t out_off[64];
   int32_t lse_at[64];
@@ -422,8 +451,9 @@ struct Control {
 // Places of the single barriers in Control's order
 constexpr int kBarQfull = 2 * kMaxK + 2 * kMaxV, kBarPfull = kBarQfull + 3,
               kBarOempty = kBarQfull + 5, kBarRfull = kBarQfull + 6, kBarRempty = kBarQfull + 8,
-              kBarDrain = kBarQfull + 10, kBarriers = 64;
-static_assert(kBarDrain + 1 + 13 == kBarriers, "barrier table");
+              kBarDrain = kBarQfull + 10, 
+              kBarSegempty = kBarDrain + 1 + kSegments, kBarriers = 64;
+static_assert(kBarSegempty + kSegments + 5 == kBarriers, "barrier table");
 constexpr uint32_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
 
 // Parity bookkeeping of a ring of slots.
@@ -461,8 +491,21 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
   const int piece = tid & 7, r0 = tid >> 3;  // rows r0 + 16 i
   bool first = true;
   Segment s;
-  for (Walk w = first_of(P); next_segment<N>(P, w, s);) {
-    if (s.v0 >= s.v1) continue;
+  Ring seg;
+  bool more = true;
+#pragma unroll 1
+  for (Walk w = first_of(P); more;) {
+    more = next_segment<N>(P, w, s);
+    if (tid < 32) {  // one without columns ends the walk of the other warps
+      wait_empty(smem_u32(&ctl.segempty[seg.slot]), seg.phase ^ 1);
+      if (!more) s.cols = 0;
+      if (tid == 0) {
+        ctl.seg[seg.slot] = s;
+        bar_arrive(smem_u32(&ctl.segfull[seg.slot]));
+      }
+      seg.next(kSegments);
+    }
+    if (!more || s.v0 >= s.v1) continue;
     const AttendItem& it = s.it;
     // Queries: [chunk][column][128 B], zeros past the key and the columns.
     // Loaded behind the first tile's key chunks: the segment before may still
@@ -474,6 +517,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
       }
       first = false;
       const bool aligned = !(((uintptr_t)it.q | c.q_qs | c.q_hs) & 15);
+#pragma unroll 1
       for (int col = tid >> 3; col < N; col += kLoadThreads / 8) {
         const bool on = col < s.cols;
         const int qc = s.col0 + min(col, s.cols - 1);
@@ -481,6 +525,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
         const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
         const uint8_t* src = it.q + qi * c.q_qs + h * c.q_hs;
         const uint32_t dst = pl.off_q + col * 128 + ((piece ^ (col & 7)) << 4);
+#pragma unroll 1
         for (int ch = 0; ch < pl.key_chunks; ++ch) {
           const int el = ch * 64 + piece * 8;
           const bool in = on && el < c.dk;
@@ -510,6 +555,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     int64_t j = (int64_t)s.v0 * kTile + tid;  // this thread's row of the tile
     uint32_t word = row_word(c, s, j, row_index(s, j));
     int32_t index = row_index(s, j + kTile);
+#pragma unroll 1
     for (int tile = s.v0; tile < s.v1; ++tile) {
       // the tile's row addresses, to every loading thread and the softmax
       wait_empty(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1);
@@ -599,15 +645,25 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
     for (int k = 0; k < 4; ++k)
       if (k < steps) mma(tm_s, at + 2 * k, hi, b + 2 * k, hi, id1, add || k > 0);
   };
-  Segment s;
-  for (Walk w = first_of(P); next_segment<N>(P, w, s);) {
-    if (s.v0 >= s.v1) continue;
+  Ring seg;
+#pragma unroll 1
+  for (;;) {
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
+    const Segment& s = ctl.seg[seg.slot];
+    const int32_t v0 = s.v0, v1 = s.v1, cols = s.cols;
+    if (!cols || ctl.gave_up) break;
+    __syncwarp();
+    if (lead) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
+    seg.next(kSegments);
+    if (v0 >= v1) continue;
     warp_wait(smem_u32(&ctl.qfull), qphase, &ctl.gave_up);
     fence_async();
     qphase ^= 1;
-    for (int tile = s.v0; tile < s.v1; ++tile) {
+#pragma unroll 1
+    for (int tile = v0; tile < v1; ++tile) {
       const int kslot = kr.slot;
       auto keys = [&](bool add) {
+#pragma unroll 1
         for (int k = 0; k < pl.only_chunks; ++k) {
           warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
           fence_async();
@@ -620,6 +676,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
       if (!pl.alias) keys(false);
       Ring v = vr;
       if (pl.shared) {
+#pragma unroll 1
         for (int u = 0; u < pl.units; ++u) {
           warp_wait(smem_u32(&ctl.vfull[v.slot]), v.phase, &ctl.gave_up);
           fence_async();
@@ -633,16 +690,17 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
       if (pl.alias) keys(true);
       if (lead) {
         commit(smem_u32(&ctl.sfull));
-        if (tile + 1 == s.v1) commit(smem_u32(&ctl.qempty));
+        if (tile + 1 == v1) commit(smem_u32(&ctl.qempty));
       }
       warp_wait(smem_u32(&ctl.pfull), pphase, &ctl.gave_up);
       pphase ^= 1;
-      if (tile == s.v0 && !first) {  // the previous segment's sums are read
+      if (tile == v0 && !first) {  // the previous segment's sums are read
         warp_wait(smem_u32(&ctl.oempty), ophase, &ctl.gave_up);
         ophase ^= 1;
       }
       tc_after();
-      const bool begun = tile > s.v0 || *(volatile uint32_t*)&ctl.o_begun;
+      const bool begun = tile > v0 || *(volatile uint32_t*)&ctl.o_begun;
+#pragma unroll 1
       for (int u = 0; u < pl.units; ++u) {
         if (!pl.shared) {
           warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
@@ -661,13 +719,14 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
       }
       if (lead) {
         if (pl.alias) commit(smem_u32(&ctl.kempty[kslot]));
-        if (tile + 1 == s.v1) commit(smem_u32(&ctl.ofull));
+        if (tile + 1 == v1) commit(smem_u32(&ctl.ofull));
       }
     }
     first = false;
   }
   // nothing of ours is in flight when tensor memory goes back
   if (lead) commit(smem_u32(&ctl.drain));
+#pragma unroll 1
   for (uint32_t n = 0; n < kWaitPolls && !bar_try(smem_u32(&ctl.drain), 0); ++n) {
   }
   __syncwarp();
@@ -677,6 +736,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
 __device__ bool finite_row(const uint8_t* p, int n, int f16) {
   const uint32_t e = f16 ? 0x7C00u : 0x7F80u;
   bool ok = true;
+#pragma unroll 1
   for (int k = 0; k < n; k += 8) {
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 2 * k));
     for (const uint32_t w : {v.x, v.y, v.z, v.w})
@@ -703,18 +763,24 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
   if ((tid & 31) == 0 && tid < kTile) ctl.odd[tid >> 5] = marked;
   float v[8];
   if (first) {
+#pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = 0.f;
+#pragma unroll 1
     for (int u = 0; u < pl.units; ++u)
+#pragma unroll 1
       for (int k = 0; k < C; k += 8) tm_store(tm_o + u * N + k, v);
     if (tid == 0) ctl.o_begun = 1;
   }
   named_sync(1, kSoftThreads);
+#pragma unroll 1
   for (int i = 0; i < kTile; ++i) {
     if (!(ctl.odd[i >> 5] >> (i & 31) & 1)) continue;
     if ((r >> 5) == (i >> 5)) {  // the warps that own the row
+#pragma unroll 1
       for (int k = 0; k < C; k += 8) {
         tm_load(tm_s + k, v);
         if (r == i)
+#pragma unroll
           for (int n = 0; n < 8; ++n) {
             const int col = k0 + k + n;
             const bool seen = tile0 + i >= ctl.col_lo[col] && tile0 + i < ctl.col_hi[col];
@@ -725,14 +791,17 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
     }
     named_sync(1, kSoftThreads);
     const uint8_t* y = ctl.odd_row;
+#pragma unroll 1
     for (int u = 0; u < pl.units; ++u) {
       const int d = u * 128 + r;
       float e = 0.f;
       if (d < c.dv)
         e = c.f16 ? __half2float(*reinterpret_cast<const __half*>(y + 2 * d))
                   : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(y + 2 * d));
+#pragma unroll 1
       for (int k = 0; k < C; k += 8) {
         tm_load(tm_o + u * N + k, v);
+#pragma unroll
         for (int n = 0; n < 8; ++n)
           if (ctl.part[0][k0 + k + n] != 0.f) v[n] += ctl.part[0][k0 + k + n] * e;
         tm_store(tm_o + u * N + k, v);
@@ -740,10 +809,12 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
     }
     named_sync(1, kSoftThreads);
   }
+#pragma unroll 1
   for (int u = 0; u < pl.units; ++u) {
     warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
     if (odd && tid < kTile) {
       uint8_t* at = sm + pl.off_v + vr.slot * kUnit + r * 128;
+#pragma unroll 1
       for (int k = 0; k < 8; ++k) {
         *reinterpret_cast<uint4*>(at + 16 * k) = make_uint4(0, 0, 0, 0);
         *reinterpret_cast<uint4*>(at + kChunk + 16 * k) = make_uint4(0, 0, 0, 0);
@@ -798,10 +869,14 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
   uint32_t sphase = 0, ophase = 0;
   auto larger = [](float a, float b) { return fmaxf(a, b); };
   auto sum = [](float a, float b) { return a + b; };
-  Segment s;
-  for (Walk w = first_of(P); next_segment<N>(P, w, s);) {
+  Ring seg;
+#pragma unroll 1
+  for (;;) {
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
+    const Segment& s = ctl.seg[seg.slot];
     const AttendItem& it = s.it;
-    named_sync(1, kSoftThreads);  // the previous segment's column tables are read
+    // the previous segment's column tables are read; all leave together
+    if (named_or(1, kSoftThreads, ctl.gave_up) || !s.cols) break;
     if (tid == 0) ctl.o_begun = 0;
     if (tid < N) {
       const bool on = tid < s.cols;
@@ -821,6 +896,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
     // rows [all_lo, all_hi) are visible to every column
     int32_t all_lo = 0, all_hi = INT32_MAX;
     if (!it.loc) {
+#pragma unroll 1
       for (int k = 0; k < s.cols; ++k) {
         all_lo = max(all_lo, ctl.col_lo[k]);
         all_hi = min(all_hi, ctl.col_hi[k]);
@@ -830,6 +906,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
 #pragma unroll
     for (int k = 0; k < C; ++k) l[k] = 0.f;
 
+#pragma unroll 1
     for (int tile = s.v0; tile < s.v1; ++tile) {
       const int32_t j = tile * kTile + r;
       warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, &ctl.gave_up);
@@ -884,7 +961,9 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
           for (int k = 0; k < C; ++k) l[k] *= ctl.fac[k0 + k];
           // products of the tiles before are complete: they were issued
           // before this tile's scores
+#pragma unroll 1
           for (int u = 0; u < pl.units; ++u)
+#pragma unroll 1
             for (int k = 0; k < C; k += 8) {
               float v[8];
               tm_load(tm_o + u * N + k, v);
@@ -904,6 +983,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
         if (named_or(1, kSoftThreads, odd))
           odd_rows<N>(P, sm, ctl, tid, odd, value, vr, tile * kTile, tile == s.v0);
       }
+#pragma unroll 1
       for (int u = 0; u < pl.units; ++u) vr.next(pl.vslots);
       // weights: half of a row of N in the swizzled layout
 #pragma unroll
@@ -973,6 +1053,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       tc_after();
     }
     const bool quads = wide && !((uintptr_t)it.out & 7);
+#pragma unroll 1
     for (int u = 0; u < pl.units; ++u) {
       // after the exchange lane i of four has column k + i of four elements
       const int d = u * 128 + quarter * 32 + (lane & ~3);
@@ -1029,6 +1110,9 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       __syncwarp();
       if (lane == 0) bar_arrive(smem_u32(&ctl.oempty));
     }
+    __syncwarp();
+    if (lane == 0) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
+    seg.next(kSegments);
   }
 }
 
@@ -1040,6 +1124,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Control& ctl = *reinterpret_cast<Control*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
+  // Each warp touches one line of the launch's parameters: their misses, one
+  // after the other in any one warp, then overlap.
+  static_assert(offsetof(AttendParams<MAXI>, first) <= kThreads / 32 * 64, "lines to touch");
+  asm volatile("" ::"r"(reinterpret_cast<const int32_t*>(&P)[warp * 16]));
   if (warp == kThreads / 32 - 1) {
 #pragma unroll
     for (int k = 0; k < kBarriers; k += 32) {
@@ -1048,7 +1136,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool soft = i == kBarPfull || i == kBarOempty || i == kBarRempty || i == kBarRempty + 1;
       const bool rows = i == kBarRfull || i == kBarRfull + 1;
       bar_init(smem_u32(&ctl.kfull[0]) + 8 * i,
-               full ? kLoadThreads : soft ? kSoftThreads / 32 : rows ? kTile : 1);
+               full ? kLoadThreads : soft ? kSoftThreads / 32 : rows ? kTile
+               : i >= kBarSegempty && i < kBarSegempty + kSegments ? kSoftThreads / 32 + 1 : 1);
     }
     ctl.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1086,7 +1175,6 @@ constexpr int kMergeWarps = 16;
 constexpr int kMergeElems = 128;  // value elements of a warp: a float4 a lane
 
 struct MergeParams {
-  int32_t blocks;     // of the attention's grid
   int32_t groups;     // warps that share one column's parts: 1, 4 or 16
   uint8_t cut[kAttendMaxBlocks];  // per split job: the first block that begins inside it
 };
@@ -1103,12 +1191,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   __shared__ float4 sums[kMergeWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b0 = M.cut[blockIdx.x] - 1;
-  const int32_t t = first_tile(c.n_tiles, c.waved, M.blocks, b0 + 1);
+  const int32_t t = first_tile(c, b0 + 1);
   const Segment s = segment_at<N>(P, t, t + 1);
-  // the block that holds the job's last tile: the largest b with
-  // first_tile(b) <= last
-  const int64_t last = (int64_t)(t - s.t0) + s.tiles - 1;
-  const int n = (int)(((last + 1 - c.waved) * M.blocks - 1) / (c.n_tiles - c.waved)) - b0 + 1;
+  // the block that holds the job's last tile
+  const int32_t last = t - s.t0 + s.tiles - 1 - c.waved, more = c.extra * (c.share + 1);
+  const int n = (last < more ? last / (c.share + 1) : c.extra + (last - more) / c.share) - b0 + 1;
   const int spans = (c.dv + kMergeElems - 1) / kMergeElems;
   const int pair = blockIdx.y * (kMergeWarps / M.groups) + warp / M.groups;
   const int col = pair / spans, d = pair % spans * kMergeElems + lane * 4;
@@ -1243,9 +1330,6 @@ struct Shape {
   int n;            // columns of a block
   int64_t tiles;
   int blocks;
-  int waves;        // whole jobs that every block takes first, one at a time
-  int64_t waved;    // tiles of them all
-  int64_t job_tiles;
   int n_cut;        // jobs cut by a block's boundary
   int parts;        // of the longest job, about
   MergeParams merge;
@@ -1257,22 +1341,24 @@ int columns_of(const AttendCommon& c, const AttendItem& it, int most) {
   return (all + blk - 1) / blk;
 }
 
-// Fills in every item's tiles.
-Shape shape_of(const AttendCommon& c, AttendItem* items, int n_items, int sms) {
+// Fills in every item's tiles, and how the blocks share them.
+Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms) {
   Shape s{};
   const int most = widest_block(c);
   int widest = 1;
   int64_t n_jobs = 0, longest = 0, shortest = INT64_MAX;
   for (int i = 0; i < n_items; ++i) widest = std::max(widest, columns_of(c, items[i], most));
   s.n = (widest + 15) / 16 * 16;
-  const int kv = c.heads / c.group;
+  c.kv = c.heads / c.group;
   for (int i = 0; i < n_items; ++i) {
     AttendItem& it = items[i];
     it.tile0 = (int32_t)std::min<int64_t>(s.tiles, INT32_MAX);
     // an item without rows still has one tile, that writes its empty outputs
     it.tiles = (int32_t)std::max<int64_t>(1, (it.len + kTile - 1) / kTile);
     const int64_t all = it.loc ? c.group : (int64_t)it.Q * c.group;
-    const int64_t jobs = (it.loc ? it.Q : 1) * (int64_t)kv * ((all + s.n - 1) / s.n);
+    it.blocks = (int32_t)((all + s.n - 1) / s.n);
+    it.width = it.blocks ? (int32_t)((all + it.blocks - 1) / it.blocks) : 0;
+    const int64_t jobs = (it.loc ? it.Q : 1) * (int64_t)c.kv * it.blocks;
     s.tiles += jobs * it.tiles;
     n_jobs += jobs;
     longest = std::max<int64_t>(longest, it.tiles);
@@ -1280,6 +1366,8 @@ Shape shape_of(const AttendCommon& c, AttendItem* items, int n_items, int sms) {
   }
   sms = std::min(sms, kAttendMaxBlocks);
   s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(sms, s.tiles));
+  c.waves = c.waved = c.job_tiles = c.share = c.extra = 0;
+  if (s.tiles > INT32_MAX) return s;  // refused
   // Jobs of equal length: whole ones in waves over the blocks (64 verify
   // blocks of 8 queries, whose rows are mostly the same: XXX), fewer blocks if
   // that leaves nothing to split and no block with more to do.
@@ -1287,19 +1375,20 @@ Shape shape_of(const AttendCommon& c, AttendItem* items, int n_items, int sms) {
     const int64_t each = (n_jobs + sms - 1) / sms;
     if (n_jobs % each == 0 && each * longest <= (s.tiles + s.blocks - 1) / s.blocks)
       s.blocks = (int)(n_jobs / each);
-    s.waves = (int)(n_jobs / s.blocks);
-    s.job_tiles = longest;
-    s.waved = s.waves * s.blocks * longest;
+    c.waves = (int)(n_jobs / s.blocks);
+    c.job_tiles = (int32_t)longest;
+    c.waved = (int32_t)(c.waves * s.blocks * longest);
   }
-  const int64_t rest = s.tiles - s.waved;  // dealt out evenly, cut where it falls
+  const int64_t rest = s.tiles - c.waved;  // dealt out evenly, cut where it falls
+  c.share = (int32_t)(rest / s.blocks);
+  c.extra = (int32_t)(rest % s.blocks);
   s.parts = rest ? (int)std::min<int64_t>(s.blocks, longest * s.blocks / rest + 2) : 0;
-  s.merge.blocks = s.blocks;
   s.merge.groups = s.parts > 24 ? 16 : s.parts > 4 ? 4 : 1;
-  if (s.tiles <= INT32_MAX && rest) {
+  if (rest) {
     int k = 0;
     int64_t cut_job = -1;  // first tile of the job cut last
     for (int b = 1; b < s.blocks; ++b) {
-      const int32_t t = first_tile(s.tiles, (int32_t)s.waved, s.blocks, b);
+      const int32_t t = first_tile(c, b);
       while (k + 1 < n_items && items[k + 1].tile0 <= t) ++k;
       const int32_t in = (t - items[k].tile0) % items[k].tiles;
       if (in == 0 || t - in == cut_job || t >= s.tiles) continue;
@@ -1335,11 +1424,8 @@ cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items
   AttendParams<MAXI> P;
   P.c = c;
   P.c.n_items = n_items;
-  P.c.n_tiles = (int32_t)s.tiles;
-  P.c.waves = s.waves;
-  P.c.waved = (int32_t)s.waved;
-  P.c.job_tiles = (int32_t)s.job_tiles;
   P.plan = make_plan(c, s.n);
+  for (int i = 0; i < MAXI; ++i) P.first[i] = i < n_items ? items[i].tile0 : INT32_MAX;
   for (int i = 0; i < n_items; ++i) P.items[i] = items[i];
   switch (s.n) {
     case 16: return launch_n<16, MAXI>(P, s, parts, stream);
@@ -1366,13 +1452,13 @@ cudaError_t attend_set_smem_limit() {
   return cudaSuccess;
 }
 
-bool attend_shape(const AttendCommon& c, AttendItem* items, int n_items, int sms, size_t* bytes) {
+bool attend_shape(AttendCommon c, AttendItem* items, int n_items, int sms, size_t* bytes) {
   const Shape s = shape_of(c, items, n_items, sms);
   *bytes = s.n_cut ? (size_t)2 * s.blocks * s.n * (c.dv + 2) * sizeof(float) : 0;
   return s.tiles <= INT32_MAX;
 }
 
-cudaError_t launch_attend(const AttendCommon& c, AttendItem* items, int n_items, int sms,
+cudaError_t launch_attend(AttendCommon c, AttendItem* items, int n_items, int sms,
                           void* work, cudaStream_t stream) {
   if (n_items <= 0) return cudaSuccess;
   if (n_items > kAttendItemsLarge) return cudaErrorInvalidValue;

@@ -291,7 +291,7 @@ cudaError_t gather_set_smem_limit(int row_bytes, int optin, bool* tma_ok);
 constexpr int kAttendItemsLarge = 240, kAttendItemsSmall = 16;
 constexpr int kAttendMaxKey = 576, kAttendMaxValue = 512;
 
-struct AttendItem {
+struct alignas(16) AttendItem {
   const uint8_t* q;
   const uint32_t* loc;    // located items, else null
   const int32_t* index;   // union positions, or null
@@ -305,6 +305,7 @@ struct AttendItem {
   int32_t Q;
   int32_t tiles;          // tiles of each of its jobs
   int32_t tile0;          // first tile of this item in the launch
+  int32_t blocks, width;  // a query's (history: the item's) columns: blocks of them, columns of a block
 };
 
 struct AttendCommon {
@@ -315,10 +316,12 @@ struct AttendCommon {
   uint32_t tail_rows, opt_rows, hot_rows;  // arena sizes in rows
   int32_t row_bytes, T, Pmax, page_shift;
   uint32_t* status;
-  int32_t n_items, n_tiles;
+  int32_t n_items;
   int32_t waves, waved, job_tiles;  // whole jobs dealt out first (launch_attend)
+  int32_t share, extra;   // tiles of a block after that, and blocks that have one more
   int32_t f16;            // rows are f16, else bf16
   int32_t heads, group;   // query heads, query heads per kv head
+  int32_t kv;             // kv heads
   int32_t dk, dv;         // elements of a key and of a value
   int32_t key_off, val_off, key_stride, val_stride;  // bytes within a row
   float scale;
@@ -330,8 +333,8 @@ constexpr int kAttendMaxBlocks = 256;
 // Once per device: let the attention's blocks use all of an SM's shared memory.
 cudaError_t attend_set_smem_limit();
 // Workspace of a launch; fills in the items' tiles.  False: too many tiles.
-bool attend_shape(const AttendCommon& c, AttendItem* items, int n_items, int sms, size_t* bytes);
-cudaError_t launch_attend(const AttendCommon& c, AttendItem* items, int n_items, int sms,
+bool attend_shape(AttendCommon c, AttendItem* items, int n_items, int sms, size_t* bytes);
+cudaError_t launch_attend(AttendCommon c, AttendItem* items, int n_items, int sms,
                           void* work, cudaStream_t stream);
 
 // ------------------------------------------------------------ forks
