@@ -40,11 +40,12 @@ namespace {
 
 constexpr int kTile = 128;                 // rows per tile
 constexpr int kSoftThreads = 256, kLoadThreads = 128;
-constexpr int kThreads = kSoftThreads + kLoadThreads + 32;
+constexpr int kIssueWarp = (kSoftThreads + kLoadThreads) / 32, kFindWarp = kIssueWarp + 1;
+constexpr int kThreads = 32 * (kFindWarp + 1);
 constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk of a tile
 constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
-constexpr int kSegments = 4;               // segments from the loading warps to the others
+constexpr int kSegments = 4;               // segments found ahead
 constexpr float kSlack = 8.f;              // log2 units
 constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
 
@@ -435,7 +436,7 @@ struct Control {
   uint64_t qfull, qempty, sfull, pfull, ofull, oempty, rfull[2], rempty[2], drain;
   uint64_t segfull[kSegments], segempty[kSegments];
   uint64_t unused[5];  // to 64: two barriers a lane
-  Segment seg[kSegments];  // found by the loading warps, for the others
+  Segment seg[kSegments];  // from the finding warp to the others
   const uint8_t* row[2][kTile];
   int64_t out_off[64];
   int32_t lse_at[64];
@@ -490,22 +491,13 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
   };
   const int piece = tid & 7, r0 = tid >> 3;  // rows r0 + 16 i
   bool first = true;
-  Segment s;
   Ring seg;
-  bool more = true;
 #pragma unroll 1
-  for (Walk w = first_of(P); more;) {
-    more = next_segment<N>(P, w, s);
-    if (tid < 32) {  // one without columns ends the walk of the other warps
-      wait_empty(smem_u32(&ctl.segempty[seg.slot]), seg.phase ^ 1);
-      if (!more) s.cols = 0;
-      if (tid == 0) {
-        ctl.seg[seg.slot] = s;
-        bar_arrive(smem_u32(&ctl.segfull[seg.slot]));
-      }
-      seg.next(kSegments);
-    }
-    if (!more || s.v0 >= s.v1) continue;
+  for (;;) {
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
+    const Segment s = ctl.seg[seg.slot];  // in registers: read several times a tile
+    if (named_or(2, kLoadThreads, ctl.gave_up) || !s.cols) break;  // all leave together
+    const int32_t v0 = s.v0, v1 = s.v1;
     const AttendItem& it = s.it;
     // Queries: [chunk][column][128 B], zeros past the key and the columns.
     // Loaded behind the first tile's key chunks: the segment before may still
@@ -552,11 +544,11 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     const uint32_t key_at = c.key_off + s.g * c.key_stride;
     const uint32_t val_at = c.val_off + s.g * c.val_stride;
     static_assert(kLoadThreads == kTile, "one row address per loading thread");
-    int64_t j = (int64_t)s.v0 * kTile + tid;  // this thread's row of the tile
+    int64_t j = (int64_t)v0 * kTile + tid;  // this thread's row of the tile
     uint32_t word = row_word(c, s, j, row_index(s, j));
     int32_t index = row_index(s, j + kTile);
 #pragma unroll 1
-    for (int tile = s.v0; tile < s.v1; ++tile) {
+    for (int tile = v0; tile < v1; ++tile) {
       // the tile's row addresses, to every loading thread and the softmax
       wait_empty(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1);
       ctl.row[rr.slot][tid] = row_of(c, s, j, word);
@@ -591,7 +583,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
       for (int i = 0; i < items; ++i) {
         const bool key = pl.alias ? i >= pl.units : i < pl.only_chunks;
         // a slot that this tile itself has to free needs the queries
-        if (tile == s.v0 && i == (pl.alias ? 0 : min(pl.kslots, pl.only_chunks))) load_queries();
+        if (tile == v0 && i == (pl.alias ? 0 : min(pl.kslots, pl.only_chunks))) load_queries();
         if (key) {
           wait_empty(smem_u32(&ctl.kempty[kr.slot]), kr.phase ^ 1);
           chunk(base + pl.off_k + kr.slot * kChunk, key_at, (c0 + (pl.alias ? 0 : i)) * 64, c.dk);
@@ -608,8 +600,34 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
         }
       }
     }
+    __syncwarp();
+    if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
+    seg.next(kSegments);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Finding warp: the block's segments, ahead of the others, who read them from
+// shared memory.  One without columns ends the walk.  The first one is found
+// while the block sets up.
+template <int N, int MAXI>
+__device__ void find_segments(const AttendParams<MAXI>& P, Control& ctl) {
+  Ring seg;
+  Walk w = first_of(P);
+  bool more = true;
+#pragma unroll 1
+  for (bool begin = true; more; begin = false) {
+    Segment s;
+    more = next_segment<N>(P, w, s);
+    if (begin) __syncthreads();
+    if (!more) s.cols = 0;
+    warp_wait(smem_u32(&ctl.segempty[seg.slot]), seg.phase ^ 1, &ctl.gave_up);
+    if (elected()) {
+      ctl.seg[seg.slot] = s;
+      bar_arrive(smem_u32(&ctl.segfull[seg.slot]));
+    }
+    seg.next(kSegments);
+  }
 }
 
 // Issuing warp: all its lanes walk the same path, one of them issues.
@@ -1128,7 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // after the other in any one warp, then overlap.
   static_assert(offsetof(AttendParams<MAXI>, first) <= kThreads / 32 * 64, "lines to touch");
   asm volatile("" ::"r"(reinterpret_cast<const int32_t*>(&P)[warp * 16]));
-  if (warp == kThreads / 32 - 1) {
+  if (warp == kIssueWarp) {
 #pragma unroll
     for (int k = 0; k < kBarriers; k += 32) {
       const int i = k + (tid & 31);
@@ -1137,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool rows = i == kBarRfull || i == kBarRfull + 1;
       bar_init(smem_u32(&ctl.kfull[0]) + 8 * i,
                full ? kLoadThreads : soft ? kSoftThreads / 32 : rows ? kTile
-               : i >= kBarSegempty && i < kBarSegempty + kSegments ? kSoftThreads / 32 + 1 : 1);
+               : i >= kBarSegempty && i < kBarSegempty + kSegments ? kFindWarp : 1);
     }
     ctl.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1148,21 +1166,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  tc_before();
-  __syncthreads();
-  tc_after();
-  if (warp < kSoftThreads / 32) {
-    softmax_rows<N>(P, sm, ctl, tid, parts);
-  } else if (warp < (kSoftThreads + kLoadThreads) / 32) {
-    load_rows<N>(P, sm, ctl, tid - kSoftThreads);
+  if (warp == kFindWarp) {
+    find_segments<N>(P, ctl);  // meets the others' barrier inside
   } else {
-    issue_products<N>(P, sm, ctl);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp < kSoftThreads / 32) softmax_rows<N>(P, sm, ctl, tid, parts);
+    else if (warp < kIssueWarp) load_rows<N>(P, sm, ctl, tid - kSoftThreads);
+    else issue_products<N>(P, sm, ctl);
   }
   __syncwarp();
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == kThreads / 32 - 1)
+  if (warp == kIssueWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl.tmem),
                  "r"(tmem_columns(N))
                  : "memory");
