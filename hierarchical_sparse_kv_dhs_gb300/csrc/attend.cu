@@ -41,11 +41,13 @@ namespace {
 constexpr int kTile = 128;                 // rows per tile
 constexpr int kSoftThreads = 256, kLoadThreads = 128;
 constexpr int kIssueWarp = (kSoftThreads + kLoadThreads) / 32, kFindWarp = kIssueWarp + 1;
-constexpr int kThreads = 32 * (kFindWarp + 1);
+constexpr int kRowWarp = kFindWarp + 1, kRowThreads = 64;
+constexpr int kThreads = 32 * kRowWarp + kRowThreads;
 constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk of a tile
 constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
 constexpr int kSegments = 4;               // segments found ahead
+constexpr int kRowSlots = 2;               // tiles whose row addresses are found ahead
 constexpr float kSlack = 8.f;              // log2 units
 constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
 
@@ -431,13 +433,14 @@ __device__ __forceinline__ const uint8_t* row_of(const AttendCommon& c, const Se
 
 // ------------------------------------------------------------------ kernel
 
+constexpr int kUnusedBars = 9 - 2 * kRowSlots;
 struct Control {
   uint64_t kfull[kMaxK], kempty[kMaxK], vfull[kMaxV], vempty[kMaxV];
-  uint64_t qfull, qempty, sfull, pfull, ofull, oempty, rfull[2], rempty[2], drain;
+  uint64_t qfull, qempty, sfull, pfull, ofull, oempty, rfull[kRowSlots], rempty[kRowSlots], drain;
   uint64_t segfull[kSegments], segempty[kSegments];
-  uint64_t unused[5];  // to 64: two barriers a lane
+  uint64_t unused[kUnusedBars];  // to 64: two barriers a lane
   Segment seg[kSegments];  // from the finding warp to the others
-  const uint8_t* row[2][kTile];
+  const uint8_t* row[kRowSlots][kTile];
   int64_t out_off[64];
   int32_t lse_at[64];
   int32_t col_lo[64], col_hi[64];
@@ -451,10 +454,10 @@ struct Control {
 };
 // Places of the single barriers in Control's order
 constexpr int kBarQfull = 2 * kMaxK + 2 * kMaxV, kBarPfull = kBarQfull + 3,
-              kBarOempty = kBarQfull + 5, kBarRfull = kBarQfull + 6, kBarRempty = kBarQfull + 8,
-              kBarDrain = kBarQfull + 10, 
+              kBarOempty = kBarQfull + 5, kBarRfull = kBarQfull + 6,
+              kBarRempty = kBarRfull + kRowSlots, kBarDrain = kBarRempty + kRowSlots,
               kBarSegempty = kBarDrain + 1 + kSegments, kBarriers = 64;
-static_assert(kBarSegempty + kSegments + 5 == kBarriers, "barrier table");
+static_assert(kBarSegempty + kSegments + kUnusedBars == kBarriers, "barrier table");
 constexpr uint32_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
 
 // Parity bookkeeping of a ring of slots.
@@ -495,8 +498,8 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
 #pragma unroll 1
   for (;;) {
     warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
-    const Segment s = ctl.seg[seg.slot];  // in registers: read several times a tile
-    if (named_or(2, kLoadThreads, ctl.gave_up) || !s.cols) break;  // all leave together
+    const Segment& s = ctl.seg[seg.slot];
+    if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
     const int32_t v0 = s.v0, v1 = s.v1;
     const AttendItem& it = s.it;
     // Queries: [chunk][column][128 B], zeros past the key and the columns.
@@ -543,24 +546,15 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
 
     const uint32_t key_at = c.key_off + s.g * c.key_stride;
     const uint32_t val_at = c.val_off + s.g * c.val_stride;
-    static_assert(kLoadThreads == kTile, "one row address per loading thread");
-    int64_t j = (int64_t)v0 * kTile + tid;  // this thread's row of the tile
-    uint32_t word = row_word(c, s, j, row_index(s, j));
-    int32_t index = row_index(s, j + kTile);
 #pragma unroll 1
     for (int tile = v0; tile < v1; ++tile) {
-      // the tile's row addresses, to every loading thread and the softmax
-      wait_empty(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1);
-      ctl.row[rr.slot][tid] = row_of(c, s, j, word);
-      j += kTile;
-      word = row_word(c, s, j, index);
-      index = row_index(s, j + kTile);
-      bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
-      named_sync(2, kLoadThreads);
+      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, &ctl.gave_up);
       const uint8_t* row[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = ctl.row[rr.slot][r0 + 16 * i];
-      rr.next(2);
+      __syncwarp();
+      if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
+      rr.next(kRowSlots);
       // one 64-element chunk of the 128 rows: element el.. of a slice of
       // `n` elements at byte `at` of each row
       auto chunk = [&](uint32_t dst, uint32_t at, int el, int n) {
@@ -626,6 +620,51 @@ __device__ void find_segments(const AttendParams<MAXI>& P, Control& ctl) {
       ctl.seg[seg.slot] = s;
       bar_arrive(smem_u32(&ctl.segfull[seg.slot]));
     }
+    seg.next(kSegments);
+  }
+}
+
+// Row warps: the addresses of every tile's rows, ahead of the loading warps.
+template <int N, int MAXI>
+__device__ void find_rows(const AttendParams<MAXI>& P, Control& ctl, int tid) {
+  constexpr int R = kTile / kRowThreads;
+  const AttendCommon& c = P.c;
+  Ring seg, rr;
+#pragma unroll 1
+  for (;;) {
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
+    const Segment s = ctl.seg[seg.slot];
+    if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
+    int64_t j = (int64_t)s.v0 * kTile + tid;
+    uint32_t word[R];
+    int32_t index[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t i = j + k * kRowThreads;
+      index[k] = row_index(s, i);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t i = j + k * kRowThreads;
+      word[k] = row_word(c, s, i, index[k]);
+      index[k] = row_index(s, i + kTile);
+    }
+#pragma unroll 1
+    for (int tile = s.v0; tile < s.v1; ++tile, j += kTile) {
+      warp_wait(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1, &ctl.gave_up);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const int64_t i = j + k * kRowThreads;
+        ctl.row[rr.slot][tid + k * kRowThreads] = row_of(c, s, i, word[k]);
+        word[k] = row_word(c, s, i + kTile, index[k]);
+        index[k] = row_index(s, i + 2 * kTile);
+      }
+      __syncwarp();
+      if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
+      rr.next(kRowSlots);
+    }
+    __syncwarp();
+    if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
     seg.next(kSegments);
   }
 }
@@ -931,7 +970,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       const uint8_t* row = ctl.row[rr.slot][r];
       __syncwarp();
       if (lane == 0) bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
-      rr.next(2);
+      rr.next(kRowSlots);
       const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
       warp_wait(smem_u32(&ctl.sfull), sphase, &ctl.gave_up);
       sphase ^= 1;
@@ -1151,11 +1190,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < kBarriers; k += 32) {
       const int i = k + (tid & 31);
       const bool full = i < kMaxK || (i >= 2 * kMaxK && i < 2 * kMaxK + kMaxV) || i == kBarQfull;
-      const bool soft = i == kBarPfull || i == kBarOempty || i == kBarRempty || i == kBarRempty + 1;
-      const bool rows = i == kBarRfull || i == kBarRfull + 1;
+      const bool soft = i == kBarPfull || i == kBarOempty;
+      const bool rows = i >= kBarRfull && i < kBarRempty;
+      const bool read = i >= kBarRempty && i < kBarDrain;
+      const bool segs = i >= kBarSegempty && i < kBarSegempty + kSegments;
       bar_init(smem_u32(&ctl.kfull[0]) + 8 * i,
-               full ? kLoadThreads : soft ? kSoftThreads / 32 : rows ? kTile
-               : i >= kBarSegempty && i < kBarSegempty + kSegments ? kFindWarp : 1);
+               full ? kLoadThreads : soft ? kSoftThreads / 32 : rows ? kRowThreads / 32
+               : read ? (kSoftThreads + kLoadThreads) / 32 : segs ? kThreads / 32 - 1 : 1);
     }
     ctl.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1174,7 +1215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     if (warp < kSoftThreads / 32) softmax_rows<N>(P, sm, ctl, tid, parts);
     else if (warp < kIssueWarp) load_rows<N>(P, sm, ctl, tid - kSoftThreads);
-    else issue_products<N>(P, sm, ctl);
+    else if (warp == kIssueWarp) issue_products<N>(P, sm, ctl);
+    else find_rows<N>(P, ctl, tid - 32 * kRowWarp);
   }
   __syncwarp();
   tc_before();
