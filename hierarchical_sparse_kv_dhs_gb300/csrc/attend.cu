@@ -32,6 +32,7 @@
 
 #include <algorithm>
 #include <cstddef>
+#include <type_traits>
 
 #include "dhs_internal.h"
 
@@ -58,7 +59,7 @@ struct Plan {
   int32_t only_chunks;   // of them in the key ring (all, unless shared)
   int32_t units;         // value units
   int32_t kslots, vslots;
-  int32_t alias;         // the weights take the key ring's only slot
+  int32_t alias;         // the weights take the key ring's only slot (shared only)
   uint32_t off_q, off_p, off_k, off_v;  // from the aligned shared-memory base
   uint32_t smem;
 };
@@ -433,10 +434,10 @@ __device__ __forceinline__ const uint8_t* row_of(const AttendCommon& c, const Se
 
 // ------------------------------------------------------------------ kernel
 
-constexpr int kUnusedBars = 9 - 2 * kRowSlots;
+constexpr int kUnusedBars = 8 - 2 * kRowSlots;
 struct Control {
   uint64_t kfull[kMaxK], kempty[kMaxK], vfull[kMaxV], vempty[kMaxV];
-  uint64_t qfull, qempty, sfull, pfull, ofull, oempty, rfull[kRowSlots], rempty[kRowSlots], drain;
+  uint64_t qfull, qempty, sfull[2], pfull, odone, oempty, rfull[kRowSlots], rempty[kRowSlots], drain;
   uint64_t segfull[kSegments], segempty[kSegments];
   uint64_t unused[kUnusedBars];  // to 64: two barriers a lane
   Segment seg[kSegments];  // from the finding warp to the others
@@ -453,8 +454,8 @@ struct Control {
   volatile uint32_t gave_up;
 };
 // Places of the single barriers in Control's order
-constexpr int kBarQfull = 2 * kMaxK + 2 * kMaxV, kBarPfull = kBarQfull + 3,
-              kBarOempty = kBarQfull + 5, kBarRfull = kBarQfull + 6,
+constexpr int kBarQfull = 2 * kMaxK + 2 * kMaxV, kBarPfull = kBarQfull + 4,
+              kBarOempty = kBarQfull + 6, kBarRfull = kBarQfull + 7,
               kBarRempty = kBarRfull + kRowSlots, kBarDrain = kBarRempty + kRowSlots,
               kBarSegempty = kBarDrain + 1 + kSegments, kBarriers = 64;
 static_assert(kBarSegempty + kSegments + kUnusedBars == kBarriers, "barrier table");
@@ -472,16 +473,17 @@ struct Ring {
   }
 };
 
-__host__ __device__ constexpr uint32_t tmem_columns(int n) { return 5 * n <= 128 ? 128 : 5 * n <= 256 ? 256 : 512; }
+__host__ __device__ constexpr uint32_t tmem_columns(int n) { return 6 * n <= 128 ? 128 : 6 * n <= 256 ? 256 : 512; }
 // Bytes of one row of weights, the swizzle of that row width, and its 8-row stride.
 __host__ __device__ constexpr int weight_row(int n) { return n <= 16 ? 32 : n <= 32 ? 64 : 128; }
 __host__ __device__ constexpr uint32_t weight_swizzle(int n) { return n <= 16 ? 6 : n <= 32 ? 4 : 2; }
 
 // Loading warps: queries once per segment, rows tile by tile.
-template <int N, int MAXI>
+template <int N, bool SHARED, int MAXI>
 __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid) {
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
+  const bool alias = SHARED && pl.alias;
   const uint32_t base = smem_u32(sm);
   Ring kr, vr, rr;
   uint32_t qphase = 0;
@@ -575,17 +577,17 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
       const int c0 = pl.key_chunks - pl.only_chunks, items = pl.only_chunks + pl.units;
 #pragma unroll 1
       for (int i = 0; i < items; ++i) {
-        const bool key = pl.alias ? i >= pl.units : i < pl.only_chunks;
+        const bool key = alias ? i >= pl.units : i < pl.only_chunks;
         // a slot that this tile itself has to free needs the queries
-        if (tile == v0 && i == (pl.alias ? 0 : min(pl.kslots, pl.only_chunks))) load_queries();
+        if (tile == v0 && i == (alias ? 0 : min(pl.kslots, pl.only_chunks))) load_queries();
         if (key) {
           wait_empty(smem_u32(&ctl.kempty[kr.slot]), kr.phase ^ 1);
-          chunk(base + pl.off_k + kr.slot * kChunk, key_at, (c0 + (pl.alias ? 0 : i)) * 64, c.dk);
+          chunk(base + pl.off_k + kr.slot * kChunk, key_at, (c0 + (alias ? 0 : i)) * 64, c.dk);
           launch(smem_u32(&ctl.kfull[kr.slot]));
           kr.next(pl.kslots);
         } else {
-          const int el = (pl.alias ? i : i - pl.only_chunks) * 128, n = pl.shared ? c.dk : c.dv;
-          const uint32_t at = pl.shared ? key_at : val_at, dst = base + pl.off_v + vr.slot * kUnit;
+          const int el = (alias ? i : i - pl.only_chunks) * 128, n = SHARED ? c.dk : c.dv;
+          const uint32_t at = SHARED ? key_at : val_at, dst = base + pl.off_v + vr.slot * kUnit;
           wait_empty(smem_u32(&ctl.vempty[vr.slot]), vr.phase ^ 1);
           chunk(dst, at, el, n);
           if (el + 64 < n) chunk(dst + kChunk, at, el + 64, n);
@@ -670,12 +672,13 @@ __device__ void find_rows(const AttendParams<MAXI>& P, Control& ctl, int tid) {
 }
 
 // Issuing warp: all its lanes walk the same path, one of them issues.
-template <int N, int MAXI>
+template <int N, bool SHARED, int MAXI>
 __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl) {
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
+  const bool alias = SHARED && pl.alias;
   const uint32_t base = smem_u32(sm);
-  const uint32_t tm_s = ctl.tmem, tm_o = ctl.tmem + N;
+  const uint32_t tm_s = ctl.tmem, tm_o = ctl.tmem + 2 * N;
   const uint32_t type = c.f16 ? 0u : 1u;
   // float accumulator, operand types, N, M = 128; the second product's
   // operands are both M/N-major
@@ -684,23 +687,23 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
   constexpr uint32_t psbo = 8 * weight_row(N);
   constexpr uint32_t hi = operand_hi(1024, 2), hi_p = operand_hi(psbo, weight_swizzle(N));
   const uint32_t q_lo = operand_lo(base + pl.off_q, 16);
-  const uint32_t p_lo = operand_lo(base + (pl.alias ? pl.off_k : pl.off_p), 16);
+  const uint32_t p_lo = operand_lo(base + (alias ? pl.off_k : pl.off_p), 16);
   const uint32_t k_lo = operand_lo(base + pl.off_k, 16);
   const uint32_t v_lo = operand_lo(base + pl.off_v, 16), vt_lo = operand_lo(base + pl.off_v, kChunk);
   const bool lead = elected();
   const int c0 = pl.key_chunks - pl.only_chunks;
   const int last_steps = (c.dk - (pl.key_chunks - 1) * 64 + 15) / 16;
-  Ring kr, vr;
-  uint32_t qphase = 0, pphase = 0, ophase = 0;
+  Ring kr, vs, vr;  // key slots; value slots of the scores and of the sums
+  uint32_t qphase = 0, pphase = 0, ophase = 0, n_scores = 0;
   bool first = true;
   // the products of key chunk `ch` staged at `at`
-  auto scores = [&](uint32_t at, int ch, bool add) {
+  auto chunk = [&](uint32_t d, uint32_t at, int ch, bool add) {
     const uint32_t b = q_lo + ch * (N * 128 >> 4);
     const int steps = ch + 1 < pl.key_chunks ? 4 : last_steps;
     if (!lead) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k < steps) mma(tm_s, at + 2 * k, hi, b + 2 * k, hi, id1, add || k > 0);
+      if (k < steps) mma(d, at + 2 * k, hi, b + 2 * k, hi, id1, add || k > 0);
   };
   Ring seg;
 #pragma unroll 1
@@ -716,38 +719,43 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
     warp_wait(smem_u32(&ctl.qfull), qphase, &ctl.gave_up);
     fence_async();
     qphase ^= 1;
+    int next = v0;  // the tile whose scores are next
 #pragma unroll 1
     for (int tile = v0; tile < v1; ++tile) {
-      const int kslot = kr.slot;
-      auto keys = [&](bool add) {
+      const int last = SHARED ? tile : min(tile + 1, v1 - 1);
 #pragma unroll 1
-        for (int k = 0; k < pl.only_chunks; ++k) {
-          warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
-          fence_async();
-          tc_after();
-          scores(k_lo + kr.slot * (kChunk >> 4), c0 + k, add || k > 0);
-          if (lead && !pl.alias) commit(smem_u32(&ctl.kempty[kr.slot]));
-          kr.next(pl.kslots);
-        }
-      };
-      if (!pl.alias) keys(false);
-      Ring v = vr;
-      if (pl.shared) {
+      for (; next <= last; ++next) {
+        const uint32_t buf = SHARED ? 0 : n_scores & 1, d = tm_s + buf * N;
+        auto keys = [&](bool add) {
 #pragma unroll 1
-        for (int u = 0; u < pl.units; ++u) {
-          warp_wait(smem_u32(&ctl.vfull[v.slot]), v.phase, &ctl.gave_up);
-          fence_async();
-          tc_after();
-          const uint32_t at = v_lo + v.slot * (kUnit >> 4);
-          scores(at, 2 * u, (pl.only_chunks > 0 && !pl.alias) || u > 0);
-          if (2 * u + 1 < pl.key_chunks) scores(at + (kChunk >> 4), 2 * u + 1, true);
-          v.next(pl.vslots);
+          for (int k = 0; k < pl.only_chunks; ++k) {
+            warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
+            fence_async();
+            tc_after();
+            chunk(d, k_lo + kr.slot * (kChunk >> 4), c0 + k, add || k > 0);
+            if (lead && !alias) commit(smem_u32(&ctl.kempty[kr.slot]));
+            kr.next(pl.kslots);
+          }
+        };
+        if (!alias) keys(false);
+        if (SHARED) {
+#pragma unroll 1
+          for (int u = 0; u < pl.units; ++u) {
+            warp_wait(smem_u32(&ctl.vfull[vs.slot]), vs.phase, &ctl.gave_up);
+            fence_async();
+            tc_after();
+            const uint32_t at = v_lo + vs.slot * (kUnit >> 4);
+            chunk(d, at, 2 * u, (pl.only_chunks > 0 && !alias) || u > 0);
+            if (2 * u + 1 < pl.key_chunks) chunk(d, at + (kChunk >> 4), 2 * u + 1, true);
+            vs.next(pl.vslots);
+          }
         }
-      }
-      if (pl.alias) keys(true);
-      if (lead) {
-        commit(smem_u32(&ctl.sfull));
-        if (tile + 1 == v1) commit(smem_u32(&ctl.qempty));
+        if (alias) keys(true);
+        if (lead) {
+          commit(smem_u32(&ctl.sfull[buf]));
+          if (next + 1 == v1) commit(smem_u32(&ctl.qempty));
+        }
+        ++n_scores;
       }
       warp_wait(smem_u32(&ctl.pfull), pphase, &ctl.gave_up);
       pphase ^= 1;
@@ -759,7 +767,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
       const bool begun = tile > v0 || *(volatile uint32_t*)&ctl.o_begun;
 #pragma unroll 1
       for (int u = 0; u < pl.units; ++u) {
-        if (!pl.shared) {
+        if (!SHARED) {
           warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
           fence_async();
           tc_after();
@@ -775,8 +783,8 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
         vr.next(pl.vslots);
       }
       if (lead) {
-        if (pl.alias) commit(smem_u32(&ctl.kempty[kslot]));
-        if (tile + 1 == v1) commit(smem_u32(&ctl.ofull));
+        if (alias) commit(smem_u32(&ctl.kempty[0]));
+        if (!SHARED || tile + 1 == v1) commit(smem_u32(&ctl.odone));
       }
     }
     first = false;
@@ -809,12 +817,12 @@ __device__ bool finite_row(const uint8_t* p, int n, int f16) {
 template <int N, int MAXI>
 __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl,
                                       int tid, bool odd, const uint8_t* value, Ring vr,
-                                      int32_t tile0, bool first) {
+                                      int32_t tile0, bool first, uint32_t tm_scores) {
   constexpr int C = N / 2;
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
   const int r = tid & (kTile - 1), k0 = tid / kTile * C;
-  const uint32_t tm_s = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0, tm_o = tm_s + N;
+  const uint32_t tm_o = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0 + 2 * N;
   const float scale = c.scale * 1.44269504088896341f;
   const uint32_t marked = __ballot_sync(~0u, odd);
   if ((tid & 31) == 0 && tid < kTile) ctl.odd[tid >> 5] = marked;
@@ -835,7 +843,7 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
     if ((r >> 5) == (i >> 5)) {  // the warps that own the row
 #pragma unroll 1
       for (int k = 0; k < C; k += 8) {
-        tm_load(tm_s + k, v);
+        tm_load(tm_scores + k, v);
         if (r == i)
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
@@ -910,20 +918,21 @@ __device__ __forceinline__ void transpose4(float* v, int lane) {
 
 // Softmax warps: a thread has one row of the tile and half of the columns;
 // then the segment's output.
-template <int N, int MAXI>
+template <int N, bool SHARED, int MAXI>
 __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid,
                              float* parts) {
   constexpr int C = N / 2;
   const AttendCommon& c = P.c;
   const Plan& pl = P.plan;
+  const bool alias = SHARED && pl.alias;
   const int lane = tid & 31, r = tid & (kTile - 1), quarter = r >> 5, k0 = tid / kTile * C;
-  const uint32_t tm_s = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0, tm_o = tm_s + N;
+  const uint32_t tm_s = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0, tm_o = tm_s + 2 * N;
   const float scale = c.scale * 1.44269504088896341f;  // log2 e
-  uint8_t* const weights = sm + (pl.alias ? pl.off_k : pl.off_p) + r * weight_row(N);
+  uint8_t* const weights = sm + (alias ? pl.off_k : pl.off_p) + r * weight_row(N);
   const bool wide = !(((uintptr_t)c.o_qs | c.o_hs) & 7);  // outputs store four elements at once
   const int turn = weight_row(N) == 32 ? (r >> 2) & 1 : weight_row(N) == 64 ? (r >> 1) & 3 : r & 7;
   Ring rr, vr;
-  uint32_t sphase = 0, ophase = 0;
+  uint32_t n_scores = 0, ophase = 0;
   auto larger = [](float a, float b) { return fmaxf(a, b); };
   auto sum = [](float a, float b) { return a + b; };
   Ring seg;
@@ -972,11 +981,22 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       if (lane == 0) bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
       rr.next(kRowSlots);
       const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
-      warp_wait(smem_u32(&ctl.sfull), sphase, &ctl.gave_up);
-      sphase ^= 1;
+      const uint32_t buf = SHARED ? 0 : n_scores & 1, tm = tm_s + buf * N;
+      warp_wait(smem_u32(&ctl.sfull[buf]), (SHARED ? n_scores : n_scores >> 1) & 1, &ctl.gave_up);
+      ++n_scores;
       tc_after();
+      // The products of the tile before: complete, unless these scores were
+      // made beside its weights.
+      bool pending = !SHARED && tile > s.v0;
+      auto settle = [&] {
+        if (!pending) return;
+        warp_wait(smem_u32(&ctl.odone), ophase, &ctl.gave_up);
+        ophase ^= 1;
+        tc_after();
+        pending = false;
+      };
       float x[C];  // scores in log2 units
-      tm_load(tm_s, x);
+      tm_load(tm, x);
 #pragma unroll
       for (int k = 0; k < C; ++k) x[k] = row ? x[k] * scale : -INFINITY;
       if (ragged) {
@@ -1016,8 +1036,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
         if (tile > s.v0) {
 #pragma unroll
           for (int k = 0; k < C; ++k) l[k] *= ctl.fac[k0 + k];
-          // products of the tiles before are complete: they were issued
-          // before this tile's scores
+          settle();
 #pragma unroll 1
           for (int u = 0; u < pl.units; ++u)
 #pragma unroll 1
@@ -1037,12 +1056,15 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       if (ragged) {
         const uint8_t* value = row + c.val_off + (int64_t)s.g * c.val_stride;
         if (row && (j < all_lo || j >= all_hi)) odd = !finite_row(value, c.dv, c.f16);
-        if (named_or(1, kSoftThreads, odd))
-          odd_rows<N>(P, sm, ctl, tid, odd, value, vr, tile * kTile, tile == s.v0);
+        if (named_or(1, kSoftThreads, odd)) {
+          settle();
+          odd_rows<N>(P, sm, ctl, tid, odd, value, vr, tile * kTile, tile == s.v0, tm);
+        }
       }
 #pragma unroll 1
       for (int u = 0; u < pl.units; ++u) vr.next(pl.vslots);
       // weights: half of a row of N in the swizzled layout
+      settle();
 #pragma unroll
       for (int k = 0; k < C; k += 8) {
         const float4 b0 = *reinterpret_cast<const float4*>(&ctl.base[k0 + k]);
@@ -1105,7 +1127,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
     }
     named_sync(1, kSoftThreads);
     if (!none) {
-      warp_wait(smem_u32(&ctl.ofull), ophase, &ctl.gave_up);
+      warp_wait(smem_u32(&ctl.odone), ophase, &ctl.gave_up);
       ophase ^= 1;
       tc_after();
     }
@@ -1173,7 +1195,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
   }
 }
 
-template <int N, int MAXI>
+template <int N, bool SHARED, int MAXI>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ AttendParams<MAXI> P, float* parts) {
   extern __shared__ uint8_t raw[];
@@ -1213,9 +1235,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp < kSoftThreads / 32) softmax_rows<N>(P, sm, ctl, tid, parts);
-    else if (warp < kIssueWarp) load_rows<N>(P, sm, ctl, tid - kSoftThreads);
-    else if (warp == kIssueWarp) issue_products<N>(P, sm, ctl);
+    if (warp < kSoftThreads / 32) softmax_rows<N, SHARED>(P, sm, ctl, tid, parts);
+    else if (warp < kIssueWarp) load_rows<N, SHARED>(P, sm, ctl, tid - kSoftThreads);
+    else if (warp == kIssueWarp) issue_products<N, SHARED>(P, sm, ctl);
     else find_rows<N>(P, ctl, tid - 32 * kRowWarp);
   }
   __syncwarp();
@@ -1357,7 +1379,7 @@ Plan make_plan(const AttendCommon& c, int n) {
     return 1024 + kControlBytes + q + (alias ? 0 : w) + (uint32_t)k * kChunk + (uint32_t)v * kUnit;
   };
   // the weights can take the place of a key chunk that is done with by then
-  p.alias = bytes(p.kslots, p.vslots, false) > kSmemLimit && p.only_chunks == 1;
+  p.alias = p.shared && p.only_chunks == 1 && bytes(p.kslots, p.vslots, false) > kSmemLimit;
   for (bool more = true; more;) {
     more = false;
     if (p.vslots < std::min(kMaxV, 2 * p.units) && bytes(p.kslots, p.vslots + 1, p.alias) <= kSmemLimit) {
@@ -1461,7 +1483,8 @@ Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms) {
 
 template <int N, int MAXI>
 cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
-  attend_kernel<N, MAXI><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
+  if (P.plan.shared) attend_kernel<N, true><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
+  else attend_kernel<N, false><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !s.n_cut) return e;
   cudaLaunchConfig_t cfg{};
@@ -1498,18 +1521,22 @@ cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items
 }  // namespace
 
 cudaError_t attend_set_smem_limit() {
-  for (const void* k : {(const void*)attend_kernel<16, kAttendItemsSmall>,
-                        (const void*)attend_kernel<32, kAttendItemsSmall>,
-                        (const void*)attend_kernel<48, kAttendItemsSmall>,
-                        (const void*)attend_kernel<64, kAttendItemsSmall>,
-                        (const void*)attend_kernel<16, kAttendItemsLarge>,
-                        (const void*)attend_kernel<32, kAttendItemsLarge>,
-                        (const void*)attend_kernel<48, kAttendItemsLarge>,
-                        (const void*)attend_kernel<64, kAttendItemsLarge>}) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  auto of = [](auto n) {
+    constexpr int N = decltype(n)::value;
+    cudaError_t e = cudaSuccess;
+    for (const void* k : {(const void*)attend_kernel<N, false, kAttendItemsSmall>,
+                          (const void*)attend_kernel<N, true, kAttendItemsSmall>,
+                          (const void*)attend_kernel<N, false, kAttendItemsLarge>,
+                          (const void*)attend_kernel<N, true, kAttendItemsLarge>})
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    return e;
+  };
+  cudaError_t e = of(std::integral_constant<int, 16>{});
+  if (e == cudaSuccess) e = of(std::integral_constant<int, 32>{});
+  if (e == cudaSuccess) e = of(std::integral_constant<int, 48>{});
+  if (e == cudaSuccess) e = of(std::integral_constant<int, 64>{});
+  return e;
 }
 
 bool attend_shape(AttendCommon c, AttendItem* items, int n_items, int sms, size_t* bytes) {
