@@ -1255,80 +1255,91 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kMergeWarps = 16;
 constexpr int kMergeElems = 128;  // value elements of a warp: a float4 a lane
+constexpr int kCutsSmall = 16;    // split jobs that the small parameter table holds
 
+// A split job: parts of the blocks [b0, b0 + n).
+struct Cut {
+  uint8_t* out;       // of the job's kv head and, if located, query
+  float* lse;         // or null
+  int32_t b0, n;
+  int32_t col0, cols;
+};
+
+template <int CUTS>
 struct MergeParams {
   int32_t groups;     // warps that share one column's parts: 1, 4 or 16
-  uint8_t cut[kAttendMaxBlocks];  // per split job: the first block that begins inside it
+  int32_t columns;    // of a part
+  int32_t dv, f16, heads, group;
+  int64_t o_qs, o_hs;
+  Cut cut[CUTS];
 };
 
 // Joins the parts of the split jobs in block order.  A warp has 128 value
 // elements of one column and every `groups`-th part; the groups' sums meet in
 // shared memory.
-template <int N, int MAXI>
-__global__ void __launch_bounds__(kMergeWarps * 32)
-    merge_kernel(const __grid_constant__ AttendParams<MAXI> P, const __grid_constant__ MergeParams M,
-                 const float* parts) {
-  const AttendCommon& c = P.c;
-  __shared__ float weight[kMergeWarps][kAttendMaxBlocks];
+template <int CUTS>
+__global__ void __launch_bounds__(kMergeWarps * 32, 2)
+    merge_kernel(const __grid_constant__ MergeParams<CUTS> M, const float* parts) {
   __shared__ float4 sums[kMergeWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b0 = M.cut[blockIdx.x] - 1;
-  const int32_t t = first_tile(c, b0 + 1);
-  const Segment s = segment_at<N>(P, t, t + 1);
-  // the block that holds the job's last tile
-  const int32_t last = t - s.t0 + s.tiles - 1 - c.waved, more = c.extra * (c.share + 1);
-  const int n = (last < more ? last / (c.share + 1) : c.extra + (last - more) / c.share) - b0 + 1;
-  const int spans = (c.dv + kMergeElems - 1) / kMergeElems;
+  const Cut& cut = M.cut[blockIdx.x];
+  const int n = cut.n, b0 = cut.b0;
+  const int spans = (M.dv + kMergeElems - 1) / kMergeElems;
   const int pair = blockIdx.y * (kMergeWarps / M.groups) + warp / M.groups;
   const int col = pair / spans, d = pair % spans * kMergeElems + lane * 4;
   const int group = warp % M.groups;
-  const bool on = col < s.cols;
-  const size_t stride = (size_t)N * (c.dv + 2);
+  const bool on = col < cut.cols;
+  const size_t stride = (size_t)M.columns * (M.dv + 2);
   auto part = [&](int i) { return parts + (size_t)(2 * (b0 + i) + (i == 0)) * stride; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const AttendItem& it = s.it;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   float base = 0.f, z = 0.f;
   if (on) {
-    const size_t ml = (size_t)N * c.dv + col;
+    const size_t ml = (size_t)M.columns * M.dv + col;
     float m = -INFINITY;
+#pragma unroll 1
     for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ml]);
+#pragma unroll
     for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
     base = m == -INFINITY ? 0.f : m;
-    for (int i = lane; i < n; i += 32) {
-      const float w = exp2f(part(i)[ml] - base);
-      weight[warp][i] = w;
-      z += w * part(i)[ml + N];
-    }
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32)
+      z += exp2_fast(part(i)[ml] - base) * part(i)[ml + M.columns];
+#pragma unroll
     for (int w = 16; w; w >>= 1) z += __shfl_xor_sync(~0u, z, w);
-    __syncwarp();
-    if (d < c.dv) {
-      const size_t at = (size_t)col * c.dv + d;
-      auto add = [&](float w, const float4& y) {
-        if (w != 0.f) {  // a part without weight may hold sums that are not finite
-          x.x += w * y.x;
-          x.y += w * y.y;
-          x.z += w * y.z;
-          x.w += w * y.w;
-        }
-      };
-      int i = group;
-      for (; i + 3 * M.groups < n; i += 4 * M.groups) {
+    // lane k's weight is that of the group's k-th part, of 32 at a time
+#pragma unroll 1
+    for (int i0 = group; i0 < n; i0 += 32 * M.groups) {
+      const int mine = i0 + lane * M.groups;
+      const float weight = mine < n ? exp2_fast(part(mine)[ml] - base) : 0.f;
+      const int count = min(32, (n - i0 + M.groups - 1) / M.groups);
+#pragma unroll 1
+      for (int k = 0; k < count; k += 4) {
         float4 y[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          y[k] = *reinterpret_cast<const float4*>(part(i + k * M.groups) + at);
+        for (int u = 0; u < 4; ++u)
+          if (k + u < count && d < M.dv)
+            y[u] = *reinterpret_cast<const float4*>(part(i0 + (k + u) * M.groups) +
+                                                    (size_t)col * M.dv + d);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) add(weight[warp][i + k * M.groups], y[k]);
+        for (int u = 0; u < 4; ++u) {
+          const float w = __shfl_sync(~0u, weight, (k + u) & 31);
+          // a part without weight may hold sums that are not finite
+          if (k + u < count && w != 0.f && d < M.dv) {
+            x.x += w * y[u].x;
+            x.y += w * y[u].y;
+            x.z += w * y[u].z;
+            x.w += w * y[u].w;
+          }
+        }
       }
-      for (; i < n; i += M.groups)
-        add(weight[warp][i], *reinterpret_cast<const float4*>(part(i) + at));
     }
   }
   if (M.groups > 1) {
     sums[warp][lane] = x;
     __syncthreads();
     if (group) return;
+#pragma unroll 1
     for (int k = 1; k < M.groups; ++k) {
       const float4 y = sums[warp + k][lane];
       x.x += y.x;
@@ -1338,21 +1349,28 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     }
   }
   if (!on) return;
-  const int qc = s.col0 + col;
-  const int qi = it.loc ? s.qbase : qc / c.group;
-  const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
-  if (it.lse && lane == 0 && d == 0)
-    it.lse[(size_t)qi * c.heads + h] =
+  const int qc = cut.col0 + col, qi = qc / M.group, h = qc - qi * M.group;
+  if (cut.lse && lane == 0 && d == 0)
+    cut.lse[(size_t)qi * M.heads + h] =
         z == 0.f ? -INFINITY : (base + log2f(z)) * 0.693147180559945309f;
-  if (d >= c.dv) return;
-  uint8_t* out = it.out + qi * c.o_qs + h * c.o_hs + 2 * d;
+  if (d >= M.dv) return;
+  uint8_t* out = cut.out + qi * M.o_qs + h * M.o_hs + 2 * d;
   const float inv = z == 0.f ? 0.f : 1.f / z;
-  const float y[4] = {x.x, x.y, x.z, x.w};
+  float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+  uint16_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float v = inv == 0.f ? 0.f : y[k] * inv;
-    if (c.f16) reinterpret_cast<__half*>(out)[k] = __float2half_rn(v);
-    else reinterpret_cast<__nv_bfloat16*>(out)[k] = __float2bfloat16_rn(v);
+    if (inv == 0.f) y[k] = 0.f;
+    const __half a = __float2half_rn(y[k]);
+    const __nv_bfloat16 b = __float2bfloat16_rn(y[k]);
+    w[k] = M.f16 ? __half_as_ushort(a) : __bfloat16_as_ushort(b);
+  }
+  if ((uintptr_t)out & 7) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reinterpret_cast<uint16_t*>(out)[k] = w[k];
+  } else {
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
   }
 }
 
@@ -1409,12 +1427,12 @@ int widest_block(const AttendCommon& c) {
 }
 
 struct Shape {
-  int n;            // columns of a block
-  int64_t tiles;
-  int blocks;
-  int n_cut;        // jobs cut by a block's boundary
-  int parts;        // of the longest job, about
-  MergeParams merge;
+  int n = 0;          // columns of a block
+  int64_t tiles = 0;
+  int blocks = 0;
+  int n_cut = 0;      // jobs cut by a block's boundary
+  int groups = 1;     // of the merge
+  Cut cut[kAttendMaxBlocks];
 };
 
 int columns_of(const AttendCommon& c, const AttendItem& it, int most) {
@@ -1425,7 +1443,7 @@ int columns_of(const AttendCommon& c, const AttendItem& it, int most) {
 
 // Fills in every item's tiles, and how the blocks share them.
 Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms) {
-  Shape s{};
+  Shape s;
   const int most = widest_block(c);
   int widest = 1;
   int64_t n_jobs = 0, longest = 0, shortest = INT64_MAX;
@@ -1464,32 +1482,51 @@ Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms) {
   const int64_t rest = s.tiles - c.waved;  // dealt out evenly, cut where it falls
   c.share = (int32_t)(rest / s.blocks);
   c.extra = (int32_t)(rest % s.blocks);
-  s.parts = rest ? (int)std::min<int64_t>(s.blocks, longest * s.blocks / rest + 2) : 0;
-  s.merge.groups = s.parts > 24 ? 16 : s.parts > 4 ? 4 : 1;
+  const int parts = rest ? (int)std::min<int64_t>(s.blocks, longest * s.blocks / rest + 2) : 0;
+  s.groups = parts > 24 ? 16 : parts > 4 ? 4 : 1;
   if (rest) {
     int k = 0;
     int64_t cut_job = -1;  // first tile of the job cut last
     for (int b = 1; b < s.blocks; ++b) {
       const int32_t t = first_tile(c, b);
+      if (t >= s.tiles) break;
       while (k + 1 < n_items && items[k + 1].tile0 <= t) ++k;
-      const int32_t in = (t - items[k].tile0) % items[k].tiles;
-      if (in == 0 || t - in == cut_job || t >= s.tiles) continue;
+      const AttendItem& it = items[k];
+      const int32_t job = (t - it.tile0) / it.tiles, in = (t - it.tile0) - job * it.tiles;
+      if (in == 0 || t - in == cut_job) continue;
       cut_job = t - in;
-      s.merge.cut[s.n_cut++] = (uint8_t)b;
+      Cut& cut = s.cut[s.n_cut++];
+      const int32_t query = job / it.blocks, q = query / c.kv, head = (query - q * c.kv) * c.group;
+      const int32_t columns = it.loc ? c.group : it.Q * c.group;
+      cut.out = it.out + q * c.o_qs + head * c.o_hs;
+      cut.lse = it.lse ? it.lse + (size_t)q * c.heads + head : nullptr;
+      cut.col0 = (job - query * it.blocks) * it.width;
+      cut.cols = std::min(it.width, columns - cut.col0);
+      // up to the block that holds the job's last tile
+      const int32_t last = (int32_t)cut_job + it.tiles - 1 - c.waved, more = c.extra * (c.share + 1);
+      cut.b0 = b - 1;
+      cut.n = (last < more ? last / (c.share + 1) : c.extra + (last - more) / c.share) - b + 2;
     }
   }
   return s;
 }
 
-template <int N, int MAXI>
-cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
-  if (P.plan.shared) attend_kernel<N, true><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
-  else attend_kernel<N, false><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !s.n_cut) return e;
+template <int CUTS>
+cudaError_t launch_merge(const AttendCommon& c, const Shape& s, const float* parts,
+                         cudaStream_t stream) {
+  MergeParams<CUTS> M;
+  M.groups = s.groups;
+  M.columns = s.n;
+  M.dv = c.dv;
+  M.f16 = c.f16;
+  M.heads = c.heads;
+  M.group = c.group;
+  M.o_qs = c.o_qs;
+  M.o_hs = c.o_hs;
+  std::copy(s.cut, s.cut + s.n_cut, M.cut);
   cudaLaunchConfig_t cfg{};
-  const int per = kMergeWarps / s.merge.groups;
-  const int pairs = N * ((P.c.dv + kMergeElems - 1) / kMergeElems);
+  const int per = kMergeWarps / s.groups;
+  const int pairs = s.n * ((c.dv + kMergeElems - 1) / kMergeElems);
   cfg.gridDim = dim3(s.n_cut, (pairs + per - 1) / per);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
@@ -1498,7 +1535,17 @@ cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<N, MAXI>, P, s.merge, (const float*)parts);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<CUTS>, M, parts);
+}
+
+template <int N, int MAXI>
+cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
+  if (P.plan.shared) attend_kernel<N, true><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
+  else attend_kernel<N, false><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !s.n_cut) return e;
+  return s.n_cut <= kCutsSmall ? launch_merge<kCutsSmall>(P.c, s, parts, stream)
+                               : launch_merge<kAttendMaxBlocks>(P.c, s, parts, stream);
 }
 
 template <int MAXI>
