@@ -10,23 +10,51 @@
 // out = o / l, log-sum = m + ln l.
 //
 // Both products run on the 5th-generation tensor cores with the rows as the
-// M side, because few query heads share a row and M is at least 64 there:
+// M side, because few query heads share a row and M is 64 or 128 there:
 //   S^T[128 rows x N] = X[128 x dk] . Q^T      (tile of 128 rows, N columns)
 //   O^T[dv x N]      += Y^T[dv x 128] . P^T    (M = 128 value elements)
 // A column is one (query, head) pair sharing the rows: up to 64 of them.
-// The tile of rows is staged once in shared memory and feeds both products
-// (as a K-major operand first, as an M-major one then); where keys and
-// values are the same bytes (one latent row) they are loaded once.  S^T, O^T
-// stay in tensor memory; a thread owns one row of S^T, so weights need no
-// shuffles, and the maximum is only reduced across rows when m moves.
+// (A product takes 48 cycles for N = 16, 55 for N = 64: narrow blocks cost
+// nearly as much each, so columns that share rows share a block.)  The tile
+// of rows is staged once in shared memory and feeds both products (as a
+// K-major operand first, as an M-major one then); where keys and values are
+// the same bytes (one latent row) they are loaded once.  S^T, O^T stay in
+// tensor memory; a thread owns one row of S^T, so weights need no shuffles,
+// and the maximum is only reduced across rows when m moves.
 //
-// A block has 8 softmax warps, 4 loading warps and 1 issuing warp, joined by
-// mbarriers.  Rows lie at arbitrary addresses of four memories, so loads are
-// 16-byte asynchronous copies into the swizzled layout.  The launch is one
-// block per SM; all tiles of all jobs (a job: one item, kv head and block of
-// columns) are dealt out evenly in order, so that long and short items
-// balance; a job cut by a block's boundary leaves (m, l, o) parts that
-// merge_kernel joins in order.
+// Roundings: scores, m, l and o are 32-bit; the weights alone are rounded to
+// the rows' 16-bit type, as the second product's operand, while l sums them
+// unrounded: an error of half a unit of each weight, of the size of the
+// output's own rounding.  m being up to 2^8 behind the maximum costs an f16
+// weight nothing (2^8 < 65504) and gives small ones 8 bits more above zero.
+//
+// A block has 8 softmax warps, 4 loading warps, an issuing warp, a warp that
+// finds the block's segments ahead and two that find the rows' addresses,
+// joined by mbarriers.  Each role's code is kept short, loops rolled: a
+// launch starts with cold instruction caches, and a kernel of 167 KB instead
+// of 70 spent 10 us there (one query over 256 rows 16.4 us -> 14.4; grouped
+// verify blocks, whose loading warps then also found their rows, 78 -> 54).
+//
+// Rows lie at arbitrary addresses of four memories, so loads are 16-byte
+// asynchronous copies into the swizzled layout, at most 27 bytes a cycle and
+// SM (7.9 TB/s).  Tensor gathers of four rows reach twice that, but take a
+// map for each memory and 65 cycles a warp each; with 64-row tiles, which
+// let scores run ahead, they lost everywhere (500K rows 126 -> 150 us, 64
+// verify blocks 265 -> 287): less of the ring was left for rows in flight.
+//
+// The launch is one block per SM (its shared memory is filled by rows in
+// flight); all tiles of all jobs (a job: one item, kv head and block of
+// columns) are dealt out in order, evenly; a job cut by a block's boundary
+// leaves (m, l, o) parts that merge_kernel joins in block order, so that a
+// call's bits do not depend on timing.
+//
+// What bounds it (16 query heads on a 1152-byte latent row unless said):
+// 64 verify blocks of 8 queries over 2048 rows each, 234 us: every query's
+// rows staged once, 1.21 GB through the loading warps at 5.2 TB/s (DRAM
+// reads 376 MB, each distinct row once).  One token over 512K rows, 116 us:
+// 590 MB of DRAM reads at 5.8 TB/s between a start of 4 us and a merge of 10.
+// 128 heads, 160 us: one tile at a time is resident beside 64 queries, so
+// that loads, scores, weights and sums follow each other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -722,6 +750,10 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
     int next = v0;  // the tile whose scores are next
 #pragma unroll 1
     for (int tile = v0; tile < v1; ++tile) {
+      // Values of their own arrive behind the keys, so that the next tile's
+      // scores can be made while the softmax warps have this one's (grouped
+      // histories 49 -> 45 us); shared rows hold their slots until the sums
+      // are made, and leave none for the next tile.
       const int last = SHARED ? tile : min(tile + 1, v1 - 1);
 #pragma unroll 1
       for (; next <= last; ++next) {
@@ -1255,7 +1287,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kMergeWarps = 16;
 constexpr int kMergeElems = 128;  // value elements of a warp: a float4 a lane
-constexpr int kCutsSmall = 16;    // split jobs that the small parameter table holds
 
 // A split job: parts of the blocks [b0, b0 + n).
 struct Cut {
@@ -1265,21 +1296,21 @@ struct Cut {
   int32_t col0, cols;
 };
 
-template <int CUTS>
 struct MergeParams {
   int32_t groups;     // warps that share one column's parts: 1, 4 or 16
   int32_t columns;    // of a part
   int32_t dv, f16, heads, group;
   int64_t o_qs, o_hs;
-  Cut cut[CUTS];
+  Cut cut[kAttendMaxBlocks];
 };
 
 // Joins the parts of the split jobs in block order.  A warp has 128 value
 // elements of one column and every `groups`-th part; the groups' sums meet in
-// shared memory.
-template <int CUTS>
+// shared memory.  Bound by latency: statistics, then weights, then parts, each
+// a trip to L2; 104 jobs of 64 columns in 2 to 3 parts, 34 MB, take 23 us, one
+// job of 16 columns in 152 parts 13 (each on cold caches).
 __global__ void __launch_bounds__(kMergeWarps * 32, 2)
-    merge_kernel(const __grid_constant__ MergeParams<CUTS> M, const float* parts) {
+    merge_kernel(const __grid_constant__ MergeParams M, const float* parts) {
   __shared__ float4 sums[kMergeWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Cut& cut = M.cut[blockIdx.x];
@@ -1468,9 +1499,11 @@ Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms) {
   s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(sms, s.tiles));
   c.waves = c.waved = c.job_tiles = c.share = c.extra = 0;
   if (s.tiles > INT32_MAX) return s;  // refused
-  // Jobs of equal length: whole ones in waves over the blocks (64 verify
-  // blocks of 8 queries, whose rows are mostly the same: XXX), fewer blocks if
-  // that leaves nothing to split and no block with more to do.
+  // Jobs of equal length: whole ones in waves over the blocks, as neighbours
+  // often read the same rows (64 verify blocks of 8 queries with 80 % of their
+  // rows in common 267 -> 250 us, 128 heads 191 -> 185; grouped heads on
+  // unrelated rows lose, 76 -> 82).  Fewer blocks if that leaves nothing to
+  // split and no block with more to do.
   if (longest == shortest) {
     const int64_t each = (n_jobs + sms - 1) / sms;
     if (n_jobs % each == 0 && each * longest <= (s.tiles + s.blocks - 1) / s.blocks)
@@ -1483,6 +1516,9 @@ Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms) {
   c.share = (int32_t)(rest / s.blocks);
   c.extra = (int32_t)(rest % s.blocks);
   const int parts = rest ? (int)std::min<int64_t>(s.blocks, longest * s.blocks / rest + 2) : 0;
+  // Warps that share a column: few parts leave too little to each, many wait
+  // in line.  8 x 2048 rows in 20 parts: 4 groups 16.4 us, 1 18.5, 16 20.5;
+  // 512 K rows in 152 parts: 16 groups 116.5 us, 4 122.3.
   s.groups = parts > 24 ? 16 : parts > 4 ? 4 : 1;
   if (rest) {
     int k = 0;
@@ -1511,10 +1547,9 @@ Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms) {
   return s;
 }
 
-template <int CUTS>
 cudaError_t launch_merge(const AttendCommon& c, const Shape& s, const float* parts,
                          cudaStream_t stream) {
-  MergeParams<CUTS> M;
+  MergeParams M;
   M.groups = s.groups;
   M.columns = s.n;
   M.dv = c.dv;
@@ -1535,17 +1570,19 @@ cudaError_t launch_merge(const AttendCommon& c, const Shape& s, const float* par
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<CUTS>, M, parts);
+  return cudaLaunchKernelEx(&cfg, merge_kernel, M, parts);
 }
 
 template <int N, int MAXI>
 cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
+  // A kernel for each kind of layout: with one that asked at run time, both
+  // were slower (128 heads 172 us instead of 166, grouped heads 55.7 instead
+  // of 54.4).
   if (P.plan.shared) attend_kernel<N, true><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
   else attend_kernel<N, false><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !s.n_cut) return e;
-  return s.n_cut <= kCutsSmall ? launch_merge<kCutsSmall>(P.c, s, parts, stream)
-                               : launch_merge<kAttendMaxBlocks>(P.c, s, parts, stream);
+  return launch_merge(P.c, s, parts, stream);
 }
 
 template <int MAXI>
@@ -1599,6 +1636,8 @@ cudaError_t launch_attend(AttendCommon c, AttendItem* items, int n_items, int sm
   const Shape s = shape_of(c, items, n_items, sms);
   if (s.tiles > INT32_MAX) return cudaErrorInvalidValue;
   float* parts = static_cast<float*>(work);
+  // The whole table travels with a launch: a small one for few items (12
+  // histories 41.7 us instead of 42.5, 8 of 32 K rows 66.3 instead of 67.0).
   return n_items <= kAttendItemsSmall
              ? launch_t<kAttendItemsSmall>(c, items, n_items, s, parts, stream)
              : launch_t<kAttendItemsLarge>(c, items, n_items, s, parts, stream);
