@@ -51,15 +51,14 @@
 // What bounds it (16 query heads on a 1152-byte latent row unless said):
 // 64 verify blocks of 8 queries over 2048 rows each, 234 us: every query's
 // rows staged once, 1.21 GB through the loading warps at 5.2 TB/s (DRAM
-// reads 376 MB, each distinct row once).  One token over 512K rows, 116 us:
+// reads 406 MB, each distinct row once).  One token over 512K rows, 116 us:
 // 590 MB of DRAM reads at 5.8 TB/s between a start of 4 us and a merge of 10.
-// 128 heads, 160 us: one tile at a time is resident beside 64 queries, so
+// 128 heads, 157 us: one tile at a time is resident beside 64 queries, so
 // that loads, scores, weights and sums follow each other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <cstddef>
 #include <type_traits>
 
 #include "dhs_internal.h"
@@ -298,28 +297,10 @@ __device__ __forceinline__ void query_rows(const AttendItem& it, int i, int64_t&
   hi = (it.range ? min((int64_t)it.range[2 * i + 1], L) : L - it.Q + 1 + i) - it.first;
 }
 
-// Launch parameters through memory: lanes read different ones, and many at a
-// time, where constant memory answers one miss after the other (~500 cycles
-// each, after every launch).
-template <class T>
-__device__ __forceinline__ T fetch(const T* p) {
-  union {
-    T t;
-    uint4 q[sizeof(T) / 16];
-  } u;
-  static_assert(sizeof(T) % 16 == 0, "whole 16-byte words");
-  const uint4* a = reinterpret_cast<const uint4*>(p);
-  asm volatile("" : "+l"(a));  // no longer known to be a parameter
-#pragma unroll
-  for (int k = 0; k < (int)(sizeof(T) / 16); ++k) u.q[k] = a[k];
-  return u.t;
-}
-
 // The last item whose first tile is <= t (an item without jobs has none).
 template <int MAXI>
 __device__ __forceinline__ int item_at(const AttendParams<MAXI>& P, int32_t t) {
   const int32_t* first = P.first + (threadIdx.x & 31);
-  asm volatile("" : "+l"(first));
   int32_t x[(MAXI + 31) / 32];
 #pragma unroll
   for (int k = 0; k < (MAXI + 31) / 32; ++k)
@@ -337,7 +318,7 @@ __device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te
   const AttendCommon& c = P.c;
   __syncwarp();
   Segment s;
-  s.it = fetch(&P.items[item_at(P, t)]);
+  s.it = P.items[item_at(P, t)];
   const AttendItem& it = s.it;
   const bool located = it.loc != nullptr;
   s.tiles = it.tiles;
@@ -413,7 +394,7 @@ __device__ bool next_segment(const AttendParams<MAXI>& P, Walk& w, Segment& s) {
 
 // Finding row j of a job takes up to two dependent loads: a list position
 // (union items), then the location or (histories) the page's slot.  They are
-// split so that a loading thread can keep them in flight: `row_index` two
+// split so that a row thread can keep them in flight: `row_index` two
 // tiles ahead, `row_word` one tile ahead, `row_of` when the tile is loaded.
 __device__ __forceinline__ int32_t row_index(const Segment& s, int64_t j) {
   const AttendItem& it = s.it;
@@ -501,7 +482,10 @@ struct Ring {
   }
 };
 
-__host__ __device__ constexpr uint32_t tmem_columns(int n) { return 6 * n <= 128 ? 128 : 6 * n <= 256 ? 256 : 512; }
+// Two buffers of scores, then up to four units of sums.
+__host__ __device__ constexpr uint32_t tmem_columns(int n) {
+  return 6 * n <= 128 ? 128 : 6 * n <= 256 ? 256 : 512;
+}
 // Bytes of one row of weights, the swizzle of that row width, and its 8-row stride.
 __host__ __device__ constexpr int weight_row(int n) { return n <= 16 ? 32 : n <= 32 ? 64 : 128; }
 __host__ __device__ constexpr uint32_t weight_swizzle(int n) { return n <= 16 ? 6 : n <= 32 ? 4 : 2; }
@@ -1235,10 +1219,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   Control& ctl = *reinterpret_cast<Control*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
-  // Each warp touches one line of the launch's parameters: their misses, one
-  // after the other in any one warp, then overlap.
-  static_assert(offsetof(AttendParams<MAXI>, first) <= kThreads / 32 * 64, "lines to touch");
-  asm volatile("" ::"r"(reinterpret_cast<const int32_t*>(&P)[warp * 16]));
   if (warp == kIssueWarp) {
 #pragma unroll
     for (int k = 0; k < kBarriers; k += 32) {
@@ -1590,7 +1570,6 @@ cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items
                      float* parts, cudaStream_t stream) {
   AttendParams<MAXI> P;
   P.c = c;
-  P.c.n_items = n_items;
   P.plan = make_plan(c, s.n);
   for (int i = 0; i < MAXI; ++i) P.first[i] = i < n_items ? items[i].tile0 : INT32_MAX;
   for (int i = 0; i < n_items; ++i) P.items[i] = items[i];

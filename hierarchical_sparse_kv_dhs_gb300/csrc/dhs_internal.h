@@ -316,7 +316,6 @@ struct AttendCommon {
   uint32_t tail_rows, opt_rows, hot_rows;  // arena sizes in rows
   int32_t row_bytes, T, Pmax, page_shift;
   uint32_t* status;
-  int32_t n_items;
   int32_t waves, waved, job_tiles;  // whole jobs dealt out first (launch_attend)
   int32_t share, extra;   // tiles of a block after that, and blocks that have one more
   int32_t f16;            // rows are f16, else bf16
