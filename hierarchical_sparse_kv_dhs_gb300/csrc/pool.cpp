@@ -1958,13 +1958,14 @@ int dhs_attend_on(dhs_pool* p, const dhs_attend_step* st, void* stream) {
 // ---------------------------------------------------------------------------
 // Forks and compaction (fork.cu).
 
-// Forget everything of a child that dhs_fork could not complete.
+// Forget everything of a child that dhs_fork could not complete.  All its maps
+// await an upload again: the fork may have dropped one.
 static void undo_fork(dhs_pool* p, int32_t child) {
   for (int32_t s = 0; s < p->cfg.sources; ++s) {
     const int64_t pair = (int64_t)child * p->cfg.sources + s;
+    mark_dirty(p, pair);
     if (!p->ps[pair].admitted) continue;
     drop_pages(p, pair, false);
-    mark_dirty(p, pair);
     p->complete_pages -= p->ps[pair].N >> p->page_shift;
     p->ps[pair] = PairState();
   }
@@ -2034,9 +2035,11 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
     }
     reserve_backup(p, (size_t)want);
     // The parent's pending pages and the maps, before the copy reads them.  If
-    // only the child's map awaits an upload (its release, mostly), none is
-    // needed: the copy writes that map itself.
-    if (direct && !p->any_pending && p->dirty_lo >= to0 && p->dirty_hi < to0 + c.sources) {
+    // only the child's maps await an upload (its release, mostly) and the copy
+    // writes every one of them itself, none is needed.  A source that the
+    // parent lacks has a map that the copy does not write.
+    if (direct && !p->any_pending && src.size() == (size_t)c.sources && p->dirty_lo >= to0 &&
+        p->dirty_hi < to0 + c.sources) {
       p->dirty_lo = INT64_MAX;
       p->dirty_hi = -1;
     }
