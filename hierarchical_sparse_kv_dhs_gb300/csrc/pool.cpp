@@ -2000,10 +2000,10 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
   if (rc) return rc;
   std::vector<dhs::ForkSource> src;
   std::vector<int32_t> slots;  // the child's, where they travel with the launch
+  int64_t pages = 0;           // complete ones, of all sources
   bool direct = false;
   try {
     src.reserve(c.sources);
-    int64_t pages = 0;
     for (int32_t s = 0; s < c.sources; ++s) {
       const PairState& f = p->ps[from0 + s];
       if (!f.admitted) continue;
@@ -2027,7 +2027,7 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
       src.push_back(k);
     }
     direct = pages <= dhs::kForkSlotsMax && src.size() <= (size_t)dhs::kForkSourcesSome;
-    if (direct) slots.assign((size_t)pages + 1, -1);
+    if (direct) slots.assign((size_t)std::max<int64_t>(pages, 1), -1);  // data() never null
     const int64_t usable = p->capacity - c.admission_reserve_pages;
     if (p->used + want > usable) {
       if (deficit) *deficit = p->used + want - usable;
@@ -2094,7 +2094,7 @@ int dhs_fork(dhs_pool* p, int32_t req, int32_t child, void* const* host_rows,
   for (size_t b = 0; b < src.size(); b += dhs::kForkSourcesMax) {
     const int n = (int)std::min<size_t>(dhs::kForkSourcesMax, src.size() - b);
     if (dhs::launch_fork(f, src.data() + b, n, direct ? slots.data() : nullptr,
-                         (int)slots.size(), std::max(1, p->sm_count), p->stream) !=
+                         direct ? (int)pages : 0, std::max(1, p->sm_count), p->stream) !=
         cudaSuccess) {
       undo_fork(p, child);
       return DHS_ECUDA;

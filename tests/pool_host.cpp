@@ -263,12 +263,30 @@ static void fork_without_memory() {
   }
 }
 
+// Forks around the sizes of the launch's tables of page slots, spread over
+// one source or several.
+static void fork_table_limits() {
+  for (int sources : {1, 4})
+    for (int64_t pages : {511, 512, 513, dhs::kForkSlotsMax - 1, dhs::kForkSlotsMax,
+                          dhs::kForkSlotsMax + 1}) {
+      Host h(2, sources, pages * kPage, 2 * pages);
+      for (int s = 0; s < sources; ++s) {
+        const int64_t mine = pages / sources + (s < pages % sources);
+        CHECK(h.admit(0, s, mine * kPage, true) == DHS_OK);
+      }
+      CHECK(h.fork(0, 1) == DHS_OK);
+      CHECK(dhs_pool_used(h.p) == 2 * pages);
+      for (int s = 0; s < sources; ++s) CHECK(h.device_slots(1, s) == h.slots(1, s));
+    }
+}
+
 int main(int argc, char** argv) {
   std::vector<std::string> log;
   g_log = &log;
   const std::map<std::string, void (*)()> all = {
       {"fork_of_fewer_sources", fork_of_fewer_sources},
       {"fork_without_memory", fork_without_memory},
+      {"fork_table_limits", fork_table_limits},
   };
   const auto f = all.find(argc > 1 ? argv[1] : "");
   if (f == all.end()) return 2;

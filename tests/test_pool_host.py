@@ -25,7 +25,8 @@ def program(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("scenario", ["fork_of_fewer_sources", "fork_without_memory"])
+@pytest.mark.parametrize("scenario", ["fork_of_fewer_sources", "fork_without_memory",
+                                      "fork_table_limits"])
 def test_scenario(program, scenario):
     r = subprocess.run([program, scenario], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout == "ok\n", r.stdout + r.stderr
