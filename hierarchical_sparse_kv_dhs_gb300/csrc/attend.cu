@@ -77,7 +77,6 @@ constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
 constexpr int kSegments = 4;               // segments found ahead
 constexpr int kRowSlots = 2;               // tiles whose row addresses are found ahead
 constexpr float kSlack = 8.f;              // log2 units
-constexpr uint32_t kWaitPolls = 1u << 22;  // polls of an mbarrier before giving up
 
 // How a launch's row slices are staged.
 struct Plan {
@@ -126,22 +125,29 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait.  A wait that runs out raises *gave_up; every later wait of
-// the block then falls through, so that all its warps still reach their end
-// (on wrong data: the launch's status says so).
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+// Bounded wait (a poll that fails takes 4 us).  A wait that runs out raises
+// *gave_up; every later wait of the block then falls through, so that all its
+// warps still reach their end, on wrong data: the launch's status says so.
+// What lies behind a wait that fell through may not have been written, so no
+// address is taken from there: a segment is used only if gave_up is still
+// down after the wait for it, and not replaced after a wait that gave up; the
+// table of rows holds nothing but rows and nulls from the start.
+struct Patience {
+  volatile uint32_t* gave_up;
+  uint32_t polls;
+};
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, const Patience& until) {
 #pragma unroll 1
-  for (uint32_t n = 0; n < kWaitPolls; ++n) {
-    if (bar_try(bar, parity)) return;
-    if ((n & 255) == 255 && *gave_up) return;
+  for (uint32_t n = 0; !bar_try(bar, parity); ++n) {
+    if (*until.gave_up) return;
+    if (n >= until.polls) *until.gave_up = 1;
   }
-  *gave_up = 1;
 }
 
 // The same by whole warps, together again afterwards: what follows may be an
 // instruction that a warp executes as one (block barriers, tcgen05 loads).
-__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
-  bar_wait(bar, parity, gave_up);
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, const Patience& until) {
+  bar_wait(bar, parity, until);
   __syncwarp();
 }
 
@@ -494,12 +500,13 @@ __host__ __device__ constexpr uint32_t weight_swizzle(int n) { return n <= 16 ? 
 template <int N, bool SHARED, int MAXI>
 __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid) {
   const AttendCommon& c = P.c;
+  const Patience until{&ctl.gave_up, c.polls};
   const Plan& pl = P.plan;
   const bool alias = SHARED && pl.alias;
   const uint32_t base = smem_u32(sm);
   Ring kr, vr, rr;
   uint32_t qphase = 0;
-  auto wait_empty = [&](uint32_t bar, uint32_t parity) { warp_wait(bar, parity, &ctl.gave_up); };
+  auto wait_empty = [&](uint32_t bar, uint32_t parity) { warp_wait(bar, parity, until); };
   // The slot's barrier gets this thread's arrival when its copies so far have
   // landed.  The issuing warp makes them visible to the tensor cores: a proxy
   // fence here would wait for every copy in flight.
@@ -511,7 +518,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
   Ring seg;
 #pragma unroll 1
   for (;;) {
-    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
     if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
     const int32_t v0 = s.v0, v1 = s.v1;
@@ -521,7 +528,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     // hold the buffer, and does so about as long as the slots of its rows.
     auto load_queries = [&] {
       if (!first) {
-        warp_wait(smem_u32(&ctl.qempty), qphase, &ctl.gave_up);
+        warp_wait(smem_u32(&ctl.qempty), qphase, until);
         qphase ^= 1;
       }
       first = false;
@@ -562,7 +569,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
     const uint32_t val_at = c.val_off + s.g * c.val_stride;
 #pragma unroll 1
     for (int tile = v0; tile < v1; ++tile) {
-      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, &ctl.gave_up);
+      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
       const uint8_t* row[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = ctl.row[rr.slot][r0 + 16 * i];
@@ -620,6 +627,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
 // while the block sets up.
 template <int N, int MAXI>
 __device__ void find_segments(const AttendParams<MAXI>& P, Control& ctl) {
+  const Patience until{&ctl.gave_up, P.c.polls};
   Ring seg;
   Walk w = first_of(P);
   bool more = true;
@@ -629,7 +637,8 @@ __device__ void find_segments(const AttendParams<MAXI>& P, Control& ctl) {
     more = next_segment<N>(P, w, s);
     if (begin) __syncthreads();
     if (!more) s.cols = 0;
-    warp_wait(smem_u32(&ctl.segempty[seg.slot]), seg.phase ^ 1, &ctl.gave_up);
+    warp_wait(smem_u32(&ctl.segempty[seg.slot]), seg.phase ^ 1, until);
+    if (__any_sync(~0u, ctl.gave_up)) break;  // the slot may still be in use
     if (elected()) {
       ctl.seg[seg.slot] = s;
       bar_arrive(smem_u32(&ctl.segfull[seg.slot]));
@@ -643,10 +652,11 @@ template <int N, int MAXI>
 __device__ void find_rows(const AttendParams<MAXI>& P, Control& ctl, int tid) {
   constexpr int R = kTile / kRowThreads;
   const AttendCommon& c = P.c;
+  const Patience until{&ctl.gave_up, c.polls};
   Ring seg, rr;
 #pragma unroll 1
   for (;;) {
-    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment s = ctl.seg[seg.slot];
     if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
     int64_t j = (int64_t)s.v0 * kTile + tid;
@@ -665,7 +675,7 @@ __device__ void find_rows(const AttendParams<MAXI>& P, Control& ctl, int tid) {
     }
 #pragma unroll 1
     for (int tile = s.v0; tile < s.v1; ++tile, j += kTile) {
-      warp_wait(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1, &ctl.gave_up);
+      warp_wait(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1, until);
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         const int64_t i = j + k * kRowThreads;
@@ -687,6 +697,7 @@ __device__ void find_rows(const AttendParams<MAXI>& P, Control& ctl, int tid) {
 template <int N, bool SHARED, int MAXI>
 __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl) {
   const AttendCommon& c = P.c;
+  const Patience until{&ctl.gave_up, c.polls};
   const Plan& pl = P.plan;
   const bool alias = SHARED && pl.alias;
   const uint32_t base = smem_u32(sm);
@@ -720,15 +731,14 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
   Ring seg;
 #pragma unroll 1
   for (;;) {
-    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
     const int32_t v0 = s.v0, v1 = s.v1, cols = s.cols;
-    if (!cols || ctl.gave_up) break;
-    __syncwarp();
+    if (__any_sync(~0u, ctl.gave_up) || !cols) break;
     if (lead) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
     seg.next(kSegments);
     if (v0 >= v1) continue;
-    warp_wait(smem_u32(&ctl.qfull), qphase, &ctl.gave_up);
+    warp_wait(smem_u32(&ctl.qfull), qphase, until);
     fence_async();
     qphase ^= 1;
     int next = v0;  // the tile whose scores are next
@@ -745,7 +755,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
         auto keys = [&](bool add) {
 #pragma unroll 1
           for (int k = 0; k < pl.only_chunks; ++k) {
-            warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, &ctl.gave_up);
+            warp_wait(smem_u32(&ctl.kfull[kr.slot]), kr.phase, until);
             fence_async();
             tc_after();
             chunk(d, k_lo + kr.slot * (kChunk >> 4), c0 + k, add || k > 0);
@@ -757,7 +767,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
         if (SHARED) {
 #pragma unroll 1
           for (int u = 0; u < pl.units; ++u) {
-            warp_wait(smem_u32(&ctl.vfull[vs.slot]), vs.phase, &ctl.gave_up);
+            warp_wait(smem_u32(&ctl.vfull[vs.slot]), vs.phase, until);
             fence_async();
             tc_after();
             const uint32_t at = v_lo + vs.slot * (kUnit >> 4);
@@ -773,10 +783,10 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
         }
         ++n_scores;
       }
-      warp_wait(smem_u32(&ctl.pfull), pphase, &ctl.gave_up);
+      warp_wait(smem_u32(&ctl.pfull), pphase, until);
       pphase ^= 1;
       if (tile == v0 && !first) {  // the previous segment's sums are read
-        warp_wait(smem_u32(&ctl.oempty), ophase, &ctl.gave_up);
+        warp_wait(smem_u32(&ctl.oempty), ophase, until);
         ophase ^= 1;
       }
       tc_after();
@@ -784,7 +794,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
 #pragma unroll 1
       for (int u = 0; u < pl.units; ++u) {
         if (!SHARED) {
-          warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
+          warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, until);
           fence_async();
           tc_after();
         }
@@ -808,7 +818,7 @@ __device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control
   // nothing of ours is in flight when tensor memory goes back
   if (lead) commit(smem_u32(&ctl.drain));
 #pragma unroll 1
-  for (uint32_t n = 0; n < kWaitPolls && !bar_try(smem_u32(&ctl.drain), 0); ++n) {
+  for (uint32_t n = 0; n < kAttendPolls && !bar_try(smem_u32(&ctl.drain), 0); ++n) {
   }
   __syncwarp();
 }
@@ -836,6 +846,7 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
                                       int32_t tile0, bool first, uint32_t tm_scores) {
   constexpr int C = N / 2;
   const AttendCommon& c = P.c;
+  const Patience until{&ctl.gave_up, c.polls};
   const Plan& pl = P.plan;
   const int r = tid & (kTile - 1), k0 = tid / kTile * C;
   const uint32_t tm_o = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0 + 2 * N;
@@ -868,7 +879,7 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
             ctl.part[0][col] = seen ? exp2_fast(v[n] * scale - ctl.base[col]) : 0.f;
           }
       }
-      if (r == i) ctl.odd_row = value;
+      if (tid == i) ctl.odd_row = value;
     }
     named_sync(1, kSoftThreads);
     const uint8_t* y = ctl.odd_row;
@@ -892,7 +903,7 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
   }
 #pragma unroll 1
   for (int u = 0; u < pl.units; ++u) {
-    warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, &ctl.gave_up);
+    warp_wait(smem_u32(&ctl.vfull[vr.slot]), vr.phase, until);
     if (odd && tid < kTile) {
       uint8_t* at = sm + pl.off_v + vr.slot * kUnit + r * 128;
 #pragma unroll 1
@@ -939,6 +950,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
                              float* parts) {
   constexpr int C = N / 2;
   const AttendCommon& c = P.c;
+  const Patience until{&ctl.gave_up, c.polls};
   const Plan& pl = P.plan;
   const bool alias = SHARED && pl.alias;
   const int lane = tid & 31, r = tid & (kTile - 1), quarter = r >> 5, k0 = tid / kTile * C;
@@ -954,7 +966,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
   Ring seg;
 #pragma unroll 1
   for (;;) {
-    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, &ctl.gave_up);
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
     const AttendItem& it = s.it;
     // the previous segment's column tables are read; all leave together
@@ -991,14 +1003,14 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
 #pragma unroll 1
     for (int tile = s.v0; tile < s.v1; ++tile) {
       const int32_t j = tile * kTile + r;
-      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, &ctl.gave_up);
+      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
       const uint8_t* row = ctl.row[rr.slot][r];
       __syncwarp();
       if (lane == 0) bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
       rr.next(kRowSlots);
       const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
       const uint32_t buf = SHARED ? 0 : n_scores & 1, tm = tm_s + buf * N;
-      warp_wait(smem_u32(&ctl.sfull[buf]), (SHARED ? n_scores : n_scores >> 1) & 1, &ctl.gave_up);
+      warp_wait(smem_u32(&ctl.sfull[buf]), (SHARED ? n_scores : n_scores >> 1) & 1, until);
       ++n_scores;
       tc_after();
       // The products of the tile before: complete, unless these scores were
@@ -1006,7 +1018,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
       bool pending = !SHARED && tile > s.v0;
       auto settle = [&] {
         if (!pending) return;
-        warp_wait(smem_u32(&ctl.odone), ophase, &ctl.gave_up);
+        warp_wait(smem_u32(&ctl.odone), ophase, until);
         ophase ^= 1;
         tc_after();
         pending = false;
@@ -1143,7 +1155,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
     }
     named_sync(1, kSoftThreads);
     if (!none) {
-      warp_wait(smem_u32(&ctl.odone), ophase, &ctl.gave_up);
+      warp_wait(smem_u32(&ctl.odone), ophase, until);
       ophase ^= 1;
       tc_after();
     }
@@ -1219,6 +1231,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Control& ctl = *reinterpret_cast<Control*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
+  static_assert(kRowSlots * kTile == kSoftThreads, "one address a softmax thread");
+  if (tid < kSoftThreads) (&ctl.row[0][0])[tid] = nullptr;
   if (warp == kIssueWarp) {
 #pragma unroll
     for (int k = 0; k < kBarriers; k += 32) {
@@ -1232,7 +1246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                full ? kLoadThreads : soft ? kSoftThreads / 32 : rows ? kRowThreads / 32
                : read ? (kSoftThreads + kLoadThreads) / 32 : segs ? kThreads / 32 - 1 : 1);
     }
-    ctl.gave_up = 0;
+    ctl.gave_up = P.c.polls == 0;  // nothing is waited for then
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(

@@ -324,10 +324,12 @@ struct AttendCommon {
   int32_t dk, dv;         // elements of a key and of a value
   int32_t key_off, val_off, key_stride, val_stride;  // bytes within a row
   float scale;
+  uint32_t polls;         // polls of a barrier before the block gives up
   int64_t q_qs, q_hs, o_qs, o_hs;  // bytes
 };
 
 constexpr int kAttendMaxBlocks = 256;
+constexpr uint32_t kAttendPolls = 1u << 22;  // DHS_OPT_ATTEND_POLLS default
 
 // Once per device: let the attention's blocks use all of an SM's shared memory.
 cudaError_t attend_set_smem_limit();

@@ -205,6 +205,7 @@ struct dhs_pool {
   int64_t ent_cap = 0;
   int stage_misses = 1;         // DHS_OPT_STAGE_MISSES
   uint32_t mark_polls = dhs::kMarkPolls;  // DHS_OPT_MARK_POLLS
+  uint32_t attend_polls = dhs::kAttendPolls;  // DHS_OPT_ATTEND_POLLS
   int copy_pdl = -1;            // DHS_OPT_COPY_PDL: -1 auto, 0 off, 1 on
   int resolve_paired = -1;      // DHS_OPT_RESOLVE_PAIRED: -1 auto, 0 off, 1 whenever it fits
   int copy_steal = -1;          // DHS_OPT_COPY_STEAL: -1 auto, 0 off, 1 on
@@ -823,6 +824,11 @@ int dhs_set_option(dhs_pool* pool, int32_t key, int64_t value) {
     pool->mark_polls = value < 0 ? dhs::kMarkPolls : (uint32_t)value;
     return DHS_OK;
   }
+  if (key == DHS_OPT_ATTEND_POLLS) {
+    if (value < -1 || value > (int64_t)dhs::kAttendPolls) return DHS_EINVAL;
+    pool->attend_polls = value < 0 ? dhs::kAttendPolls : (uint32_t)value;
+    return DHS_OK;
+  }
   return DHS_EINVAL;
 }
 
@@ -849,6 +855,7 @@ int dhs_get_option(dhs_pool* pool, int32_t key, int64_t* value) {
     case DHS_OPT_GATHER_TPC: *value = pool->gather_tpc; return DHS_OK;
     case DHS_OPT_STAGE_MISSES: *value = pool->stage_misses; return DHS_OK;
     case DHS_OPT_MARK_POLLS: *value = pool->mark_polls; return DHS_OK;
+    case DHS_OPT_ATTEND_POLLS: *value = pool->attend_polls; return DHS_OK;
     case DHS_OPT_COPY_PDL: *value = pool->copy_pdl; return DHS_OK;
     case DHS_OPT_RESOLVE_PAIRED: *value = pool->resolve_paired; return DHS_OK;
     case DHS_OPT_COPY_STEAL: *value = pool->copy_steal; return DHS_OK;
@@ -1837,6 +1844,7 @@ static int attend_tables(dhs_pool* p, const dhs_attend_step* st, dhs::AttendComm
   a.key_stride = st->kv_heads > 1 ? st->key_stride * 2 : 0;
   a.val_stride = st->kv_heads > 1 ? st->value_stride * 2 : 0;
   a.scale = st->scale;
+  a.polls = p->attend_polls;
   a.q_qs = st->q_query_stride * 2;
   a.q_hs = st->q_head_stride * 2;
   a.o_qs = st->out_query_stride * 2;

@@ -50,6 +50,7 @@ DHS_OPT_COPY_PDL = 9
 DHS_OPT_RESOLVE_PAIRED = 10
 DHS_OPT_COPY_STEAL = 11
 DHS_OPT_RESOLVE_CTAS = 12
+DHS_OPT_ATTEND_POLLS = 13
 DHS_BF16, DHS_F16 = 0, 1
 DHS_ATTEND_HISTORY = 1
 DHS_ATTEND_MAX_KEY, DHS_ATTEND_MAX_VALUE = 576, 512

@@ -91,7 +91,8 @@ enum {
 #define DHS_STATUS_ERANGE 1u  /* a selection held a row outside [0, L) */
 #define DHS_STATUS_EBUDGET 2u /* a resolve needed more victims than slots */
 #define DHS_STATUS_ELOC 4u    /* a gather location pointed outside its arena */
-#define DHS_STATUS_ETIMEDOUT 8u /* a bounded device wait gave up; its tile was skipped */
+#define DHS_STATUS_ETIMEDOUT 8u /* a bounded device wait gave up: a gather's tile was
+                                 * skipped, an attention's outputs hold no result */
 
 /* ------------------------------------------------------------ pool */
 typedef struct dhs_pool dhs_pool;
@@ -742,6 +743,12 @@ int dhs_read_state(dhs_pool *pool, int32_t req, int32_t src, int32_t *tags,
  * several items in turn); n > 0 = at most n CTAs, each resolving items b,
  * b + n, ... */
 #define DHS_OPT_RESOLVE_CTAS 12
+/* Polls of a barrier, at most 4 us each, before a block of the attention gives
+ * up (-1: the default, 2^22).  A launch that gives up raises
+ * DHS_STATUS_ETIMEDOUT; it reads and writes only what its step names, but its
+ * outputs and log-sums hold no result.  0: every launch gives up (to test what
+ * handles the status). */
+#define DHS_OPT_ATTEND_POLLS 13
 int dhs_set_option(dhs_pool *pool, int32_t key, int64_t value);
 /* The value in effect (DHS_OPT_FRESH_LIST: 0 or 1, the auto rule resolved
  * for the pool's current admissions).  DHS_EINVAL for an unknown key. */
