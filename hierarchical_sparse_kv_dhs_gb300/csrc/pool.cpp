@@ -24,7 +24,6 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
-#include <functional>
 #include <new>
 #include <vector>
 
@@ -439,6 +438,53 @@ int enter_step(dhs_pool* p, const dhs_step* st) {
   return rc;
 }
 
+// Room for n elements in all, so that adding them cannot throw.
+template <class T>
+bool room(std::vector<T>& v, size_t n) {
+  try {
+    v.reserve(n);
+  } catch (...) {
+    return false;
+  }
+  return true;
+}
+
+// Run `launch` on a caller's stream: after everything the pool's stream holds,
+// and joined by the pool's next call that can change rows.
+template <class Launch>
+int on_stream(dhs_pool* p, void* stream, Launch launch) {
+  cudaStream_t other = (cudaStream_t)stream;
+  cudaEvent_t done = nullptr;
+  // the events come back to ev_free when they are joined
+  const size_t gathers = p->ev_gathers.size() + 1;
+  if (!room(p->ev_gathers, gathers) || !room(p->ev_free, p->ev_free.size() + gathers))
+    return DHS_ENOMEM;
+  if (!p->ev_free.empty()) {
+    done = p->ev_free.back();
+    p->ev_free.pop_back();
+  } else if (cudaEventCreateWithFlags(&done, cudaEventDisableTiming) != cudaSuccess) {
+    return DHS_ECUDA;
+  }
+  // after everything the pool's stream holds (resolves, copies, appends)
+  if (cudaEventRecord(p->ev_main, p->stream) != cudaSuccess ||
+      cudaStreamWaitEvent(other, p->ev_main, 0) != cudaSuccess) {
+    p->ev_free.push_back(done);
+    return DHS_ECUDA;
+  }
+  cudaStream_t main = p->stream;
+  p->stream = other;
+  const int rc = launch();
+  p->stream = main;
+  // joined before the pool's next call that can change rows, even if the
+  // launch failed part way
+  if (cudaEventRecord(done, other) != cudaSuccess) {
+    p->ev_free.push_back(done);
+    return DHS_ECUDA;
+  }
+  p->ev_gathers.push_back(done);
+  return rc;
+}
+
 void mark_dirty(dhs_pool* p, int64_t pair) {
   p->dirty_lo = std::min(p->dirty_lo, pair);
   p->dirty_hi = std::max(p->dirty_hi, pair);
@@ -451,6 +497,9 @@ int flush(dhs_pool* p) {
   const size_t page_bytes = (size_t)c.page_rows * c.row_bytes;
   if (p->any_pending) {
     p->moves.clear();
+    size_t pages = 0;
+    for (const PairState& s : p->ps) pages += s.pending.size();
+    if (small_pages(p) && !room(p->moves, pages)) return DHS_ENOMEM;
     for (int64_t pair = 0; pair < p->pairs; ++pair) {
       PairState& s = p->ps[pair];
       if (s.pending.empty()) continue;
@@ -553,7 +602,8 @@ int64_t lowest_free_slot(dhs_pool* p) {
 
 // Free every optional page of pair; returns pages freed.
 // Queue the device-to-host copy of one resident page whose backup was
-// deferred (p->moves; launched by run_moves) and mark it backed.
+// deferred (p->moves, which has room; launched by run_moves) and mark it
+// backed.
 int backup_page(dhs_pool* p, int64_t pair, int64_t q) {
   PairState& s = p->ps[pair];
   const dhs_pool_config& c = p->cfg;
@@ -891,6 +941,7 @@ int dhs_admit(dhs_pool* p, int32_t req, int32_t src, void* host_rows, int64_t n_
     if (deficit) *deficit = p->used + want - usable;
     return DHS_EWOULDWAIT;
   }
+  if (!room(s.pending, (size_t)want)) return DHS_ENOMEM;
   // tail ring <- rows [max(0, N-T), N)
   const int64_t T = c.tail_rows, rb = c.row_bytes;
   const int64_t lo = std::max<int64_t>(0, n_rows - T);
@@ -956,6 +1007,12 @@ int dhs_admit_device(dhs_pool* p, int32_t req, int32_t src, const void* dev_rows
     if (deficit) *deficit = p->used + want - usable;
     return DHS_EWOULDWAIT;
   }
+  try {
+    reserve_backup(p, (size_t)want);
+    s.backup.assign((size_t)p->pmax, 0);
+  } catch (...) {
+    return DHS_ENOMEM;
+  }
   // the copies are enqueued now; the page map reaches the device at the next
   // flush, after them in stream order
   const int64_t T = c.tail_rows, rb = c.row_bytes, PR = c.page_rows;
@@ -975,8 +1032,6 @@ int dhs_admit_device(dhs_pool* p, int32_t req, int32_t src, const void* dev_rows
     row += run;
   }
   int32_t* pm = p->map_host.data() + pair * p->pmax;
-  reserve_backup(p, (size_t)want);
-  s.backup.assign((size_t)p->pmax, 0);
   for (int64_t q = 0; q < complete; ++q) {
     if (mask && !mask[q]) continue;
     const int64_t slot = lowest_free_slot(p);
@@ -1023,6 +1078,8 @@ int dhs_backup(dhs_pool* p, int64_t max_pages, int64_t* done) {
   int rc = enter(p);
   if (rc) return rc;
   p->moves.clear();
+  if (small_pages(p) && !room(p->moves, (size_t)std::min(max_pages, p->backup_live)))
+    return DHS_ENOMEM;
   int64_t n = 0;
   while (n < max_pages && p->backup_live > 0) {
     BackupRun& r = p->backup_queue[p->backup_head];
@@ -1081,7 +1138,8 @@ int dhs_refill(dhs_pool* p, int64_t max_pages, int64_t* filled) {
   const int64_t usable = p->capacity - c.admission_reserve_pages;
   int64_t n = 0, idle = 0;
   int32_t r = p->rr;
-  while (n < max_pages && p->used < usable && idle < c.max_requests) {
+  int rc = DHS_OK;
+  while (!rc && n < max_pages && p->used < usable && idle < c.max_requests) {
     bool found = false;
     for (int32_t src = 0; src < c.sources && !found; ++src) {
       const int64_t pair = (int64_t)r * c.sources + src;
@@ -1090,17 +1148,24 @@ int dhs_refill(dhs_pool* p, int64_t max_pages, int64_t* filled) {
       int32_t* pm = p->map_host.data() + pair * p->pmax;
       for (int64_t q = 0; q < s.N / c.page_rows && !found; ++q) {
         if (pm[q] >= 0) continue;
+        try {
+          s.pending.push_back((int32_t)q);  // copied from the host copy at flush
+        } catch (...) {
+          rc = DHS_ENOMEM;
+          break;
+        }
         const int64_t slot = lowest_free_slot(p);
         p->slot_pair[slot] = (int32_t)pair;
         p->slot_page[slot] = (int32_t)q;
         p->used += 1;
         pm[q] = (int32_t)slot;
-        s.pending.push_back((int32_t)q);  // copied from the host copy at flush
         p->any_pending = true;
         mark_dirty(p, pair);
         found = true;
       }
+      if (rc) break;
     }
+    if (rc) break;
     if (found) {
       ++n;
       idle = 0;
@@ -1111,7 +1176,7 @@ int dhs_refill(dhs_pool* p, int64_t max_pages, int64_t* filled) {
   }
   p->rr = r;
   if (filled) *filled = n;
-  return DHS_OK;
+  return n ? DHS_OK : rc;  // fewer pages than asked for are filled ones too
 }
 
 int dhs_reclaim(dhs_pool* p, const int32_t* order, int32_t n, int64_t deficit,
@@ -1121,7 +1186,9 @@ int dhs_reclaim(dhs_pool* p, const int32_t* order, int32_t n, int64_t deficit,
   for (int32_t i = 0; i < n; ++i)
     if (order[i] < 0 || order[i] >= p->cfg.max_requests) return DHS_EINVAL;
   int64_t avail = 0;
-  std::vector<uint8_t> counted((size_t)p->cfg.max_requests, 0);
+  std::vector<uint8_t> counted;
+  if (!room(counted, (size_t)p->cfg.max_requests)) return DHS_ENOMEM;
+  counted.assign((size_t)p->cfg.max_requests, 0);
   for (int32_t i = 0; i < n; ++i) {
     if (counted[order[i]]) continue;
     counted[order[i]] = 1;
@@ -1131,6 +1198,7 @@ int dhs_reclaim(dhs_pool* p, const int32_t* order, int32_t n, int64_t deficit,
   int rc = enter(p);
   if (rc) return rc;
   p->moves.clear();
+  if (small_pages(p) && !room(p->moves, (size_t)p->backup_live)) return DHS_ENOMEM;
   int64_t got = 0;
   for (int32_t i = 0; i < n && got < deficit; ++i)
     for (int32_t s = 0; s < p->cfg.sources; ++s) {
@@ -1183,6 +1251,7 @@ int dhs_append(dhs_pool* p, const dhs_append_item* items, int32_t n_items) {
     if (!s.admitted) return DHS_ESTATE;
     if (s.L + it.count > c.max_rows_per_request) return DHS_EINVAL;
   }
+  if (!room(p->aitems, (size_t)n_items)) return DHS_ENOMEM;
   int rc = enter(p);
   if (rc) return rc;
   p->aitems.clear();
@@ -1212,6 +1281,7 @@ int dhs_append(dhs_pool* p, const dhs_append_item* items, int32_t n_items) {
   return DHS_OK;
 }
 
+// Also makes room for the step's tables, so that its launches cannot throw.
 static int validate_step(dhs_pool* p, const dhs_step* st, bool resolving) {
   if (!p || !st || st->n_items < 0 || (st->n_items > 0 && !st->items)) return DHS_EINVAL;
   if (resolving && st->step == 0) return DHS_EINVAL;
@@ -1239,6 +1309,10 @@ static int validate_step(dhs_pool* p, const dhs_step* st, bool resolving) {
     p->seen[pair] = 1;
     if (!p->ps[pair].admitted) return DHS_ESTATE;
   }
+  const size_t n = (size_t)st->n_items;
+  if (!room(p->ritems, n) || !room(p->citems, n) || !room(p->staged_item, n) ||
+      !room(p->loc_keys, n) || !room(p->gitems, n))
+    return DHS_ENOMEM;
   return DHS_OK;
 }
 
@@ -1575,43 +1649,6 @@ int dhs_gather(dhs_pool* p, const dhs_step* st) {
   if ((rc = enter_gather(p, st))) return rc;
   if ((rc = flush(p))) return rc;
   return launch_gathers(p, st, false);
-}
-
-// Run `launch` on a caller's stream: after everything the pool's stream holds,
-// and joined by the pool's next call that can change rows.
-static int on_stream(dhs_pool* p, void* stream, const std::function<int()>& launch) {
-  cudaStream_t other = (cudaStream_t)stream;
-  cudaEvent_t done = nullptr;
-  try {
-    p->ev_gathers.reserve(p->ev_gathers.size() + 1);
-    p->ev_free.reserve(p->ev_free.size() + p->ev_gathers.size() + 1);
-  } catch (...) {
-    return DHS_ENOMEM;
-  }
-  if (!p->ev_free.empty()) {
-    done = p->ev_free.back();
-    p->ev_free.pop_back();
-  } else if (cudaEventCreateWithFlags(&done, cudaEventDisableTiming) != cudaSuccess) {
-    return DHS_ECUDA;
-  }
-  // after everything the pool's stream holds (resolves, copies, appends)
-  if (cudaEventRecord(p->ev_main, p->stream) != cudaSuccess ||
-      cudaStreamWaitEvent(other, p->ev_main, 0) != cudaSuccess) {
-    p->ev_free.push_back(done);
-    return DHS_ECUDA;
-  }
-  cudaStream_t main = p->stream;
-  p->stream = other;
-  const int rc = launch();
-  p->stream = main;
-  // joined before the pool's next call that can change rows, even if the
-  // launch failed part way
-  if (cudaEventRecord(done, other) != cudaSuccess) {
-    p->ev_free.push_back(done);
-    return DHS_ECUDA;
-  }
-  p->ev_gathers.push_back(done);
-  return rc;
 }
 
 int dhs_gather_on(dhs_pool* p, const dhs_step* st, void* stream) {
@@ -2122,11 +2159,7 @@ int dhs_compact(dhs_pool* p, int64_t capacity, int64_t* moved) {
   int64_t n = 0;
   for (int64_t i = capacity; i < p->capacity; ++i) n += p->slot_pair[i] >= 0;
   p->runs.clear();
-  try {
-    p->runs.reserve(n);
-  } catch (...) {
-    return DHS_ENOMEM;
-  }
+  if (!room(p->runs, (size_t)n)) return DHS_ENOMEM;
   int64_t to = p->first_free;
   for (int64_t i = capacity; i < p->capacity; ++i) {
     if (p->slot_pair[i] < 0) continue;

@@ -13,7 +13,8 @@
  *
  * Conventions for every call:
  *   - Return value: DHS_OK (0) or a negative DHS_E* code.  No call throws,
- *     aborts or prints.  A call that fails validation changes nothing.
+ *     aborts or prints.  A call that fails validation changes nothing, and
+ *     after DHS_ENOMEM the same call may be made again.
  *   - Device work is asynchronous and ordered on the pool's stream; no call
  *     on the hot path (dhs_append, dhs_resolve, dhs_gather,
  *     dhs_resolve_gather) synchronises the host.

@@ -157,7 +157,7 @@ struct Host {
   dhs_pool_config c{};
   int64_t pmax;
   std::map<int, uint8_t*> rows;  // host rows of each pair
-  std::vector<uint8_t> dev;
+  std::vector<uint8_t> dev, mask[2];  // prefilled rows; no page resident, every page
 
   Host(int requests, int sources, int64_t max_rows, int64_t pages) {
     c.max_requests = requests;
@@ -181,12 +181,12 @@ struct Host {
     pmax = (max_rows + kPage - 1) / kPage;
     for (int i = 0; i < requests * sources; ++i) rows[i] = (uint8_t*)zeros(max_rows * kRow);
     dev.assign(max_rows * kRow, 1);
+    for (int i = 0; i < 2; ++i) mask[i].assign(pmax, i);
   }
   ~Host() { dhs_pool_destroy(p); }
   int admit(int req, int src, int64_t n, bool resident) {
-    std::vector<uint8_t> mask(n / kPage + 1, resident);
-    return dhs_admit_device(p, req, src, dev.data(), rows[req * c.sources + src], n, mask.data(),
-                            nullptr);
+    return dhs_admit_device(p, req, src, dev.data(), rows[req * c.sources + src], n,
+                            mask[resident].data(), nullptr);
   }
   int fork(int req, int child) {
     std::vector<void*> h;
@@ -280,6 +280,106 @@ static void fork_table_limits() {
     }
 }
 
+// Everything of a pool's state that calls change, the device's maps included.
+static std::vector<int64_t> state(Host& h) {
+  CHECK(dhs_flush(h.p) == DHS_OK);
+  std::vector<int64_t> all{dhs_pool_used(h.p), dhs_pending_backup(h.p), dhs_pool_capacity(h.p)};
+  for (int r = 0; r < h.c.max_requests; ++r)
+    for (int s = 0; s < h.c.sources; ++s) {
+      int64_t info[4];
+      CHECK(dhs_read_state(h.p, r, s, nullptr, nullptr, nullptr, info) == DHS_OK);
+      all.insert(all.end(), info, info + 3);
+      for (int32_t x : h.slots(r, s)) all.push_back(x);
+      if (info[2]) CHECK(h.device_slots(r, s) == h.slots(r, s));
+    }
+  return all;
+}
+
+// Each call with its allocations failing one after the other: DHS_ENOMEM and
+// no exception, and the same call then leaves what it would have left.
+static void calls_without_memory() {
+  const int kCalls = 18;
+  for (int k = 0; k < kCalls; ++k) {
+    std::vector<int64_t> want;
+    for (int n = -1;; ++n) {  // -1: nothing fails
+      Host h(4, 2, 64, 40);
+      for (int s = 0; s < 2; ++s) CHECK(h.admit(0, s, 40, true) == DHS_OK);
+      CHECK(h.admit(1, 0, 40, false) == DHS_OK);
+      CHECK(dhs_flush(h.p) == DHS_OK);
+      // pages still to be copied, and some whose backup is deferred
+      const auto admit_host = [&](int req) {
+        return dhs_admit(h.p, req, 0, h.rows[req * 2], 20, nullptr, nullptr);
+      };
+      CHECK(admit_host(2) == DHS_OK);
+      int32_t sel[4] = {0, 1, 2, 3};
+      uint32_t loc[4] = {};
+      alignas(16) uint8_t row[kRow] = {};
+      dhs_item it[3]{};
+      for (int i = 0; i < 3; ++i) {
+        it[i].req = i;
+        it[i].queries = 1;
+        it[i].topk = 4;
+        it[i].sel_dev = sel;
+        it[i].loc_dev = loc;
+        it[i].staging_dev = h.c.tail_dev;
+      }
+      const dhs_step st{1, 3, it};
+      dhs_append_item ap[3]{};
+      for (int i = 0; i < 3; ++i) {
+        ap[i].req = i;
+        ap[i].count = 1;
+        ap[i].rows_dev = row;
+      }
+      const int32_t order[2] = {0, 1};
+      int64_t x = 0, filled = 0;
+      const auto call = [&]() -> int {
+        switch (k) {
+          case 0: return admit_host(3);
+          case 1: return h.admit(3, 1, 40, true);
+          case 2: return dhs_admit_window(h.p, 3, 0, h.c.tail_dev, 9);
+          case 3: return dhs_backup(h.p, 7, &x);
+          case 4:
+            for (int rc; filled < 5; filled += x)
+              if ((rc = dhs_refill(h.p, 5 - filled, &x))) return rc;
+            return DHS_OK;
+          case 5: return dhs_reclaim(h.p, order, 2, 12, &x);
+          case 6: return dhs_release(h.p, 0);
+          case 7: return dhs_flush(h.p);
+          case 8: return dhs_append(h.p, ap, 3);
+          case 9: return dhs_resolve(h.p, &st);
+          case 10: return dhs_gather(h.p, &st);
+          case 11: return dhs_gather_on(h.p, &st, (void*)0x200);
+          case 12: return dhs_resolve_gather(h.p, &st);
+          case 13: return dhs_decode_step(h.p, ap, 3, &st);
+          case 14: return dhs_prefetch(h.p, &st, (void*)0x200);
+          case 15: return h.attend(0, 1);
+          case 16: return h.attend(0, 1, (void*)0x200);
+          default: return dhs_compact(h.p, dhs_pool_used(h.p), &x);
+        }
+      };
+      if (n < 0) {
+        CHECK(call() == DHS_OK);
+        want = state(h);
+        continue;
+      }
+      g_failed = false;
+      g_fail = n;
+      int rc = 1;
+      try {
+        rc = call();
+      } catch (...) {
+      }
+      g_fail = -1;
+      if (k == 4 && g_failed && rc == DHS_OK) rc = DHS_ENOMEM;  // filled in two calls
+      if (rc != (g_failed ? DHS_ENOMEM : DHS_OK)) std::printf("call %d, allocation %d: %d\n", k, n, rc);
+      CHECK(rc == (g_failed ? DHS_ENOMEM : DHS_OK));
+      if (g_failed) CHECK(call() == DHS_OK);
+      CHECK(state(h) == want);
+      if (!g_failed) break;
+    }
+  }
+}
+
 int main(int argc, char** argv) {
   std::vector<std::string> log;
   g_log = &log;
@@ -287,6 +387,7 @@ int main(int argc, char** argv) {
       {"fork_of_fewer_sources", fork_of_fewer_sources},
       {"fork_without_memory", fork_without_memory},
       {"fork_table_limits", fork_table_limits},
+      {"calls_without_memory", calls_without_memory},
   };
   const auto f = all.find(argc > 1 ? argv[1] : "");
   if (f == all.end()) return 2;

@@ -18,7 +18,7 @@ def program(tmp_path_factory):
     if not os.path.exists(os.path.join(cuda, "cuda_runtime.h")):
         pytest.skip("no CUDA headers")
     exe = str(tmp_path_factory.mktemp("pool_host") / "pool_host")
-    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-I", os.path.join(PKG, "csrc"),
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-Wno-mismatched-new-delete", "-I", os.path.join(PKG, "csrc"),
                     "-I", os.path.join(os.path.dirname(HERE), "include"), "-I", cuda,
                     os.path.join(HERE, "pool_host.cpp"), os.path.join(PKG, "csrc", "pool.cpp"),
                     "-o", exe], check=True)
@@ -26,7 +26,7 @@ def program(tmp_path_factory):
 
 
 @pytest.mark.parametrize("scenario", ["fork_of_fewer_sources", "fork_without_memory",
-                                      "fork_table_limits"])
+                                      "fork_table_limits", "calls_without_memory"])
 def test_scenario(program, scenario):
     r = subprocess.run([program, scenario], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout == "ok\n", r.stdout + r.stderr
