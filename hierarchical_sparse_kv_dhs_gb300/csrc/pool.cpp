@@ -251,6 +251,7 @@ struct dhs_pool {
   // resolve / append / admission may change; one event per such call,
   // joined (and recycled) by the pool's next call that can change rows
   std::vector<cudaEvent_t> ev_free, ev_gathers;
+  bool map_readers = false;  // some of them read the page maps (histories)
   ~dhs_pool() {
     if (ev_main) cudaEventDestroy(ev_main);
     if (ev_prefetch) cudaEventDestroy(ev_prefetch);
@@ -395,6 +396,17 @@ bool small_pages(const dhs_pool* p) {
   return (int64_t)p->cfg.page_rows * p->cfg.row_bytes <= ((int64_t)1 << 24);
 }
 
+// The pool's stream waits for the reads that run on other streams.
+int join_readers(dhs_pool* p) {
+  for (cudaEvent_t e : p->ev_gathers) {
+    if (cudaStreamWaitEvent(p->stream, e, 0) != cudaSuccess) return DHS_ECUDA;
+    p->ev_free.push_back(e);
+  }
+  p->ev_gathers.clear();
+  p->map_readers = false;
+  return DHS_OK;
+}
+
 // Every call that enqueues device work starts here: the pool's device, and
 // the pool's stream ordered after an outstanding dhs_prefetch.
 int enter(dhs_pool* p) {
@@ -406,13 +418,7 @@ int enter(dhs_pool* p) {
     p->prefetch_pending = false;
     std::fill(p->pf_pair.begin(), p->pf_pair.end(), 0);
   }
-  if (!p->join_gathers) return DHS_OK;
-  for (cudaEvent_t e : p->ev_gathers) {
-    if (cudaStreamWaitEvent(p->stream, e, 0) != cudaSuccess) return DHS_ECUDA;
-    p->ev_free.push_back(e);
-  }
-  p->ev_gathers.clear();
-  return DHS_OK;
+  return p->join_gathers ? join_readers(p) : DHS_OK;
 }
 
 // enter() for a resolve or gather of `st`: the outstanding prefetch is
@@ -491,9 +497,14 @@ void mark_dirty(dhs_pool* p, int64_t pair) {
 }
 
 // Copy pending resident pages (coalescing runs of consecutive pages in
-// consecutive slots) and upload changed page maps, in stream order.
+// consecutive slots) and upload changed page maps, in stream order and after
+// the attention to histories on other streams, which reads the maps.
 int flush(dhs_pool* p) {
   const dhs_pool_config& c = p->cfg;
+  if (p->map_readers && (p->any_pending || p->dirty_hi >= 0)) {
+    const int rc = join_readers(p);
+    if (rc) return rc;
+  }
   const size_t page_bytes = (size_t)c.page_rows * c.row_bytes;
   if (p->any_pending) {
     p->moves.clear();
@@ -1997,6 +2008,7 @@ int dhs_attend_on(dhs_pool* p, const dhs_attend_step* st, void* stream) {
   if (rc) return rc;
   if ((rc = enter_attend(p))) return rc;
   if ((rc = flush(p))) return rc;
+  for (const dhs::AttendItem& it : p->titems) p->map_readers |= !it.loc;
   return on_stream(p, stream, [&] { return launch_attends(p, st, a); });
 }
 

@@ -380,6 +380,35 @@ static void calls_without_memory() {
   }
 }
 
+// A refill flushed while an attention to a history runs on another stream: the
+// map that it reads is replaced behind it, and nothing else waits for it.
+static void flush_behind_side_attention() {
+  Host h(2, 1, 64, 40);
+  CHECK(h.admit(0, 0, 40, false) == DHS_OK);
+  CHECK(dhs_flush(h.p) == DHS_OK);
+  int64_t n = 0;
+  const auto waits = [] {
+    int k = 0;
+    for (const std::string& s : *g_log)
+      k += s.compare(0, 4, "wait") == 0 && s.find("on 0x100") != std::string::npos;
+    return k;
+  };
+  for (int flushed = 0; flushed < 2; ++flushed) {
+    CHECK(h.attend(0, 0, (void*)0x200) == DHS_OK);
+    if (flushed) CHECK(dhs_refill(h.p, 3, &n) == DHS_OK && n == 3);
+    g_log->clear();
+    CHECK(h.attend(0, 0) == DHS_OK);
+    CHECK((waits() > 0) == flushed);
+    const auto first = [](const char* what) {
+      size_t i = 0;
+      while (i < g_log->size() && (*g_log)[i].compare(0, strlen(what), what)) ++i;
+      return i;
+    };
+    if (flushed) CHECK(first("wait") < first("moves") && first("wait") < first("copy"));
+  }
+  CHECK(h.device_slots(0, 0) == h.slots(0, 0));
+}
+
 int main(int argc, char** argv) {
   std::vector<std::string> log;
   g_log = &log;
@@ -388,6 +417,7 @@ int main(int argc, char** argv) {
       {"fork_without_memory", fork_without_memory},
       {"fork_table_limits", fork_table_limits},
       {"calls_without_memory", calls_without_memory},
+      {"flush_behind_side_attention", flush_behind_side_attention},
   };
   const auto f = all.find(argc > 1 ? argv[1] : "");
   if (f == all.end()) return 2;

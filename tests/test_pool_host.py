@@ -26,7 +26,8 @@ def program(tmp_path_factory):
 
 
 @pytest.mark.parametrize("scenario", ["fork_of_fewer_sources", "fork_without_memory",
-                                      "fork_table_limits", "calls_without_memory"])
+                                      "fork_table_limits", "calls_without_memory",
+                                      "flush_behind_side_attention"])
 def test_scenario(program, scenario):
     r = subprocess.run([program, scenario], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout == "ok\n", r.stdout + r.stderr
