@@ -439,6 +439,8 @@ class Pool:
         for a, s in zip(given, sizes):
             if a.dtype != torch.uint8 or not a.is_contiguous() or a.numel() < s:
                 raise ValueError(f"an arena of {s} contiguous bytes is needed")
+            if a.device != self.device:
+                raise ValueError(f"an arena on {self.device} is needed, not on {a.device}")
         self.buffers = given + [torch.empty(max(s, 256), dtype=torch.uint8, device=self.device)
                                 for s in sizes[len(given):]]
         cfg.hot_dev, cfg.tail_dev, cfg.opt_dev, cfg.meta_dev = [
