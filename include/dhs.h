@@ -583,9 +583,11 @@ typedef struct {
 } dhs_attend_step;
 
 /* Bytes of work_dev that dhs_attend needs for `st` now (history items: at
- * the sources' present lengths).  Pool and
- * step are validated as in dhs_attend, except for work_dev.  Host
- * arithmetic only.  Errors: as dhs_attend. */
+ * the sources' present lengths).  They change with the lengths, but never
+ * pass 512 * (value_elems + 2) for each SM of the GPU: a workspace of that
+ * size serves every step of these heads.  Pool and step are validated as in
+ * dhs_attend, except for work_dev.  Host arithmetic only.  Errors: as
+ * dhs_attend. */
 int dhs_attend_bytes(dhs_pool *pool, const dhs_attend_step *st, size_t *bytes);
 
 /*
@@ -597,8 +599,10 @@ int dhs_attend_bytes(dhs_pool *pool, const dhs_attend_step *st, size_t *bytes);
  * It reads rows where they lie, so a step that attends needs no staging and
  * no dhs_gather.  Scores, sums and outputs are accumulated in float; the
  * weights p_j are rounded to `dtype` for the second product, out once more.
- * Asynchronous, in order on the pool's stream; results do not depend on how
- * the rows were split (no atomics), only on the GPU's number of SMs.
+ * Asynchronous, in order on the pool's stream.  No atomics: the same step
+ * with the same lengths gives the same bits on every GPU of as many SMs.  How
+ * an item's rows are split, and with it the last bits of its sums, depends on
+ * the step's other items too, so an item alone may differ in them.
  * Errors: DHS_EINVAL (arguments, sizes, alignment, workspace), DHS_ESTATE
  * (history of a source that is not admitted), DHS_ECUDA.
  */
