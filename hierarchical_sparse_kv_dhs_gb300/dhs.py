@@ -136,6 +136,7 @@ def _load():
         "dhs_resolve": (ctypes.c_int, [_vp, P(dhs_step)]),
         "dhs_gather": (ctypes.c_int, [_vp, P(dhs_step)]),
         "dhs_resolve_gather": (ctypes.c_int, [_vp, P(dhs_step)]),
+        "dhs_resolve_noalloc": (ctypes.c_int, [_vp, P(dhs_step)]),
         "dhs_decode_step": (ctypes.c_int, [_vp, P(dhs_append_item), _i32, P(dhs_step)]),
         "dhs_attend_bytes": (ctypes.c_int, [_vp, P(dhs_attend_step), P(ctypes.c_size_t)]),
         "dhs_attend": (ctypes.c_int, [_vp, P(dhs_attend_step)]),
