@@ -319,7 +319,7 @@ __device__ __forceinline__ int item_at(const AttendParams<MAXI>& P, int32_t t) {
 
 // The segment that begins at tile `t` of the launch and ends before `te`.
 // Called by whole warps.
-template <int N, int MAXI>
+template <int MAXI>
 __device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te) {
   const AttendCommon& c = P.c;
   __syncwarp();
@@ -381,7 +381,7 @@ __device__ __forceinline__ Walk first_of(const AttendParams<MAXI>& P) {
   const AttendCommon& c = P.c;
   return {0, first_tile(c, blockIdx.x), first_tile(c, blockIdx.x + 1)};
 }
-template <int N, int MAXI>
+template <int MAXI>
 __device__ bool next_segment(const AttendParams<MAXI>& P, Walk& w, Segment& s) {
   const AttendCommon& c = P.c;
   int32_t t = w.t, te = w.te;
@@ -393,7 +393,7 @@ __device__ bool next_segment(const AttendParams<MAXI>& P, Walk& w, Segment& s) {
   } else if (t >= te) {
     return false;
   }
-  s = segment_at<N>(P, t, te);
+  s = segment_at(P, t, te);
   if (!wave) w.t += s.t1 - s.t0;
   return true;
 }
@@ -625,7 +625,7 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
 // Finding warp: the block's segments, ahead of the others, who read them from
 // shared memory.  One without columns ends the walk.  The first one is found
 // while the block sets up.
-template <int N, int MAXI>
+template <int MAXI>
 __device__ void find_segments(const AttendParams<MAXI>& P, Control& ctl) {
   const Patience until{&ctl.gave_up, P.c.polls};
   Ring seg;
@@ -634,7 +634,7 @@ __device__ void find_segments(const AttendParams<MAXI>& P, Control& ctl) {
 #pragma unroll 1
   for (bool begin = true; more; begin = false) {
     Segment s;
-    more = next_segment<N>(P, w, s);
+    more = next_segment(P, w, s);
     if (begin) __syncthreads();
     if (!more) s.cols = 0;
     warp_wait(smem_u32(&ctl.segempty[seg.slot]), seg.phase ^ 1, until);
@@ -648,7 +648,7 @@ __device__ void find_segments(const AttendParams<MAXI>& P, Control& ctl) {
 }
 
 // Row warps: the addresses of every tile's rows, ahead of the loading warps.
-template <int N, int MAXI>
+template <int MAXI>
 __device__ void find_rows(const AttendParams<MAXI>& P, Control& ctl, int tid) {
   constexpr int R = kTile / kRowThreads;
   const AttendCommon& c = P.c;
@@ -1256,7 +1256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (warp == kFindWarp) {
-    find_segments<N>(P, ctl);  // meets the others' barrier inside
+    find_segments(P, ctl);  // meets the others' barrier inside
   } else {
     tc_before();
     __syncthreads();
@@ -1264,7 +1264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kSoftThreads / 32) softmax_rows<N, SHARED>(P, sm, ctl, tid, parts);
     else if (warp < kIssueWarp) load_rows<N, SHARED>(P, sm, ctl, tid - kSoftThreads);
     else if (warp == kIssueWarp) issue_products<N, SHARED>(P, sm, ctl);
-    else find_rows<N>(P, ctl, tid - 32 * kRowWarp);
+    else find_rows(P, ctl, tid - 32 * kRowWarp);
   }
   __syncwarp();
   tc_before();

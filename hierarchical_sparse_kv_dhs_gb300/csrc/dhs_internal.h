@@ -289,7 +289,6 @@ cudaError_t gather_set_smem_limit(int row_bytes, int optin, bool* tma_ok);
 
 // ------------------------------------------------------------ attention
 constexpr int kAttendItemsLarge = 240, kAttendItemsSmall = 16;
-constexpr int kAttendMaxKey = 576, kAttendMaxValue = 512;
 
 struct alignas(16) AttendItem {
   const uint8_t* q;
