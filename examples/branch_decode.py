@@ -28,9 +28,9 @@ SCALE = KEY ** -0.5
 class Serving:
     """A one-source pool of latent rows (the value is the key's beginning)."""
 
-    def __init__(self, requests, rows, seed=0):
+    def __init__(self, requests, rows, steps, seed=0):
         self.g = torch.Generator("cuda").manual_seed(seed)
-        self.max_rows = rows + 256
+        self.max_rows = rows + steps
         self.pool = dhs.Pool(max_requests=requests, sources=1, row_bytes=2 * KEY, page_rows=64,
                              tail_rows=128, hot_rows=2048, max_queries=QUERIES, max_topk=TOPK,
                              max_rows_per_request=self.max_rows, optional_pages=3 * rows // 64)
@@ -134,7 +134,7 @@ def main(argv=None):
     a = ap.parse_args(argv)
     if a.rows < TOPK:
         ap.error("--rows: at least %d" % TOPK)
-    s = Serving(requests=3, rows=a.rows)
+    s = Serving(requests=3, rows=a.rows, steps=max(0, a.steps))
     s.admit(1, max(TOPK, a.rows // 2))
     s.admit(0, a.rows)
     s.dense(a.check)
