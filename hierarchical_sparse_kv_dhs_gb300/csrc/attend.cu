@@ -59,7 +59,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <type_traits>
+#include <atomic>
 
 #include "dhs_internal.h"
 
@@ -1570,16 +1570,43 @@ cudaError_t launch_merge(const AttendCommon& c, const Shape& s, const float* par
   return cudaLaunchKernelEx(&cfg, merge_kernel, M, parts);
 }
 
-template <int N, int MAXI>
-cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
-  // A kernel for each kind of layout: with one that asked at run time, both
-  // were slower (128 heads 172 us instead of 166, grouped heads 55.7 instead
-  // of 54.4).
-  if (P.plan.shared) attend_kernel<N, true><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
-  else attend_kernel<N, false><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
-  cudaError_t e = cudaGetLastError();
+// Lets a kernel's blocks use all of an SM's shared memory: once on each device,
+// with its first launch there.  (The driver loads a kernel when it is first
+// named.  Pools that named all 16 of these when they were made took 1 ms more
+// for that, and their resolve and gather kernels, loaded around them, ran 25.2
+// us a step of 8 items with one build of this file and 24.7 with another;
+// without them 24.8 with either.)
+template <int N, bool SHARED, int MAXI>
+cudaError_t use_all_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(attend_kernel<N, SHARED, MAXI>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <int N, bool SHARED, int MAXI>
+cudaError_t launch_kernel(const AttendParams<MAXI>& P, const Shape& s, float* parts,
+                          cudaStream_t stream) {
+  cudaError_t e = use_all_smem<N, SHARED, MAXI>();
+  if (e != cudaSuccess) return e;
+  attend_kernel<N, SHARED><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
+  e = cudaGetLastError();
   if (e != cudaSuccess || !s.n_cut) return e;
   return launch_merge(P.c, s, parts, stream);
+}
+
+// A kernel for each kind of layout: with one that asked at run time, both were
+// slower (128 heads 172 us instead of 166, grouped heads 55.7 instead of 54.4).
+template <int N, int MAXI>
+cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
+  return P.plan.shared ? launch_kernel<N, true, MAXI>(P, s, parts, stream)
+                       : launch_kernel<N, false, MAXI>(P, s, parts, stream);
 }
 
 template <int MAXI>
@@ -1599,25 +1626,6 @@ cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items
 }
 
 }  // namespace
-
-cudaError_t attend_set_smem_limit() {
-  auto of = [](auto n) {
-    constexpr int N = decltype(n)::value;
-    cudaError_t e = cudaSuccess;
-    for (const void* k : {(const void*)attend_kernel<N, false, kAttendItemsSmall>,
-                          (const void*)attend_kernel<N, true, kAttendItemsSmall>,
-                          (const void*)attend_kernel<N, false, kAttendItemsLarge>,
-                          (const void*)attend_kernel<N, true, kAttendItemsLarge>})
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-    return e;
-  };
-  cudaError_t e = of(std::integral_constant<int, 16>{});
-  if (e == cudaSuccess) e = of(std::integral_constant<int, 32>{});
-  if (e == cudaSuccess) e = of(std::integral_constant<int, 48>{});
-  if (e == cudaSuccess) e = of(std::integral_constant<int, 64>{});
-  return e;
-}
 
 bool attend_shape(AttendCommon c, AttendItem* items, int n_items, int sms, size_t* bytes) {
   const Shape s = shape_of(c, items, n_items, sms);

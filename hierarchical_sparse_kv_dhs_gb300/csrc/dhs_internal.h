@@ -330,8 +330,6 @@ struct AttendCommon {
 constexpr int kAttendMaxBlocks = 256;
 constexpr uint32_t kAttendPolls = 1u << 22;  // DHS_OPT_ATTEND_POLLS default
 
-// Once per device: let the attention's blocks use all of an SM's shared memory.
-cudaError_t attend_set_smem_limit();
 // Workspace of a launch; fills in the items' tiles.  False: too many tiles.
 bool attend_shape(AttendCommon c, AttendItem* items, int n_items, int sms, size_t* bytes);
 cudaError_t launch_attend(AttendCommon c, AttendItem* items, int n_items, int sms,

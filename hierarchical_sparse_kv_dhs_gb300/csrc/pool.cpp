@@ -788,8 +788,7 @@ int dhs_pool_create(const dhs_pool_config* cfg, dhs_pool** out) {
   }
   if (dhs::resolve_set_carveout() != cudaSuccess ||
       dhs::hostcopy_set_carveout(copy_hold_limit(optin)) != cudaSuccess ||
-      dhs::gather_set_carveout() != cudaSuccess || dhs::append_set_carveout() != cudaSuccess ||
-      dhs::attend_set_smem_limit() != cudaSuccess) {
+      dhs::gather_set_carveout() != cudaSuccess || dhs::append_set_carveout() != cudaSuccess) {
     delete p;
     return DHS_ECUDA;
   }

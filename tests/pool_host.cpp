@@ -87,7 +87,6 @@ cudaError_t resolve_set_carveout() { return cudaSuccess; }
 cudaError_t hostcopy_set_carveout(size_t) { return cudaSuccess; }
 cudaError_t gather_set_carveout() { return cudaSuccess; }
 cudaError_t append_set_carveout() { return cudaSuccess; }
-cudaError_t attend_set_smem_limit() { return cudaSuccess; }
 cudaError_t gather_set_smem_limit(int, int, bool* ok) { *ok = true; return cudaSuccess; }
 cudaError_t noalloc_scratch(NoallocScratch*) { return cudaErrorInvalidValue; }
 cudaError_t launch_resolve(const ResolveCommon&, const ResolveItem*, int, int, size_t, bool,
