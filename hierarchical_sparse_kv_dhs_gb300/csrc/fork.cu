@@ -202,7 +202,8 @@ cudaError_t launch_fork(const ForkCommon& c, const ForkSource* sources, int n_so
   if (!slots) return launch_fork_t<kForkSourcesMax, 1>(c, sources, n_sources, slots, 0, sms, stream);
   if (n_sources > kForkSourcesSome || n_slots > kForkSlotsMax) return cudaErrorInvalidValue;
   // the whole table travels with every launch: a small one for small requests
-  // (a fork of 4096 rows 20.4 us, with the large one 22.9)
+  // (a request of 4096 rows released and forked anew 21 us, with the large
+  // table 24)
   if (n_sources <= 8 && n_slots <= 512)
     return launch_fork_t<8, 512>(c, sources, n_sources, slots, n_slots, sms, stream);
   return launch_fork_t<kForkSourcesSome, kForkSlotsMax>(c, sources, n_sources, slots, n_slots, sms,
