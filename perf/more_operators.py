@@ -413,7 +413,7 @@ def _own_append(s):
     from hierarchical_sparse_kv_dhs_gb300 import dhs
     c, R, n = s["case"], s["case"]["requests"], s["case"]["tokens"]
     s["pool"] = _pool(c, max_requests=R, tail_rows=c["window"], page_rows=4096,
-                      max_rows_per_request=1 << 26)
+                      max_rows_per_request=1 << 19)
     _read_into(s, R, n)
     part = lambda x, r: None if x is None else x[r * n:(r + 1) * n]  # noqa: E731
     items = []
@@ -479,8 +479,13 @@ def _run_own(s):
     if c["op"] == "store":
         dhs.check(pool.pack(s["st"]), "dhs_pack")
     if c["op"] == "append":
-        dhs.check(pool.append_packed(s["st"]), "dhs_append_packed")
         n = c["tokens"]
+        if s["len"] + n > 1 << 19:  # as long as a request may get: the next one
+            for r in range(c["requests"]):
+                dhs.check(pool.release(r), "dhs_release")
+                dhs.check(pool.admit_window(r, 0, None, 0), "dhs_admit_window")
+            s["len"] = 0
+        dhs.check(pool.append_packed(s["st"]), "dhs_append_packed")
         _own_read(s, [dhs.unpack_item(n, s["k"][r], value=None if c["shared"] else s["v"][r], req=r,
                                       first=s["len"], flags=dhs.DHS_UNPACK_HISTORY)
                       for r in range(c["requests"])])
