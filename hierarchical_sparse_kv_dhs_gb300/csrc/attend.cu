@@ -61,20 +61,14 @@
 #include <algorithm>
 #include <atomic>
 
-#include "dhs_internal.h"
+#include "attend_core.cuh"
 
 namespace dhs {
 namespace {
 
-constexpr int kTile = 128;                 // rows per tile
-constexpr int kSoftThreads = 256, kLoadThreads = 128;
-constexpr int kIssueWarp = (kSoftThreads + kLoadThreads) / 32, kFindWarp = kIssueWarp + 1;
-constexpr int kRowWarp = kFindWarp + 1, kRowThreads = 64;
-constexpr int kThreads = 32 * kRowWarp + kRowThreads;
 constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk of a tile
 constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
-constexpr int kSegments = 4;               // segments found ahead
 constexpr int kRowSlots = 2;               // tiles whose row addresses are found ahead
 constexpr float kSlack = 8.f;              // log2 units
 
@@ -91,366 +85,14 @@ struct Plan {
 };
 
 template <int MAXI>
-struct AttendParams {
-  AttendCommon c;
-  Plan plan;
-  int32_t first[MAXI];   // first tile of each item, past the last one INT32_MAX
-  AttendItem items[MAXI];
-};
-static_assert(sizeof(AttendParams<kAttendItemsLarge>) <= 32764, "attend item table too large");
-
-// ------------------------------------------------------------------ PTX
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait (a poll that fails takes 4 us).  A wait that runs out raises
-// *gave_up; every later wait of the block then falls through, so that all its
-// warps still reach their end, on wrong data: the launch's status says so.
-// What lies behind a wait that fell through may not have been written, so no
-// address is taken from there: a segment is used only if gave_up is still
-// down after the wait for it, and not replaced after a wait that gave up; the
-// table of rows holds nothing but rows and nulls from the start.
-struct Patience {
-  volatile uint32_t* gave_up;
-  uint32_t polls;
-};
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, const Patience& until) {
-#pragma unroll 1
-  for (uint32_t n = 0; !bar_try(bar, parity); ++n) {
-    if (*until.gave_up) return;
-    if (n >= until.polls) *until.gave_up = 1;
-  }
-}
-
-// The same by whole warps, together again afterwards: what follows may be an
-// instruction that a warp executes as one (block barriers, tcgen05 loads).
-__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, const Patience& until) {
-  bar_wait(bar, parity, until);
-  __syncwarp();
-}
-
-__device__ __forceinline__ void fence_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ void tc_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// One of the warp's threads, the same one each time.
-__device__ __forceinline__ bool elected() {
-  uint32_t p;
-  asm volatile(
-      "{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(p)::"memory");
-  return p != 0;
-}
-
-// D += A B (D = A B unless add) with operand descriptors given as halves: the
-// high one is fixed for a kind of operand, the low one moves with the address.
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t ahi, uint32_t b, uint32_t bhi,
-                                    uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 x, y;\n"
-      "mov.b64 x, {%1, %2};\nmov.b64 y, {%3, %4};\nsetp.ne.b32 p, %6, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(ahi), "r"(b), "r"(bhi), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-
-// Arrives on `bar` once every product issued so far is done.
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-// Eight columns of the warp's 32 lanes.  The values may be used only behind
-// tm_wait, which every later use depends on.
-__device__ __forceinline__ void tm_load8(uint32_t addr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-        "=f"(v[7])
-      : "r"(addr)
-      : "memory");
-}
-
-template <int C>
-__device__ __forceinline__ void tm_wait(float (&v)[C]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int k = 0; k < C; ++k) asm volatile("" : "+f"(v[k]));
-}
-
-template <int C>
-__device__ __forceinline__ void tm_load(uint32_t addr, float (&v)[C]) {
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < C; k += 8) tm_load8(addr + k, v + k);
-  tm_wait(v);
-}
-
-template <int C>
-__device__ __forceinline__ void tm_store(uint32_t addr, const float (&v)[C]) {
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < C; k += 8)
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(v[k]),
-        "f"(v[k + 1]), "f"(v[k + 2]), "f"(v[k + 3]), "f"(v[k + 4]), "f"(v[k + 5]), "f"(v[k + 6]),
-        "f"(v[k + 7]), "r"(addr + k)
-        : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  __syncwarp();
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-__device__ __forceinline__ bool named_or(int id, int threads, bool v) {
-  uint32_t r;
-  __syncwarp();
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\n"
-      "bar.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Shared-memory operand descriptor.  Low half: start and leading stride
-// (bytes); high half: 8-row stride, format version, swizzle (2 = 128 B, 4 =
-// 64 B, 6 = 32 B rows).
-__device__ __forceinline__ uint32_t operand_lo(uint32_t addr, uint32_t lead) {
-  return (addr & 0x3FFFF) >> 4 | (lead >> 4) << 16;
-}
-__host__ __device__ constexpr uint32_t operand_hi(uint32_t eight, uint32_t swizzle) {
-  return eight >> 4 | 1u << 14 | swizzle << 29;
-}
-
-// Eight values of each lane reduced over the warp: lane i gets the result of
-// value i & 7.
-template <class F>
-__device__ __forceinline__ float fold8(const float* in, int lane, F f) {
-  float v[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = in[k];
-#pragma unroll
-  for (int w = 4; w; w >>= 1) {
-    const bool up = lane & w;
-#pragma unroll
-    for (int k = 0; k < w; ++k) {
-      const float send = up ? v[k] : v[k + w], keep = up ? v[k + w] : v[k];
-      v[k] = f(keep, __shfl_xor_sync(~0u, send, w));
-    }
-  }
-  v[0] = f(v[0], __shfl_xor_sync(~0u, v[0], 8));
-  return f(v[0], __shfl_xor_sync(~0u, v[0], 16));
-}
-
-// ------------------------------------------------------------------ jobs
-
-// A block's share of one job: tiles [t0, t1) of item `it`, columns [col0,
-// col0 + cols) of kv head g (column = query * group + head within the group
-// for a history; located items: query qbase, column = head).
-struct Segment {
-  AttendItem it;     // a copy: the table is indexed constant memory, slow to read
-  int32_t tiles;     // of the whole job
-  int32_t t0, t1;    // the segment's tiles before clipping to visible rows
-  int32_t g, qbase, col0, cols;
-  int64_t lo, hi;    // rows any of the columns may see, relative to it->first
-  int32_t v0, v1;    // tiles that hold some of them (v0 >= v1: none)
-  __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
-};
-
-// Rows [lo, hi) (relative to it.first) that query i of a history item sees.
-__device__ __forceinline__ void query_rows(const AttendItem& it, int i, int64_t& lo, int64_t& hi) {
-  const int64_t L = it.first + it.len;
-  lo = it.range ? max((int64_t)it.range[2 * i] - it.first, (int64_t)0) : 0;
-  hi = (it.range ? min((int64_t)it.range[2 * i + 1], L) : L - it.Q + 1 + i) - it.first;
-}
-
-// The last item whose first tile is <= t (an item without jobs has none).
-template <int MAXI>
-__device__ __forceinline__ int item_at(const AttendParams<MAXI>& P, int32_t t) {
-  const int32_t* first = P.first + (threadIdx.x & 31);
-  int32_t x[(MAXI + 31) / 32];
-#pragma unroll
-  for (int k = 0; k < (MAXI + 31) / 32; ++k)
-    x[k] = 32 * k + (threadIdx.x & 31) < MAXI ? first[32 * k] : INT32_MAX;
-  int n = 0;
-#pragma unroll
-  for (int k = 0; k < (MAXI + 31) / 32; ++k) n += __popc(__ballot_sync(~0u, x[k] <= t));
-  return n - 1;
-}
-
-// The segment that begins at tile `t` of the launch and ends before `te`.
-// Called by whole warps.
-template <int MAXI>
-__device__ Segment segment_at(const AttendParams<MAXI>& P, int32_t t, int32_t te) {
-  const AttendCommon& c = P.c;
-  __syncwarp();
-  Segment s;
-  s.it = P.items[item_at(P, t)];
-  const AttendItem& it = s.it;
-  const bool located = it.loc != nullptr;
-  s.tiles = it.tiles;
-  const int32_t job = (t - it.tile0) / it.tiles;
-  s.t0 = (t - it.tile0) - job * it.tiles;
-  s.t1 = min(it.tiles, s.t0 + (te - t));
-  const int32_t columns = located ? c.group : it.Q * c.group;
-  const int32_t query = job / it.blocks;
-  s.col0 = (job - query * it.blocks) * it.width;
-  s.cols = min(it.width, columns - s.col0);
-  s.qbase = query / c.kv;
-  s.g = query - s.qbase * c.kv;
-  s.lo = 0;
-  s.hi = it.len;
-  if (!located) {
-    const int q0 = s.col0 / c.group, q1 = (s.col0 + s.cols - 1) / c.group;
-    int64_t lo = it.len, hi = 0;
-#pragma unroll 1
-    for (int i = q0 + (threadIdx.x & 31); i <= q1; i += 32) {
-      int64_t x, y;
-      query_rows(it, i, x, y);
-      if (x < y) {
-        lo = min(lo, x);
-        hi = max(hi, y);
-      }
-    }
-#pragma unroll 1
-    for (int w = 16; w; w >>= 1) {
-      lo = min(lo, (int64_t)__shfl_xor_sync(~0u, (long long)lo, w));
-      hi = max(hi, (int64_t)__shfl_xor_sync(~0u, (long long)hi, w));
-    }
-    s.lo = lo;
-    s.hi = hi;
-  }
-  s.v0 = max(s.t0, (int32_t)(s.lo / kTile));
-  s.v1 = min(s.t1, (int32_t)((s.hi + kTile - 1) / kTile));
-  return s;
-}
-
-// First tile of block b's share of what the waves leave.
-__host__ __device__ __forceinline__ int32_t first_tile(const AttendCommon& c, int32_t b) {
-  return c.waved + b * c.share + min(b, c.extra);
-}
-
-// A block's segments: first a whole job of each wave (jobs of equal length go
-// to the blocks in order, so that blocks running side by side work on
-// neighbouring jobs, which read the same rows), then its even share of the
-// tiles that are left.
-struct Walk {
-  int32_t wave, t, te;
-};
-template <int MAXI>
-__device__ __forceinline__ Walk first_of(const AttendParams<MAXI>& P) {
-  const AttendCommon& c = P.c;
-  return {0, first_tile(c, blockIdx.x), first_tile(c, blockIdx.x + 1)};
-}
-template <int MAXI>
-__device__ bool next_segment(const AttendParams<MAXI>& P, Walk& w, Segment& s) {
-  const AttendCommon& c = P.c;
-  int32_t t = w.t, te = w.te;
-  const bool wave = w.wave < c.waves;
-  if (wave) {
-    t = (int32_t)((w.wave * gridDim.x + blockIdx.x) * c.job_tiles);
-    te = t + c.job_tiles;
-    ++w.wave;
-  } else if (t >= te) {
-    return false;
-  }
-  s = segment_at(P, t, te);
-  if (!wave) w.t += s.t1 - s.t0;
-  return true;
-}
-
-// Finding row j of a job takes up to two dependent loads: a list position
-// (union items), then the location or (histories) the page's slot.  They are
-// split so that a row thread can keep them in flight: `row_index` two
-// tiles ahead, `row_word` one tile ahead, `row_of` when the tile is loaded.
-__device__ __forceinline__ int32_t row_index(const Segment& s, int64_t j) {
-  const AttendItem& it = s.it;
-  if (!it.index || j < s.lo || j >= s.hi) return -1;
-  return __ldg(it.index + (int64_t)s.qbase * it.len + j);
-}
-
-__device__ __forceinline__ uint32_t row_word(const AttendCommon& c, const Segment& s, int64_t j,
-                                             int32_t index) {
-  const AttendItem& it = s.it;
-  if (j < s.lo || j >= s.hi) return kNoLoc;
-  if (it.loc) {
-    if (!it.index) return __ldg(it.loc + (int64_t)s.qbase * it.len + j);
-    if (index < 0) return kNoLoc;
-    // a position past the list: a location of no tier
-    return index < (int64_t)it.Q * it.len ? __ldg(it.loc + index) : 3u << 30;
-  }
-  const int64_t page = (it.first + j) >> c.page_shift;
-  return page < it.complete ? (uint32_t)__ldg(c.map + (size_t)it.pair * c.Pmax + page) : kNoLoc;
-}
-
-// Address of row j of the job, or null when there is none.
-__device__ __forceinline__ const uint8_t* row_of(const AttendCommon& c, const Segment& s, int64_t j,
-                                                 uint32_t word) {
-  const AttendItem& it = s.it;
-  if (j < s.lo || j >= s.hi) return nullptr;
-  if (it.loc) {
-    if (word >= kEndLoc) return nullptr;
-    const uint32_t tier = word >> 30, x = word & 0x3FFFFFFFu;
-    const uint32_t rows = tier == kTierTail ? c.tail_rows : tier == kTierOpt ? c.opt_rows
-                          : tier == kTierHot ? c.hot_rows : 0;
-    if (x >= rows) {
-      atomicOr(c.status, kStatusEloc);
-      return nullptr;
-    }
-    const uint8_t* base = tier == kTierTail ? c.tail : tier == kTierOpt ? c.opt : c.hot;
-    return base + (size_t)x * c.row_bytes;
-  }
-  const int64_t r = it.first + j;
-  if (r >= it.first + it.len - c.T)
-    return c.tail + ((size_t)it.pair * c.T + (uint32_t)r % (uint32_t)c.T) * c.row_bytes;
-  if ((int32_t)word >= 0)
-    return c.opt + (((size_t)word << c.page_shift) + (r & ((1 << c.page_shift) - 1))) * c.row_bytes;
-  return it.host + (size_t)r * c.row_bytes;
-}
+using Params = AttendParams<MAXI, Plan>;
+static_assert(sizeof(Params<kAttendItemsLarge>) <= 32764, "attend item table too large");
 
 // ------------------------------------------------------------------ kernel
 
 constexpr int kUnusedBars = 8 - 2 * kRowSlots;
 struct Control {
+  static constexpr int kRowSlots = dhs::kRowSlots;
   uint64_t kfull[kMaxK], kempty[kMaxK], vfull[kMaxV], vempty[kMaxV];
   uint64_t qfull, qempty, sfull[2], pfull, odone, oempty, rfull[kRowSlots], rempty[kRowSlots], drain;
   uint64_t segfull[kSegments], segempty[kSegments];
@@ -476,18 +118,6 @@ constexpr int kBarQfull = 2 * kMaxK + 2 * kMaxV, kBarPfull = kBarQfull + 4,
 static_assert(kBarSegempty + kSegments + kUnusedBars == kBarriers, "barrier table");
 constexpr uint32_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
 
-// Parity bookkeeping of a ring of slots.
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ void next(int n) {
-    if (++slot == n) {
-      slot = 0;
-      phase ^= 1;
-    }
-  }
-};
-
 // Two buffers of scores, then up to four units of sums.
 __host__ __device__ constexpr uint32_t tmem_columns(int n) {
   return 6 * n <= 128 ? 128 : 6 * n <= 256 ? 256 : 512;
@@ -498,7 +128,7 @@ __host__ __device__ constexpr uint32_t weight_swizzle(int n) { return n <= 16 ? 
 
 // Loading warps: queries once per segment, rows tile by tile.
 template <int N, bool SHARED, int MAXI>
-__device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid) {
+__device__ void load_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, int tid) {
   const AttendCommon& c = P.c;
   const Patience until{&ctl.gave_up, c.polls};
   const Plan& pl = P.plan;
@@ -622,80 +252,9 @@ __device__ void load_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Finding warp: the block's segments, ahead of the others, who read them from
-// shared memory.  One without columns ends the walk.  The first one is found
-// while the block sets up.
-template <int MAXI>
-__device__ void find_segments(const AttendParams<MAXI>& P, Control& ctl) {
-  const Patience until{&ctl.gave_up, P.c.polls};
-  Ring seg;
-  Walk w = first_of(P);
-  bool more = true;
-#pragma unroll 1
-  for (bool begin = true; more; begin = false) {
-    Segment s;
-    more = next_segment(P, w, s);
-    if (begin) __syncthreads();
-    if (!more) s.cols = 0;
-    warp_wait(smem_u32(&ctl.segempty[seg.slot]), seg.phase ^ 1, until);
-    if (__any_sync(~0u, ctl.gave_up)) break;  // the slot may still be in use
-    if (elected()) {
-      ctl.seg[seg.slot] = s;
-      bar_arrive(smem_u32(&ctl.segfull[seg.slot]));
-    }
-    seg.next(kSegments);
-  }
-}
-
-// Row warps: the addresses of every tile's rows, ahead of the loading warps.
-template <int MAXI>
-__device__ void find_rows(const AttendParams<MAXI>& P, Control& ctl, int tid) {
-  constexpr int R = kTile / kRowThreads;
-  const AttendCommon& c = P.c;
-  const Patience until{&ctl.gave_up, c.polls};
-  Ring seg, rr;
-#pragma unroll 1
-  for (;;) {
-    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
-    const Segment s = ctl.seg[seg.slot];
-    if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
-    int64_t j = (int64_t)s.v0 * kTile + tid;
-    uint32_t word[R];
-    int32_t index[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int64_t i = j + k * kRowThreads;
-      index[k] = row_index(s, i);
-    }
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int64_t i = j + k * kRowThreads;
-      word[k] = row_word(c, s, i, index[k]);
-      index[k] = row_index(s, i + kTile);
-    }
-#pragma unroll 1
-    for (int tile = s.v0; tile < s.v1; ++tile, j += kTile) {
-      warp_wait(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1, until);
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const int64_t i = j + k * kRowThreads;
-        ctl.row[rr.slot][tid + k * kRowThreads] = row_of(c, s, i, word[k]);
-        word[k] = row_word(c, s, i + kTile, index[k]);
-        index[k] = row_index(s, i + 2 * kTile);
-      }
-      __syncwarp();
-      if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
-      rr.next(kRowSlots);
-    }
-    __syncwarp();
-    if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
-    seg.next(kSegments);
-  }
-}
-
 // Issuing warp: all its lanes walk the same path, one of them issues.
 template <int N, bool SHARED, int MAXI>
-__device__ void issue_products(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl) {
+__device__ void issue_products(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
   const AttendCommon& c = P.c;
   const Patience until{&ctl.gave_up, c.polls};
   const Plan& pl = P.plan;
@@ -841,7 +400,7 @@ __device__ bool finite_row(const uint8_t* p, int n, int f16) {
 // values become zeros.  Runs while no product is in flight: those of the
 // tiles before are complete.
 template <int N, int MAXI>
-__device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl,
+__device__ __noinline__ void odd_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl,
                                       int tid, bool odd, const uint8_t* value, Ring vr,
                                       int32_t tile0, bool first, uint32_t tm_scores) {
   constexpr int C = N / 2;
@@ -916,37 +475,10 @@ __device__ __noinline__ void odd_rows(const AttendParams<MAXI>& P, uint8_t* sm, 
   }
 }
 
-// 4 x 4 values of four neighbouring lanes transposed: lane i (mod 4) gets
-// value i of lanes 0..3.
-__device__ __forceinline__ void transpose4(float* v, int lane) {
-  const bool a = lane & 1, b = lane & 2;
-  float s0 = a ? v[0] : v[1], s1 = a ? v[2] : v[3];
-  s0 = __shfl_xor_sync(~0u, s0, 1);
-  s1 = __shfl_xor_sync(~0u, s1, 1);
-  if (a) {
-    v[0] = s0;
-    v[2] = s1;
-  } else {
-    v[1] = s0;
-    v[3] = s1;
-  }
-  s0 = b ? v[0] : v[2];
-  s1 = b ? v[1] : v[3];
-  s0 = __shfl_xor_sync(~0u, s0, 2);
-  s1 = __shfl_xor_sync(~0u, s1, 2);
-  if (b) {
-    v[0] = s0;
-    v[1] = s1;
-  } else {
-    v[2] = s0;
-    v[3] = s1;
-  }
-}
-
 // Softmax warps: a thread has one row of the tile and half of the columns;
 // then the segment's output.
 template <int N, bool SHARED, int MAXI>
-__device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& ctl, int tid,
+__device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, int tid,
                              float* parts) {
   constexpr int C = N / 2;
   const AttendCommon& c = P.c;
@@ -1225,7 +757,7 @@ __device__ void softmax_rows(const AttendParams<MAXI>& P, uint8_t* sm, Control& 
 
 template <int N, bool SHARED, int MAXI>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_kernel(const __grid_constant__ AttendParams<MAXI> P, float* parts) {
+    attend_kernel(const __grid_constant__ Params<MAXI> P, float* parts) {
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   Control& ctl = *reinterpret_cast<Control*>(sm);
@@ -1277,133 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && ctl.gave_up) atomicOr(P.c.status, kStatusEtimeout);
 }
 
-// ------------------------------------------------------------------ merge
-
-constexpr int kMergeWarps = 16;
-constexpr int kMergeElems = 128;  // value elements of a warp: a float4 a lane
-
-// A split job: parts of the blocks [b0, b0 + n).
-struct Cut {
-  uint8_t* out;       // of the job's kv head and, if located, query
-  float* lse;         // or null
-  int32_t b0, n;
-  int32_t col0, cols;
-};
-
-struct MergeParams {
-  int32_t groups;     // warps that share one column's parts: 1, 4 or 16
-  int32_t columns;    // of a part
-  int32_t dv, f16, heads, group;
-  int64_t o_qs, o_hs;
-  Cut cut[kAttendMaxBlocks];
-};
-
-// Joins the parts of the split jobs in block order.  A warp has 128 value
-// elements of one column and every `groups`-th part; the groups' sums meet in
-// shared memory.  Bound by latency: statistics, then weights, then parts, each
-// a trip to L2; 104 jobs of 64 columns in 2 to 3 parts, 34 MB, take 23 us, one
-// job of 16 columns in 152 parts 13 (each on cold caches).
-__global__ void __launch_bounds__(kMergeWarps * 32, 2)
-    merge_kernel(const __grid_constant__ MergeParams M, const float* parts) {
-  __shared__ float4 sums[kMergeWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Cut& cut = M.cut[blockIdx.x];
-  const int n = cut.n, b0 = cut.b0;
-  const int spans = (M.dv + kMergeElems - 1) / kMergeElems;
-  const int pair = blockIdx.y * (kMergeWarps / M.groups) + warp / M.groups;
-  const int col = pair / spans, d = pair % spans * kMergeElems + lane * 4;
-  const int group = warp % M.groups;
-  const bool on = col < cut.cols;
-  const size_t stride = (size_t)M.columns * (M.dv + 2);
-  auto part = [&](int i) { return parts + (size_t)(2 * (b0 + i) + (i == 0)) * stride; };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  float base = 0.f, z = 0.f;
-  if (on) {
-    const size_t ml = (size_t)M.columns * M.dv + col;
-    float m = -INFINITY;
-#pragma unroll 1
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[ml]);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
-    base = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-    for (int i = lane; i < n; i += 32)
-      z += exp2_fast(part(i)[ml] - base) * part(i)[ml + M.columns];
-#pragma unroll
-    for (int w = 16; w; w >>= 1) z += __shfl_xor_sync(~0u, z, w);
-    // lane k's weight is that of the group's k-th part, of 32 at a time
-#pragma unroll 1
-    for (int i0 = group; i0 < n; i0 += 32 * M.groups) {
-      const int mine = i0 + lane * M.groups;
-      const float weight = mine < n ? exp2_fast(part(mine)[ml] - base) : 0.f;
-      const int count = min(32, (n - i0 + M.groups - 1) / M.groups);
-#pragma unroll 1
-      for (int k = 0; k < count; k += 4) {
-        float4 y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (k + u < count && d < M.dv)
-            y[u] = *reinterpret_cast<const float4*>(part(i0 + (k + u) * M.groups) +
-                                                    (size_t)col * M.dv + d);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float w = __shfl_sync(~0u, weight, (k + u) & 31);
-          // a part without weight may hold sums that are not finite
-          if (k + u < count && w != 0.f && d < M.dv) {
-            x.x += w * y[u].x;
-            x.y += w * y[u].y;
-            x.z += w * y[u].z;
-            x.w += w * y[u].w;
-          }
-        }
-      }
-    }
-  }
-  if (M.groups > 1) {
-    sums[warp][lane] = x;
-    __syncthreads();
-    if (group) return;
-#pragma unroll 1
-    for (int k = 1; k < M.groups; ++k) {
-      const float4 y = sums[warp + k][lane];
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
-    }
-  }
-  if (!on) return;
-  const int qc = cut.col0 + col, qi = qc / M.group, h = qc - qi * M.group;
-  if (cut.lse && lane == 0 && d == 0)
-    cut.lse[(size_t)qi * M.heads + h] =
-        z == 0.f ? -INFINITY : (base + log2f(z)) * 0.693147180559945309f;
-  if (d >= M.dv) return;
-  uint8_t* out = cut.out + qi * M.o_qs + h * M.o_hs + 2 * d;
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-  float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
-  uint16_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (inv == 0.f) y[k] = 0.f;
-    const __half a = __float2half_rn(y[k]);
-    const __nv_bfloat16 b = __float2bfloat16_rn(y[k]);
-    w[k] = M.f16 ? __half_as_ushort(a) : __bfloat16_as_ushort(b);
-  }
-  if ((uintptr_t)out & 7) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) reinterpret_cast<uint16_t*>(out)[k] = w[k];
-  } else {
-    *reinterpret_cast<uint2*>(out) =
-        make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
-  }
-}
-
 // ------------------------------------------------------------------ host
-
-constexpr uint32_t kSmemLimit = 232448;  // opt-in shared memory of a block
-
-uint32_t round_up(uint32_t x, uint32_t to) { return (x + to - 1) / to * to; }
 
 // Ring sizes that fit shared memory: what a tile needs at once, then one
 // value unit and one key chunk more in turn while there is room.
@@ -1451,125 +857,6 @@ int widest_block(const AttendCommon& c) {
   return n;
 }
 
-struct Shape {
-  int n = 0;          // columns of a block
-  int64_t tiles = 0;
-  int blocks = 0;
-  int n_cut = 0;      // jobs cut by a block's boundary
-  int groups = 1;     // of the merge
-  Cut cut[kAttendMaxBlocks];
-};
-
-int columns_of(const AttendCommon& c, const AttendItem& it, int most) {
-  const int all = it.loc ? c.group : it.Q * c.group;
-  const int blk = (all + most - 1) / most;
-  return (all + blk - 1) / blk;
-}
-
-// Fills in every item's tiles, and how the blocks share them.
-Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms) {
-  Shape s;
-  const int most = widest_block(c);
-  int widest = 1;
-  int64_t n_jobs = 0, longest = 0, shortest = INT64_MAX;
-  for (int i = 0; i < n_items; ++i) widest = std::max(widest, columns_of(c, items[i], most));
-  s.n = (widest + 15) / 16 * 16;
-  c.kv = c.heads / c.group;
-  for (int i = 0; i < n_items; ++i) {
-    AttendItem& it = items[i];
-    it.tile0 = (int32_t)std::min<int64_t>(s.tiles, INT32_MAX);
-    // an item without rows still has one tile, that writes its empty outputs
-    it.tiles = (int32_t)std::max<int64_t>(1, (it.len + kTile - 1) / kTile);
-    const int64_t all = it.loc ? c.group : (int64_t)it.Q * c.group;
-    it.blocks = (int32_t)((all + s.n - 1) / s.n);
-    it.width = it.blocks ? (int32_t)((all + it.blocks - 1) / it.blocks) : 0;
-    const int64_t jobs = (it.loc ? it.Q : 1) * (int64_t)c.kv * it.blocks;
-    s.tiles += jobs * it.tiles;
-    n_jobs += jobs;
-    longest = std::max<int64_t>(longest, it.tiles);
-    shortest = std::min<int64_t>(shortest, it.tiles);
-  }
-  sms = std::min(sms, kAttendMaxBlocks);
-  s.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(sms, s.tiles));
-  c.waves = c.waved = c.job_tiles = c.share = c.extra = 0;
-  if (s.tiles > INT32_MAX) return s;  // refused
-  // Jobs of equal length: whole ones in waves over the blocks, as neighbours
-  // often read the same rows (64 verify blocks of 8 queries with 80 % of their
-  // rows in common 267 -> 250 us, 128 heads 191 -> 185; grouped heads on
-  // unrelated rows lose, 76 -> 82).  Fewer blocks if that leaves nothing to
-  // split and no block with more to do, or with two tiles instead of one,
-  // which take no longer than a merge (40 x 256 rows 14.4 us instead of 16.7,
-  // 16 x 256 grouped 10.3 instead of 12.4; three tiles: 17.4 instead of 14.4).
-  if (longest == shortest) {
-    const int64_t each = (n_jobs + sms - 1) / sms;
-    const int64_t even = (s.tiles + s.blocks - 1) / s.blocks;
-    if (n_jobs % each == 0 && each * longest <= std::max<int64_t>(2, even))
-      s.blocks = (int)(n_jobs / each);
-    c.waves = (int)(n_jobs / s.blocks);
-    c.job_tiles = (int32_t)longest;
-    c.waved = (int32_t)(c.waves * s.blocks * longest);
-  }
-  const int64_t rest = s.tiles - c.waved;  // dealt out evenly, cut where it falls
-  c.share = (int32_t)(rest / s.blocks);
-  c.extra = (int32_t)(rest % s.blocks);
-  const int parts = rest ? (int)std::min<int64_t>(s.blocks, longest * s.blocks / rest + 2) : 0;
-  // Warps that share a column: few parts leave too little to each, many wait
-  // in line.  8 x 2048 rows in 20 parts: 4 groups 16.4 us, 1 18.5, 16 20.5;
-  // 512 K rows in 152 parts: 16 groups 116.5 us, 4 122.3.
-  s.groups = parts > 24 ? 16 : parts > 4 ? 4 : 1;
-  if (rest) {
-    int k = 0;
-    int64_t cut_job = -1;  // first tile of the job cut last
-    for (int b = 1; b < s.blocks; ++b) {
-      const int32_t t = first_tile(c, b);
-      if (t >= s.tiles) break;
-      while (k + 1 < n_items && items[k + 1].tile0 <= t) ++k;
-      const AttendItem& it = items[k];
-      const int32_t job = (t - it.tile0) / it.tiles, in = (t - it.tile0) - job * it.tiles;
-      if (in == 0 || t - in == cut_job) continue;
-      cut_job = t - in;
-      Cut& cut = s.cut[s.n_cut++];
-      const int32_t query = job / it.blocks, q = query / c.kv, head = (query - q * c.kv) * c.group;
-      const int32_t columns = it.loc ? c.group : it.Q * c.group;
-      cut.out = it.out + q * c.o_qs + head * c.o_hs;
-      cut.lse = it.lse ? it.lse + (size_t)q * c.heads + head : nullptr;
-      cut.col0 = (job - query * it.blocks) * it.width;
-      cut.cols = std::min(it.width, columns - cut.col0);
-      // up to the block that holds the job's last tile
-      const int32_t last = (int32_t)cut_job + it.tiles - 1 - c.waved, more = c.extra * (c.share + 1);
-      cut.b0 = b - 1;
-      cut.n = (last < more ? last / (c.share + 1) : c.extra + (last - more) / c.share) - b + 2;
-    }
-  }
-  return s;
-}
-
-cudaError_t launch_merge(const AttendCommon& c, const Shape& s, const float* parts,
-                         cudaStream_t stream) {
-  MergeParams M;
-  M.groups = s.groups;
-  M.columns = s.n;
-  M.dv = c.dv;
-  M.f16 = c.f16;
-  M.heads = c.heads;
-  M.group = c.group;
-  M.o_qs = c.o_qs;
-  M.o_hs = c.o_hs;
-  std::copy(s.cut, s.cut + s.n_cut, M.cut);
-  cudaLaunchConfig_t cfg{};
-  const int per = kMergeWarps / s.groups;
-  const int pairs = s.n * ((c.dv + kMergeElems - 1) / kMergeElems);
-  cfg.gridDim = dim3(s.n_cut, (pairs + per - 1) / per);
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel, M, parts);
-}
-
 // Lets a kernel's blocks use all of an SM's shared memory: once on each device,
 // with its first launch there.  (The driver loads a kernel when it is first
 // named.  Pools that named all 16 of these when they were made took 1 ms more
@@ -1591,7 +878,7 @@ cudaError_t use_all_smem() {
 }
 
 template <int N, bool SHARED, int MAXI>
-cudaError_t launch_kernel(const AttendParams<MAXI>& P, const Shape& s, float* parts,
+cudaError_t launch_kernel(const Params<MAXI>& P, const Shape& s, float* parts,
                           cudaStream_t stream) {
   cudaError_t e = use_all_smem<N, SHARED, MAXI>();
   if (e != cudaSuccess) return e;
@@ -1604,7 +891,7 @@ cudaError_t launch_kernel(const AttendParams<MAXI>& P, const Shape& s, float* pa
 // A kernel for each kind of layout: with one that asked at run time, both were
 // slower (128 heads 172 us instead of 166, grouped heads 55.7 instead of 54.4).
 template <int N, int MAXI>
-cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
+cudaError_t launch_n(const Params<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
   return P.plan.shared ? launch_kernel<N, true, MAXI>(P, s, parts, stream)
                        : launch_kernel<N, false, MAXI>(P, s, parts, stream);
 }
@@ -1612,7 +899,7 @@ cudaError_t launch_n(const AttendParams<MAXI>& P, const Shape& s, float* parts, 
 template <int MAXI>
 cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items, const Shape& s,
                      float* parts, cudaStream_t stream) {
-  AttendParams<MAXI> P;
+  Params<MAXI> P;
   P.c = c;
   P.plan = make_plan(c, s.n);
   for (int i = 0; i < MAXI; ++i) P.first[i] = i < n_items ? items[i].tile0 : INT32_MAX;
@@ -1628,8 +915,8 @@ cudaError_t launch_t(const AttendCommon& c, const AttendItem* items, int n_items
 }  // namespace
 
 bool attend_shape(AttendCommon c, AttendItem* items, int n_items, int sms, size_t* bytes) {
-  const Shape s = shape_of(c, items, n_items, sms);
-  *bytes = s.n_cut ? (size_t)2 * s.blocks * s.n * (c.dv + 2) * sizeof(float) : 0;
+  const Shape s = shape_of(c, items, n_items, sms, widest_block(c));
+  *bytes = parts_bytes(c, s);
   return s.tiles <= INT32_MAX;
 }
 
@@ -1637,7 +924,7 @@ cudaError_t launch_attend(AttendCommon c, AttendItem* items, int n_items, int sm
                           void* work, cudaStream_t stream) {
   if (n_items <= 0) return cudaSuccess;
   if (n_items > kAttendItemsLarge) return cudaErrorInvalidValue;
-  const Shape s = shape_of(c, items, n_items, sms);
+  const Shape s = shape_of(c, items, n_items, sms, widest_block(c));
   if (s.tiles > INT32_MAX) return cudaErrorInvalidValue;
   float* parts = static_cast<float*>(work);
   // The whole table travels with a launch: a small one for few items (12

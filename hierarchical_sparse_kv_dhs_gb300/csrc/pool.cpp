@@ -27,19 +27,19 @@
 #include <new>
 #include <vector>
 
-#include "dhs.h"
-#include "dhs_internal.h"
+#include "pool_state.h"
+
+using dhs::BackupRun;
+using dhs::cuda_rc;
+using dhs::kAlign;
+using dhs::MetaLayout;
+using dhs::on_stream;
+using dhs::PairState;
+using dhs::room;
 
 namespace {
 
-constexpr size_t kAlign = 256;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
-
-struct MetaLayout {
-  size_t tags, stamps, map, miss_rows, miss_slots, miss_count, copy_cursor, pair_status;
-  size_t loc_ready, copy_ready, fill, later_count, status, later, miss_off, miss_ent;
-  size_t total;
-};
 
 inline int64_t pages_max_of(const dhs_pool_config& c) {
   return (c.max_rows_per_request + c.page_rows - 1) / c.page_rows;
@@ -128,143 +128,6 @@ int validate_geometry(const dhs_pool_config* c) {
     return DHS_EINVAL;
   return DHS_OK;
 }
-
-struct PairState {
-  bool admitted = false;
-  bool window = false;          // window source: the tail ring is its only storage
-  int64_t N = 0, L = 0;
-  uint8_t* host = nullptr;      // caller's pinned host rows
-  uint8_t* host_dev = nullptr;  // device-visible address of the same rows
-  std::vector<int32_t> pending;  // resident pages whose bytes are not yet copied
-  std::vector<uint64_t> backup;  // per page: backup order while the host copy is
-                                 // deferred, 0 = backed (empty: all backed)
-};
-
-struct BackupRun {
-  uint64_t order;  // of the first page
-  int32_t pair, page, pages;
-};
-
-}  // namespace
-
-struct dhs_pool {
-  dhs_pool_config cfg{};
-  cudaStream_t stream = nullptr;
-  int device = 0;
-  int64_t pairs = 0, pmax = 0, mcap = 0;
-  int page_shift = 0;
-  MetaLayout layout{};
-  int32_t* tags = nullptr;
-  uint32_t* stamps = nullptr;
-  int32_t* map = nullptr;
-  int32_t* miss_rows = nullptr;
-  int32_t* miss_slots = nullptr;
-  uint32_t* miss_count = nullptr;
-  uint32_t* copy_cursor = nullptr;
-  int32_t* pair_status = nullptr;
-  uint32_t* status = nullptr;
-  std::vector<PairState> ps;
-  std::vector<int32_t> map_host;  // [pairs][pmax] mirror of the device map
-  std::vector<int32_t> slot_pair, slot_page;
-  int64_t first_free = 0, used = 0;
-  int64_t capacity = 0;  // optional page slots in use or free (dhs_compact lowers it)
-  int64_t dirty_lo = INT64_MAX, dirty_hi = -1;  // pairs whose map changed
-  bool any_pending = false;
-  int copy_ctas = 0;
-  bool union_ok = false;  // the union staging plan fits in shared memory
-  int gather_impl = dhs::kGatherTma;
-  bool tma_ok = true;  // the TMA gather's tile fits the row size
-  int gather_tpc = 1;   // DHS_OPT_GATHER_TPC
-  int early = 1;        // fused gathers copy step-1 rows before the resolve ends
-  uint32_t seq = 0;             // resolve launches so far
-  uint32_t* loc_ready = nullptr;  // [pairs] per-item "locations written" marks
-  uint32_t* copy_ready = nullptr; // [pairs] per-item "miss lists written" marks
-  uint32_t* fill = nullptr;       // [pairs][fill_words] slots the step's copy fills
-  uint32_t* later_count = nullptr;
-  dhs::LaterEntry* later = nullptr;
-  int64_t later_cap = 0;
-  int fill_words = 0;
-  uint32_t gen = 0;             // fused steps that launched a resolve
-  bool fused_resolved = false;  // the current fused step launched one
-  int fresh_list = -1;          // DHS_OPT_FRESH_LIST: -1 auto, 0 off, 1 on
-  int64_t complete_pages = 0;   // complete imported pages of admitted pairs
-  uint64_t bseq = 0;            // pages put in backup order so far
-  // Pages whose host backup is deferred, in order, as runs of consecutive
-  // pages and orders (a fork or an admission queues thousands at a time).  A
-  // page of a run counts while its PairState::backup holds its order; the
-  // others are skipped, and runs without any swept out now and then.
-  std::vector<BackupRun> backup_queue;
-  size_t backup_head = 0;       // runs before it are done with
-  int64_t backup_live = 0;
-  int32_t rr = 0;               // refill cursor: the next request visited
-  int sm_count = 0;
-  int smem_optin = 0;           // opt-in shared memory per block
-  int32_t* miss_off = nullptr;  // [pairs][Mcap + 1] staging entries of each miss
-  int32_t* miss_ent = nullptr;  // [pairs][ent_cap]
-  int64_t ent_cap = 0;
-  int stage_misses = 1;         // DHS_OPT_STAGE_MISSES
-  uint32_t mark_polls = dhs::kMarkPolls;  // DHS_OPT_MARK_POLLS
-  uint32_t attend_polls = dhs::kAttendPolls;  // DHS_OPT_ATTEND_POLLS
-  int copy_pdl = -1;            // DHS_OPT_COPY_PDL: -1 auto, 0 off, 1 on
-  int resolve_paired = -1;      // DHS_OPT_RESOLVE_PAIRED: -1 auto, 0 off, 1 whenever it fits
-  int copy_steal = -1;          // DHS_OPT_COPY_STEAL: -1 auto, 0 off, 1 on
-  int resolve_ctas = 0;         // DHS_OPT_RESOLVE_CTAS: 0 auto, > 0 at most that many
-  int smem_per_sm = 0;          // shared memory per SM
-  std::vector<uint8_t> staged_pair;  // the host copy stages this pair's misses this step
-  std::vector<uint8_t> staged_item;  // per item of the step: a gather-only item whose
-                                     // staging the host copy writes too
-  unsigned long long* trace = nullptr;  // DHS_OPT_TRACE buffer, null = off
-  // reusable launch tables
-  std::vector<dhs::ResolveItem> ritems;
-  std::vector<dhs::CopyItem> citems;
-  std::vector<dhs::GatherItem> gitems;
-  // gathers of a fused step: the resolved items' location vectors, sorted,
-  // to find which pair (if any) published a gather item's locations
-  struct LocKey {
-    const void* loc;
-    int32_t order;  // item index: of equal vectors the last one counts
-    int64_t pair;
-    bool operator<(const LocKey& o) const {
-      return loc != o.loc ? std::less<const void*>()(loc, o.loc) : order < o.order;
-    }
-  };
-  std::vector<LocKey> loc_keys;
-  std::vector<dhs::AppendItem> aitems;
-  std::vector<dhs::AttendItem> titems;
-  std::vector<dhs::PageRun> runs;      // page runs of a compaction
-  std::vector<uint8_t> seen;
-  std::vector<int32_t> app_of_pair;  // decode step: append item of each pair, -1 = none
-  std::vector<int64_t> l0_of_pair;   // length of each resolved pair before this step's append
-  std::vector<const uint8_t*> app_of_pair_rows;  // its appended rows' source, or null
-  std::vector<uint32_t> seq_of_pair; // resolve launch that last resolved each pair
-  std::vector<dhs::PageMove> moves;  // page list of the next page-move launch
-  // dhs_prefetch: resolves enqueued on a caller's side stream; the pool's
-  // stream waits for them before its next device work
-  cudaEvent_t ev_main = nullptr, ev_prefetch = nullptr;
-  // dhs_decode_step_host_async on callers' copy streams: the step waits for
-  // the inputs (ev_in), the outputs' copies wait for the step (ev_step)
-  cudaEvent_t ev_in = nullptr, ev_step = nullptr;
-  bool prefetch_pending = false;
-  bool join_gathers = true;  // enter(): also join gathers on other streams
-  std::vector<uint8_t> pf_pair;  // pairs resolved by the outstanding prefetch
-  // dhs_gather_on: gathers on callers' streams read rows the pool's next
-  // resolve / append / admission may change; one event per such call,
-  // joined (and recycled) by the pool's next call that can change rows
-  std::vector<cudaEvent_t> ev_free, ev_gathers;
-  bool map_readers = false;  // some of them read the page maps (histories)
-  ~dhs_pool() {
-    if (ev_main) cudaEventDestroy(ev_main);
-    if (ev_prefetch) cudaEventDestroy(ev_prefetch);
-    if (ev_in) cudaEventDestroy(ev_in);
-    if (ev_step) cudaEventDestroy(ev_step);
-    for (cudaEvent_t e : ev_free) cudaEventDestroy(e);
-    for (cudaEvent_t e : ev_gathers) cudaEventDestroy(e);
-  }
-};
-
-namespace {
-
-int cuda_rc(cudaError_t e) { return e == cudaSuccess ? DHS_OK : DHS_ECUDA; }
 
 // Host-copy launch policy.
 //
@@ -441,53 +304,6 @@ int enter_step(dhs_pool* p, const dhs_step* st) {
   p->prefetch_pending = false;  // device selection only
   const int rc = enter(p);
   p->prefetch_pending = pending;
-  return rc;
-}
-
-// Room for n elements in all, so that adding them cannot throw.
-template <class T>
-bool room(std::vector<T>& v, size_t n) {
-  try {
-    v.reserve(n);
-  } catch (...) {
-    return false;
-  }
-  return true;
-}
-
-// Run `launch` on a caller's stream: after everything the pool's stream holds,
-// and joined by the pool's next call that can change rows.
-template <class Launch>
-int on_stream(dhs_pool* p, void* stream, Launch launch) {
-  cudaStream_t other = (cudaStream_t)stream;
-  cudaEvent_t done = nullptr;
-  // the events come back to ev_free when they are joined
-  const size_t gathers = p->ev_gathers.size() + 1;
-  if (!room(p->ev_gathers, gathers) || !room(p->ev_free, p->ev_free.size() + gathers))
-    return DHS_ENOMEM;
-  if (!p->ev_free.empty()) {
-    done = p->ev_free.back();
-    p->ev_free.pop_back();
-  } else if (cudaEventCreateWithFlags(&done, cudaEventDisableTiming) != cudaSuccess) {
-    return DHS_ECUDA;
-  }
-  // after everything the pool's stream holds (resolves, copies, appends)
-  if (cudaEventRecord(p->ev_main, p->stream) != cudaSuccess ||
-      cudaStreamWaitEvent(other, p->ev_main, 0) != cudaSuccess) {
-    p->ev_free.push_back(done);
-    return DHS_ECUDA;
-  }
-  cudaStream_t main = p->stream;
-  p->stream = other;
-  const int rc = launch();
-  p->stream = main;
-  // joined before the pool's next call that can change rows, even if the
-  // launch failed part way
-  if (cudaEventRecord(done, other) != cudaSuccess) {
-    p->ev_free.push_back(done);
-    return DHS_ECUDA;
-  }
-  p->ev_gathers.push_back(done);
   return rc;
 }
 
@@ -1827,6 +1643,27 @@ int dhs_read_state(dhs_pool* p, int32_t req, int32_t src, int32_t* tags, uint32_
 
 }  // extern "C"
 
+int dhs::check_attend_items(dhs_pool* p, const dhs_attend_item* items, int32_t n, int32_t heads) {
+  const dhs_pool_config& c = p->cfg;
+  for (int32_t i = 0; i < n; ++i) {
+    const dhs_attend_item& it = items[i];
+    if (it.queries < 0 || it.topk < 0 || (it.flags & ~DHS_ATTEND_HISTORY)) return DHS_EINVAL;
+    if ((int64_t)it.queries * heads > (int64_t)1 << 24) return DHS_EINVAL;
+    if (it.queries > 0 && (!it.q_dev || !it.out_dev)) return DHS_EINVAL;
+    if (((uintptr_t)it.q_dev | (uintptr_t)it.out_dev) & 1 || (uintptr_t)it.lse_dev & 3)
+      return DHS_EINVAL;
+    if (it.flags & DHS_ATTEND_HISTORY) {
+      if (it.req < 0 || it.req >= c.max_requests || it.src < 0 || it.src >= c.sources)
+        return DHS_EINVAL;
+      if (!p->ps[(int64_t)it.req * c.sources + it.src].admitted) return DHS_ESTATE;
+    } else {
+      const int64_t entries = (int64_t)it.queries * it.topk;
+      if (entries > INT32_MAX || (entries > 0 && !it.loc_dev)) return DHS_EINVAL;
+    }
+  }
+  return DHS_OK;
+}
+
 static int validate_attend(dhs_pool* p, const dhs_attend_step* st) {
   if (!p || !st || st->n_items < 0 || (st->n_items > 0 && !st->items)) return DHS_EINVAL;
   const dhs_pool_config& c = p->cfg;
@@ -1846,27 +1683,11 @@ static int validate_attend(dhs_pool* p, const dhs_attend_step* st) {
       !inside(st->value_offset, st->value_stride, st->value_elems))
     return DHS_EINVAL;
   if (!(st->scale - st->scale == 0.f)) return DHS_EINVAL;  // finite
-  for (int32_t i = 0; i < st->n_items; ++i) {
-    const dhs_attend_item& it = st->items[i];
-    if (it.queries < 0 || it.topk < 0 || (it.flags & ~DHS_ATTEND_HISTORY)) return DHS_EINVAL;
-    if ((int64_t)it.queries * st->heads > (int64_t)1 << 24) return DHS_EINVAL;
-    if (it.queries > 0 && (!it.q_dev || !it.out_dev)) return DHS_EINVAL;
-    if (((uintptr_t)it.q_dev | (uintptr_t)it.out_dev) & 1 || (uintptr_t)it.lse_dev & 3)
-      return DHS_EINVAL;
-    if (it.flags & DHS_ATTEND_HISTORY) {
-      if (it.req < 0 || it.req >= c.max_requests || it.src < 0 || it.src >= c.sources)
-        return DHS_EINVAL;
-      if (!p->ps[(int64_t)it.req * c.sources + it.src].admitted) return DHS_ESTATE;
-    } else {
-      const int64_t n = (int64_t)it.queries * it.topk;
-      if (n > INT32_MAX || (n > 0 && !it.loc_dev)) return DHS_EINVAL;
-    }
-  }
-  return DHS_OK;
+  return dhs::check_attend_items(p, st->items, st->n_items, st->heads);
 }
 
-// The common parameters and the item table (p->titems) of a validated step.
-static int attend_tables(dhs_pool* p, const dhs_attend_step* st, dhs::AttendCommon* out) {
+int dhs::fill_attend_items(dhs_pool* p, const dhs_attend_item* items, int32_t n,
+                           dhs::AttendCommon* out) {
   const dhs_pool_config& c = p->cfg;
   dhs::AttendCommon a{};
   a.tail = (const uint8_t*)c.tail_dev;
@@ -1881,26 +1702,12 @@ static int attend_tables(dhs_pool* p, const dhs_attend_step* st, dhs::AttendComm
   a.Pmax = (int32_t)p->pmax;
   a.page_shift = p->page_shift;
   a.status = p->status;
-  a.f16 = st->dtype == DHS_F16;
-  a.heads = st->heads;
-  a.group = st->heads / st->kv_heads;
-  a.dk = st->key_elems;
-  a.dv = st->value_elems;
-  a.key_off = st->key_offset * 2;
-  a.val_off = st->value_offset * 2;
-  a.key_stride = st->kv_heads > 1 ? st->key_stride * 2 : 0;
-  a.val_stride = st->kv_heads > 1 ? st->value_stride * 2 : 0;
-  a.scale = st->scale;
   a.polls = p->attend_polls;
-  a.q_qs = st->q_query_stride * 2;
-  a.q_hs = st->q_head_stride * 2;
-  a.o_qs = st->out_query_stride * 2;
-  a.o_hs = st->out_head_stride * 2;
   *out = a;
   try {
     p->titems.clear();
-    for (int32_t i = 0; i < st->n_items; ++i) {
-      const dhs_attend_item& it = st->items[i];
+    for (int32_t i = 0; i < n; ++i) {
+      const dhs_attend_item& it = items[i];
       if (it.queries == 0) continue;
       dhs::AttendItem t{};
       t.q = (const uint8_t*)it.q_dev;
@@ -1929,21 +1736,31 @@ static int attend_tables(dhs_pool* p, const dhs_attend_step* st, dhs::AttendComm
   return DHS_OK;
 }
 
-// Calls f(items, n) for every launch's share of the item table.
-template <class F>
-static int each_attend_launch(dhs_pool* p, F f) {
-  for (size_t b = 0; b < p->titems.size(); b += dhs::kAttendItemsLarge) {
-    const int n = (int)std::min<size_t>(dhs::kAttendItemsLarge, p->titems.size() - b);
-    const int rc = f(p->titems.data() + b, n);
-    if (rc) return rc;
-  }
-  return DHS_OK;
+// The common parameters and the item table (p->titems) of a validated step.
+static int attend_tables(dhs_pool* p, const dhs_attend_step* st, dhs::AttendCommon* out) {
+  dhs::AttendCommon& a = *out;
+  const int rc = dhs::fill_attend_items(p, st->items, st->n_items, out);
+  a.f16 = st->dtype == DHS_F16;
+  a.heads = st->heads;
+  a.group = st->heads / st->kv_heads;
+  a.dk = st->key_elems;
+  a.dv = st->value_elems;
+  a.key_off = st->key_offset * 2;
+  a.val_off = st->value_offset * 2;
+  a.key_stride = st->kv_heads > 1 ? st->key_stride * 2 : 0;
+  a.val_stride = st->kv_heads > 1 ? st->value_stride * 2 : 0;
+  a.scale = st->scale;
+  a.q_qs = st->q_query_stride * 2;
+  a.q_hs = st->q_head_stride * 2;
+  a.o_qs = st->out_query_stride * 2;
+  a.o_hs = st->out_head_stride * 2;
+  return rc;
 }
 
 // Workspace bytes of a step whose tables are made.
 static int attend_work(dhs_pool* p, const dhs::AttendCommon& a, size_t* bytes) {
   *bytes = 0;
-  return each_attend_launch(p, [&](dhs::AttendItem* items, int n) {
+  return dhs::each_attend_launch(p, [&](dhs::AttendItem* items, int n) {
     size_t need = 0;
     if (!dhs::attend_shape(a, items, n, std::max(1, p->sm_count), &need)) return DHS_EINVAL;
     *bytes = std::max(*bytes, need);
@@ -1964,10 +1781,22 @@ static int prepare_attend(dhs_pool* p, const dhs_attend_step* st, dhs::AttendCom
 }
 
 static int launch_attends(dhs_pool* p, const dhs_attend_step* st, const dhs::AttendCommon& a) {
-  return each_attend_launch(p, [&](dhs::AttendItem* items, int n) {
+  return dhs::each_attend_launch(p, [&](dhs::AttendItem* items, int n) {
     return cuda_rc(dhs::launch_attend(a, items, n, std::max(1, p->sm_count), st->work_dev, p->stream));
   });
 }
+
+// Attention only reads rows: gathers and attentions still running on other
+// streams need not be joined, an outstanding prefetch (which fills hot slots
+// that a location vector may name) is.
+int dhs::enter_reads(dhs_pool* p) {
+  p->join_gathers = false;
+  const int rc = enter(p);
+  p->join_gathers = true;
+  return rc ? rc : flush(p);
+}
+
+int dhs::enter_writes(dhs_pool* p) { return enter(p); }
 
 extern "C" {
 
@@ -1981,22 +1810,11 @@ int dhs_attend_bytes(dhs_pool* p, const dhs_attend_step* st, size_t* bytes) {
   return attend_work(p, a, bytes);
 }
 
-// Attention only reads rows: gathers and attentions still running on other
-// streams need not be joined, an outstanding prefetch (which fills hot slots
-// that a location vector may name) is.
-static int enter_attend(dhs_pool* p) {
-  p->join_gathers = false;
-  const int rc = enter(p);
-  p->join_gathers = true;
-  return rc;
-}
-
 int dhs_attend(dhs_pool* p, const dhs_attend_step* st) {
   dhs::AttendCommon a;
   int rc = prepare_attend(p, st, &a);
   if (rc) return rc;
-  if ((rc = enter_attend(p))) return rc;
-  if ((rc = flush(p))) return rc;
+  if ((rc = dhs::enter_reads(p))) return rc;
   return launch_attends(p, st, a);
 }
 
@@ -2005,8 +1823,7 @@ int dhs_attend_on(dhs_pool* p, const dhs_attend_step* st, void* stream) {
   dhs::AttendCommon a;
   int rc = prepare_attend(p, st, &a);
   if (rc) return rc;
-  if ((rc = enter_attend(p))) return rc;
-  if ((rc = flush(p))) return rc;
+  if ((rc = dhs::enter_reads(p))) return rc;
   for (const dhs::AttendItem& it : p->titems) p->map_readers |= !it.loc;
   return on_stream(p, stream, [&] { return launch_attends(p, st, a); });
 }
