@@ -1,6 +1,6 @@
-// Internal launch interface between the host pool manager (pool.cpp) and
+// Internal launch interface between the host pool manager (pool.cpp, packed.cpp) and
 // the sm_103a kernels (resolve.cu, hostcopy.cu, gather.cu, append.cu,
-// attend.cu, fork.cu).
+// attend.cu, attend_merge.cu, attend_packed.cu, packed_rows.cu, fork.cu).
 // Not part of the C ABI.
 //
 // Item tables travel by value in the kernel parameter space
@@ -334,6 +334,96 @@ constexpr uint32_t kAttendPolls = 1u << 22;  // DHS_OPT_ATTEND_POLLS default
 bool attend_shape(AttendCommon c, AttendItem* items, int n_items, int sms, size_t* bytes);
 cudaError_t launch_attend(AttendCommon c, AttendItem* items, int n_items, int sms,
                           void* work, cudaStream_t stream);
+
+// ------------------------------------------------------------ rows in 8 bits
+
+// A packed row's parts: heads, elements of a head, bytes of the row.
+struct PackedLayout {
+  int32_t kv, key8, wide;
+  int32_t value;      // of a value head, shared or not
+  int32_t shared;
+  int32_t off_value, off_wide, off_scale, row_bytes;
+  int32_t f16;
+};
+
+// The rotation of heads (rotary 0: none).
+struct Rotation {
+  const uint64_t* turns;
+  int32_t offset, rotary;
+  int32_t interleaved;
+  float amplitude;
+  float sign;         // -1: turned back
+};
+
+struct RotateParams {
+  const uint8_t* x;
+  uint8_t* y;
+  const int32_t* position;
+  Rotation r;
+  int32_t tokens, heads, elems, f16;
+  int64_t x_ts, x_hs, y_ts, y_hs;  // bytes
+};
+cudaError_t launch_rotate(const RotateParams& p, int sms, cudaStream_t stream);
+
+constexpr int kRotaryMax = 4096;  // rotary elements whose sines a block holds
+constexpr int kPackItemsMax = 256, kUnpackItemsMax = 256;
+
+struct PackItem {
+  const uint8_t* key;
+  const uint8_t* wide;
+  const uint8_t* value;
+  const int32_t* position;
+  uint8_t* rows;   // consecutive rows, or null: appended to the pair
+  uint8_t* host;   // of an appended row (null: a window source)
+  int64_t L0;
+  int32_t pair;
+  int32_t count;
+};
+
+struct PackCommon {
+  PackedLayout l;
+  Rotation r;
+  uint8_t* tail;
+  int32_t T, n_items;
+  int64_t tokens;                          // of all items
+  int64_t k_ts, k_hs, w_ts, w_hs, v_ts, v_hs;  // bytes
+};
+cudaError_t launch_pack(const PackCommon& c, const PackItem* items, int n_items, int sms,
+                        cudaStream_t stream);
+
+struct UnpackItem {
+  const uint32_t* loc;    // located rows, else null
+  const uint8_t* rows;    // consecutive rows, else null
+  const uint8_t* host;    // history: device-visible host rows (null: a window source)
+  uint8_t* key;           // or null
+  uint8_t* value;         // or null
+  int64_t first, L;       // history
+  int32_t pair, complete;
+  int32_t count;
+};
+
+struct UnpackCommon {
+  PackedLayout l;
+  const uint8_t* tail;
+  const uint8_t* opt;
+  const uint8_t* hot;
+  const int32_t* map;
+  uint32_t tail_rows, opt_rows, hot_rows;
+  int32_t T, Pmax, page_shift, n_items;
+  uint32_t* status;
+  int64_t count;                           // of all items
+  int64_t k_rs, k_hs, v_rs, v_hs;          // bytes
+};
+cudaError_t launch_unpack(const UnpackCommon& c, const UnpackItem* items, int n_items, int sms,
+                          cudaStream_t stream);
+
+// Attention over packed rows (attend_packed.cu), as attend_shape and
+// launch_attend; of the common parameters dk, key_off, val_off and their
+// strides are not read.
+bool attend_packed_shape(AttendCommon c, const PackedLayout& l, AttendItem* items, int n_items,
+                         int sms, size_t* bytes);
+cudaError_t launch_attend_packed(AttendCommon c, const PackedLayout& l, AttendItem* items,
+                                 int n_items, int sms, void* work, cudaStream_t stream);
 
 // ------------------------------------------------------------ forks
 constexpr int kForkSourcesMax = 256;

@@ -54,6 +54,11 @@ DHS_OPT_ATTEND_POLLS = 13
 DHS_BF16, DHS_F16 = 0, 1
 DHS_ATTEND_HISTORY = 1
 DHS_ATTEND_MAX_KEY, DHS_ATTEND_MAX_VALUE = 576, 512
+DHS_ROPE_PLAIN, DHS_ROPE_LINEAR, DHS_ROPE_BASE, DHS_ROPE_PARTS = range(4)
+DHS_ROPE_HALF, DHS_ROPE_INTERLEAVED = 0, 1
+DHS_ROPE_INVERSE = 1
+DHS_PACKED_MAX_WIDE = 64
+DHS_UNPACK_HISTORY = 1
 DHS_BUF_HOT, DHS_BUF_TAIL, DHS_BUF_OPT, DHS_BUF_META = range(4)
 
 _i32, _i64, _u32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_void_p
@@ -102,6 +107,62 @@ class dhs_attend_step(ctypes.Structure):
                 ("work_bytes", ctypes.c_size_t)]
 
 
+_f64, _f32 = ctypes.c_double, ctypes.c_float
+
+
+class dhs_rope_config(ctypes.Structure):
+    _fields_ = [("rotary_elems", _i32), ("scaling", _i32), ("base", _f64), ("factor", _f64),
+                ("original", _f64), ("fast", _f64), ("slow", _f64)]
+
+
+class dhs_rotate_step(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("tokens", _i32), ("heads", _i32), ("head_elems", _i32),
+                ("rotary_offset", _i32), ("rotary_elems", _i32), ("pairs", _i32), ("flags", _u32),
+                ("amplitude", _f32), ("reserved", _i32), ("x_token_stride", _i64),
+                ("x_head_stride", _i64), ("y_token_stride", _i64), ("y_head_stride", _i64),
+                ("x_dev", _vp), ("y_dev", _vp), ("position_dev", _vp), ("turns_dev", _vp)]
+
+
+class dhs_packed_rows(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("kv_heads", _i32), ("key_elems", _i32), ("wide_elems", _i32),
+                ("value_elems", _i32), ("shared", _i32)]
+
+
+class dhs_pack_item(ctypes.Structure):
+    _fields_ = [("req", _i32), ("src", _i32), ("count", _i32), ("reserved", _i32),
+                ("key_dev", _vp), ("wide_dev", _vp), ("value_dev", _vp), ("position_dev", _vp),
+                ("rows_dev", _vp)]
+
+
+class dhs_pack_step(ctypes.Structure):
+    _fields_ = [("rows", dhs_packed_rows), ("n_items", _i32), ("rotary_offset", _i32),
+                ("rotary_elems", _i32), ("pairs", _i32), ("amplitude", _f32), ("reserved", _i32),
+                ("key_token_stride", _i64), ("key_head_stride", _i64),
+                ("wide_token_stride", _i64), ("wide_head_stride", _i64),
+                ("value_token_stride", _i64), ("value_head_stride", _i64),
+                ("turns_dev", _vp), ("items", ctypes.POINTER(dhs_pack_item))]
+
+
+class dhs_unpack_item(ctypes.Structure):
+    _fields_ = [("req", _i32), ("src", _i32), ("count", _i32), ("flags", _u32), ("first", _i64),
+                ("loc_dev", _vp), ("rows_dev", _vp), ("key_dev", _vp), ("value_dev", _vp)]
+
+
+class dhs_unpack_step(ctypes.Structure):
+    _fields_ = [("rows", dhs_packed_rows), ("n_items", _i32), ("reserved", _i32),
+                ("key_row_stride", _i64), ("key_head_stride", _i64),
+                ("value_row_stride", _i64), ("value_head_stride", _i64),
+                ("items", ctypes.POINTER(dhs_unpack_item))]
+
+
+class dhs_attend_packed_step(ctypes.Structure):
+    _fields_ = [("rows", dhs_packed_rows), ("n_items", _i32), ("heads", _i32), ("scale", _f32),
+                ("reserved", _i32), ("q_query_stride", _i64), ("q_head_stride", _i64),
+                ("out_query_stride", _i64), ("out_head_stride", _i64),
+                ("items", ctypes.POINTER(dhs_attend_item)), ("work_dev", _vp),
+                ("work_bytes", ctypes.c_size_t)]
+
+
 class dhs_step(ctypes.Structure):
     _fields_ = [("step", _u32), ("n_items", _i32), ("items", ctypes.POINTER(dhs_item))]
 
@@ -141,6 +202,18 @@ def _load():
         "dhs_attend_bytes": (ctypes.c_int, [_vp, P(dhs_attend_step), P(ctypes.c_size_t)]),
         "dhs_attend": (ctypes.c_int, [_vp, P(dhs_attend_step)]),
         "dhs_attend_on": (ctypes.c_int, [_vp, P(dhs_attend_step), _vp]),
+        "dhs_rope_table": (ctypes.c_int, [_vp, _vp]),
+        "dhs_rotate": (ctypes.c_int, [_vp, P(dhs_rotate_step)]),
+        "dhs_rotate_on": (ctypes.c_int, [_vp, P(dhs_rotate_step), _vp]),
+        "dhs_packed_bytes": (ctypes.c_int, [_vp, P(_i32)]),
+        "dhs_pack": (ctypes.c_int, [_vp, P(dhs_pack_step)]),
+        "dhs_append_packed": (ctypes.c_int, [_vp, P(dhs_pack_step)]),
+        "dhs_unpack": (ctypes.c_int, [_vp, P(dhs_unpack_step)]),
+        "dhs_unpack_on": (ctypes.c_int, [_vp, P(dhs_unpack_step), _vp]),
+        "dhs_attend_packed_bytes": (ctypes.c_int, [_vp, P(dhs_attend_packed_step),
+                                                   P(ctypes.c_size_t)]),
+        "dhs_attend_packed": (ctypes.c_int, [_vp, P(dhs_attend_packed_step)]),
+        "dhs_attend_packed_on": (ctypes.c_int, [_vp, P(dhs_attend_packed_step), _vp]),
         "dhs_fork": (ctypes.c_int, [_vp, _i32, _i32, P(_vp), P(_vp), P(_i64)]),
         "dhs_compact": (ctypes.c_int, [_vp, _i64, P(_i64)]),
         "dhs_pool_capacity": (_i64, [_vp]),
@@ -257,10 +330,14 @@ def make_step(step: int, items) -> tuple:
     return dhs_step(step, len(items), arr), arr
 
 
+def _address(t):
+    return t.data_ptr() if hasattr(t, "data_ptr") else t
+
+
 def attend_item(*, queries, q, out, req=0, src=0, topk=0, flags=0, loc=None, index=None,
                 range_=None, lse=None) -> dhs_attend_item:
     """A dhs_attend_item from torch tensors (or device addresses)."""
-    ptr = lambda t: t.data_ptr() if hasattr(t, "data_ptr") else t
+    ptr = _address
     it = dhs_attend_item()
     it.req, it.src, it.queries, it.topk, it.flags = req, src, queries, topk, flags
     it.q_dev, it.out_dev, it.loc_dev = ptr(q), ptr(out), ptr(loc)
@@ -301,6 +378,165 @@ def dhs_attend(h, st: dhs_attend_step):
 
 def dhs_attend_on(h, st: dhs_attend_step, stream):
     return lib.dhs_attend_on(h, ctypes.byref(st), stream)
+
+
+_DTYPES = {"bf16": DHS_BF16, "f16": DHS_F16}
+_PAIRS = {"half": DHS_ROPE_HALF, "interleaved": DHS_ROPE_INTERLEAVED}
+_SCALINGS = {"plain": DHS_ROPE_PLAIN, "linear": DHS_ROPE_LINEAR, "base": DHS_ROPE_BASE,
+             "parts": DHS_ROPE_PARTS}
+
+
+def rope_table(rotary, *, base=10000.0, scaling="plain", factor=1.0, original=0.0, fast=32.0,
+               slow=1.0):
+    """dhs_rope_table's turns as an int64 array (the bits of the uint64s), which
+    torch.from_numpy takes: move it to the GPU once and hand it to make_rotate
+    and make_pack."""
+    cfg = dhs_rope_config(rotary, _SCALINGS[scaling], base, factor, original, fast, slow)
+    out = np.empty(max(1, rotary // 2), np.int64)
+    check(lib.dhs_rope_table(ctypes.byref(cfg), out.ctypes.data), "dhs_rope_table")
+    return out
+
+
+def _torch_dtype(t):
+    name = {"torch.bfloat16": "bf16", "torch.float16": "f16"}.get(str(t.dtype))
+    if name is None:
+        raise ValueError(f"a bfloat16 or float16 tensor is needed, not {t.dtype}")
+    return name
+
+
+def make_rotate(x, positions, turns, *, out=None, offset=0, rotary=None, pairs="half",
+                inverse=False, amplitude=1.0) -> dhs_rotate_step:
+    """A dhs_rotate_step over x [tokens][heads][elems] (the elements of a head
+    contiguous) into `out` of the same shape, or in place.  positions: int32
+    [tokens], turns: the table on the GPU; all must outlive the step."""
+    out = x if out is None else out
+    if x.dim() != 3 or out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("x and out: [tokens][heads][elems] of one type")
+    if x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("the elements of a head must be contiguous")
+    rotary = x.shape[2] - offset if rotary is None else rotary
+    if str(positions.dtype) != "torch.int32" or positions.numel() < x.shape[0] or \
+            not positions.is_contiguous():
+        raise ValueError("positions: contiguous int32, one a token")
+    if turns.element_size() != 8 or turns.numel() < rotary // 2 or not turns.is_contiguous():
+        raise ValueError("turns: contiguous 64-bit, one a pair")
+    st = dhs_rotate_step()
+    st.dtype = _DTYPES[_torch_dtype(x)]
+    st.tokens, st.heads, st.head_elems = x.shape
+    st.rotary_offset, st.rotary_elems, st.pairs = offset, rotary, _PAIRS[pairs]
+    st.flags, st.amplitude = DHS_ROPE_INVERSE if inverse else 0, amplitude
+    st.x_token_stride, st.x_head_stride = x.stride()[:2]
+    st.y_token_stride, st.y_head_stride = out.stride()[:2]
+    st.x_dev, st.y_dev = x.data_ptr(), out.data_ptr()
+    st.position_dev, st.turns_dev = positions.data_ptr(), turns.data_ptr()
+    return st
+
+
+def dhs_rotate(h, st: dhs_rotate_step):
+    return lib.dhs_rotate(h, ctypes.byref(st))
+
+
+def dhs_rotate_on(h, st: dhs_rotate_step, stream):
+    return lib.dhs_rotate_on(h, ctypes.byref(st), stream)
+
+
+def packed_rows(*, key_elems, value_elems, kv_heads=1, wide_elems=0, shared=False,
+                dtype="bf16") -> dhs_packed_rows:
+    return dhs_packed_rows(_DTYPES[dtype], kv_heads, key_elems, wide_elems, value_elems, int(shared))
+
+
+def dhs_packed_bytes(rows: dhs_packed_rows) -> int:
+    n = _i32(0)
+    check(lib.dhs_packed_bytes(ctypes.byref(rows), ctypes.byref(n)), "dhs_packed_bytes")
+    return n.value
+
+
+def pack_item(count, key, *, wide=None, value=None, positions=None, rows=None, req=0,
+              src=0) -> dhs_pack_item:
+    """A dhs_pack_item from torch tensors (or device addresses)."""
+    return dhs_pack_item(req, src, count, 0, *[_address(t) for t in (key, wide, value, positions,
+                                                                     rows)])
+
+
+def make_pack(items, rows, *, rotary_offset=0, rotary_elems=0, pairs="half", amplitude=1.0,
+              turns=None, key_strides=None, wide_strides=None, value_strides=None) -> tuple:
+    """A dhs_pack_step plus the item array that must stay alive with it.
+    Strides are (between tokens, between heads) in elements; the default is
+    contiguous [count][kv_heads][elems]."""
+    arr = (dhs_pack_item * max(1, len(items)))(*items)
+    st = dhs_pack_step()
+    st.rows, st.n_items, st.items = rows, len(items), arr
+    st.rotary_offset, st.rotary_elems = rotary_offset, rotary_elems
+    st.pairs, st.amplitude, st.turns_dev = _PAIRS[pairs], amplitude, _address(turns)
+    n = rows.key_elems - rows.wide_elems
+    flat = lambda m: (rows.kv_heads * m, m)  # noqa: E731
+    st.key_token_stride, st.key_head_stride = key_strides or flat(n)
+    st.wide_token_stride, st.wide_head_stride = wide_strides or flat(rows.wide_elems)
+    st.value_token_stride, st.value_head_stride = value_strides or flat(rows.value_elems)
+    return st, arr
+
+
+def dhs_pack(h, st: dhs_pack_step):
+    return lib.dhs_pack(h, ctypes.byref(st))
+
+
+def dhs_append_packed(h, st: dhs_pack_step):
+    return lib.dhs_append_packed(h, ctypes.byref(st))
+
+
+def unpack_item(count, key, *, value=None, loc=None, rows=None, req=0, src=0, first=0,
+                flags=0) -> dhs_unpack_item:
+    """A dhs_unpack_item from torch tensors (or device addresses)."""
+    return dhs_unpack_item(req, src, count, flags, first, *[_address(t) for t in (loc, rows, key,
+                                                                                  value)])
+
+
+def make_unpack(items, rows, *, key_strides=None, value_strides=None) -> tuple:
+    """A dhs_unpack_step plus the item array that must stay alive with it.
+    Strides are (between rows, between heads) in elements; the default is
+    contiguous [count][kv_heads][elems]."""
+    arr = (dhs_unpack_item * max(1, len(items)))(*items)
+    st = dhs_unpack_step()
+    st.rows, st.n_items, st.items = rows, len(items), arr
+    flat = lambda m: (rows.kv_heads * m, m)  # noqa: E731
+    st.key_row_stride, st.key_head_stride = key_strides or flat(rows.key_elems)
+    st.value_row_stride, st.value_head_stride = value_strides or flat(rows.value_elems)
+    return st, arr
+
+
+def dhs_unpack(h, st: dhs_unpack_step):
+    return lib.dhs_unpack(h, ctypes.byref(st))
+
+
+def dhs_unpack_on(h, st: dhs_unpack_step, stream):
+    return lib.dhs_unpack_on(h, ctypes.byref(st), stream)
+
+
+def make_attend_packed(items, rows, *, heads, scale, q_strides=None, out_strides=None) -> tuple:
+    """A dhs_attend_packed_step (without a workspace) over attend_item()s plus
+    the item array that must stay alive with it; strides as make_attend's."""
+    arr = (dhs_attend_item * max(1, len(items)))(*items)
+    st = dhs_attend_packed_step()
+    st.rows, st.n_items, st.items, st.heads, st.scale = rows, len(items), arr, heads, scale
+    n, m = rows.key_elems, rows.value_elems
+    st.q_query_stride, st.q_head_stride = q_strides or (heads * n, n)
+    st.out_query_stride, st.out_head_stride = out_strides or (heads * m, m)
+    return st, arr
+
+
+def dhs_attend_packed_bytes(h, st: dhs_attend_packed_step) -> int:
+    n = ctypes.c_size_t(0)
+    check(lib.dhs_attend_packed_bytes(h, ctypes.byref(st), ctypes.byref(n)),
+          "dhs_attend_packed_bytes")
+    return n.value
+
+
+def dhs_attend_packed(h, st: dhs_attend_packed_step):
+    return lib.dhs_attend_packed(h, ctypes.byref(st))
+
+
+def dhs_attend_packed_on(h, st: dhs_attend_packed_step, stream):
+    return lib.dhs_attend_packed_on(h, ctypes.byref(st), stream)
 
 
 def dhs_fork(h, req, child, host_ptrs, masks=None):
@@ -526,6 +762,33 @@ class Pool:
 
     def attend_on(self, st, stream):
         return dhs_attend_on(self.h, st, stream)
+
+    def rotate(self, st):
+        return dhs_rotate(self.h, st)
+
+    def rotate_on(self, st, stream):
+        return dhs_rotate_on(self.h, st, stream)
+
+    def pack(self, st):
+        return dhs_pack(self.h, st)
+
+    def append_packed(self, st):
+        return dhs_append_packed(self.h, st)
+
+    def unpack(self, st):
+        return dhs_unpack(self.h, st)
+
+    def unpack_on(self, st, stream):
+        return dhs_unpack_on(self.h, st, stream)
+
+    def attend_packed_bytes(self, st):
+        return dhs_attend_packed_bytes(self.h, st)
+
+    def attend_packed(self, st):
+        return dhs_attend_packed(self.h, st)
+
+    def attend_packed_on(self, st, stream):
+        return dhs_attend_packed_on(self.h, st, stream)
 
     def fork(self, req, child, host_ptrs, masks=None):
         return dhs_fork(self.h, req, child, host_ptrs, masks)

@@ -652,6 +652,253 @@ int dhs_compact(dhs_pool *pool, int64_t capacity_pages, int64_t *moved);
 /* The optional capacity in pages that dhs_compact set (-1: null pool). */
 int64_t dhs_pool_capacity(const dhs_pool *pool);
 
+/* --------------------------------------------------------- rotary positions */
+
+/* How the frequencies of dhs_rope_table follow a context longer than the one
+ * trained on, `factor` times as long. */
+#define DHS_ROPE_PLAIN 0  /* base^(-2i / rotary_elems) radians a position */
+#define DHS_ROPE_LINEAR 1 /* all of them divided by factor */
+#define DHS_ROPE_BASE 2   /* base raised to base * factor^(n / (n - 2)), n = rotary_elems */
+#define DHS_ROPE_PARTS 3  /* pairs that turn more than `fast` times over `original`
+                           * positions as they are, those that turn less than `slow`
+                           * times divided by factor, between them a mean of both,
+                           * weighted linearly by the turns */
+
+typedef struct {
+  int32_t rotary_elems; /* elements of a head that turn: a multiple of 16 */
+  int32_t scaling;
+  double base;          /* > 1 */
+  double factor;        /* >= 1; DHS_ROPE_PLAIN ignores it */
+  double original;      /* DHS_ROPE_PARTS: > 0 */
+  double fast, slow;    /* DHS_ROPE_PARTS: fast > slow >= 0 */
+} dhs_rope_config;
+
+/*
+ * What each of the rotary_elems / 2 pairs turns by from one position to the
+ * next, in turns times 2^64: position times turns modulo 2^64 is then the
+ * angle, exact at any position (the fraction of a turn alone matters), where a
+ * product in floating point loses the far ones.  Host arithmetic in double.
+ * Errors: DHS_EINVAL.
+ */
+int dhs_rope_table(const dhs_rope_config *cfg, uint64_t *turns);
+
+/* Which elements of the rotary_elems make a pair. */
+#define DHS_ROPE_HALF 0        /* i and rotary_elems / 2 + i */
+#define DHS_ROPE_INTERLEAVED 1 /* 2i and 2i + 1 */
+
+#define DHS_ROPE_INVERSE 1u /* turn back: dhs_rotate's gradient (the same
+                             * amplitude), or a stored key's position undone */
+
+/*
+ * A rotation of heads: elements [rotary_offset, rotary_offset + rotary_elems)
+ * of each head, pair (a, b) at angle t = position * turns of its pair becoming
+ * amplitude * (a cos t - b sin t, b cos t + a sin t); the other elements are
+ * copied.  x and y may be the same tensor (then nothing is copied) but not
+ * overlap otherwise.
+ *   x_dev, y_dev   [tokens][heads][head_elems] of `dtype` by strides in
+ *                  elements; 2-byte aligned (16-byte aligned tensors whose
+ *                  strides are multiples of 8 move faster)
+ *   position_dev   int32 [tokens]
+ *   turns_dev      uint64 [rotary_elems / 2] (dhs_rope_table), device memory
+ * head_elems and rotary_offset are multiples of 8, rotary_elems of 16.
+ */
+typedef struct {
+  int32_t dtype;
+  int32_t tokens;
+  int32_t heads;
+  int32_t head_elems;
+  int32_t rotary_offset;
+  int32_t rotary_elems;
+  int32_t pairs;
+  uint32_t flags;
+  float amplitude;
+  int32_t reserved;
+  int64_t x_token_stride, x_head_stride;
+  int64_t y_token_stride, y_head_stride;
+  const void *x_dev;
+  void *y_dev;
+  const int32_t *position_dev;
+  const uint64_t *turns_dev;
+} dhs_rotate_step;
+
+/* Angles, sines and products in float, rounded once.  On the pool's stream;
+ * touches nothing of the pool.  Errors: DHS_EINVAL, DHS_ECUDA. */
+int dhs_rotate(dhs_pool *pool, const dhs_rotate_step *st);
+
+/* dhs_rotate on a caller's stream of the pool's device (not NULL), in that
+ * stream's order alone. */
+int dhs_rotate_on(dhs_pool *pool, const dhs_rotate_step *st, void *stream);
+
+/* --------------------------------------------------------- rows in 8 bits */
+
+/* Largest number of 16-bit elements at the end of a packed key head. */
+#define DHS_PACKED_MAX_WIDE 64
+
+/*
+ * A packed row: keys and values as e4m3 codes with a scale for each head of
+ * each row, and, where asked, the last wide_elems of each key head (a rotary
+ * part, say) unchanged in 16 bits.  A row of 512 + 64 shared latent elements
+ * takes 656 bytes instead of 1152; host link, copies, hot cache and attention
+ * all move that much less.  To resolves, gathers, forks and the rest it is a
+ * row like any other.  In bytes, back to back:
+ *   [kv_heads][key_elems - wide_elems]  key codes
+ *   [kv_heads][value_elems]             value codes (none if shared)
+ *   [kv_heads][wide_elems]              16-bit elements of `dtype`
+ *   float [kv_heads] key scales, float [kv_heads] value scales (none if
+ *   shared); zeros up to a multiple of 16
+ * A code c of scale z stands for c * z.  The scale is a power of two, so that
+ * this is exact in either 16-bit type's significand: 2^e with the smallest e
+ * in [-64, 120] that brings the head's largest finite element to 448 or
+ * below; elements are rounded to nearest, ties to even (half a step is 2^-4
+ * of the element, or 2^-10 of the scale if that is more).  An element that is
+ * not finite is held as NaN.  One row, not a block of rows, shares a scale:
+ * rows are appended, evicted and fetched one at a time.
+ */
+typedef struct {
+  int32_t dtype;       /* DHS_BF16 or DHS_F16: of everything in 16 bits */
+  int32_t kv_heads;
+  int32_t key_elems;   /* of a head, wide ones included; at most DHS_ATTEND_MAX_KEY */
+  int32_t wide_elems;  /* multiple of 8, at most DHS_PACKED_MAX_WIDE; key_elems -
+                        * wide_elems is a positive multiple of 16 */
+  int32_t value_elems; /* multiple of 16, at most DHS_ATTEND_MAX_VALUE */
+  int32_t shared;      /* 1: the value is the first value_elems of the key's codes,
+                        * held once; else 0 */
+} dhs_packed_rows;
+
+/* Bytes of a packed row (a multiple of 16, at most 65536): the row_bytes of a
+ * pool that holds them.  Host arithmetic.  Errors: DHS_EINVAL. */
+int dhs_packed_bytes(const dhs_packed_rows *rows, int32_t *row_bytes);
+
+/* `count` rows to be packed, from device tensors of the layout's dtype by the
+ * step's strides. */
+typedef struct {
+  int32_t req;                 /* dhs_append_packed */
+  int32_t src;
+  int32_t count;
+  int32_t reserved;
+  const void *key_dev;         /* [count][kv_heads][key_elems - wide_elems] */
+  const void *wide_dev;        /* [count][kv_heads][wide_elems], NULL if there are none */
+  const void *value_dev;       /* [count][kv_heads][value_elems], NULL if shared */
+  const int32_t *position_dev; /* [count], NULL without a rotation */
+  void *rows_dev;              /* dhs_pack: [count][dhs_packed_bytes], 16-byte aligned */
+} dhs_pack_item;
+
+/* Strides are in elements.  rotary_elems > 0: elements [rotary_offset,
+ * rotary_offset + rotary_elems) of each key head, wide ones counted last, are
+ * turned as in dhs_rotate before they are packed, in float; the range lies
+ * wholly among the coded or wholly among the wide elements. */
+typedef struct {
+  dhs_packed_rows rows;
+  int32_t n_items;
+  int32_t rotary_offset;
+  int32_t rotary_elems;
+  int32_t pairs;
+  float amplitude;
+  int32_t reserved;
+  int64_t key_token_stride, key_head_stride;
+  int64_t wide_token_stride, wide_head_stride;
+  int64_t value_token_stride, value_head_stride;
+  const uint64_t *turns_dev; /* NULL without a rotation */
+  const dhs_pack_item *items;
+} dhs_pack_step;
+
+/* Pack rows into the caller's memory: a prompt's rows for dhs_admit_device or
+ * dhs_admit_window, for instance.  On the pool's stream; touches nothing of
+ * the pool, whose rows may be of another size.  Errors: DHS_EINVAL,
+ * DHS_ENOMEM, DHS_ECUDA. */
+int dhs_pack(dhs_pool *pool, const dhs_pack_step *st);
+
+/* Pack rows and append them as dhs_append would (the tail ring, and the pinned
+ * host copy of a source that has one), in one launch: rows_dev is unused.
+ * The pool's row_bytes must be dhs_packed_bytes.  Errors: as dhs_append and
+ * dhs_pack. */
+int dhs_append_packed(dhs_pool *pool, const dhs_pack_step *st);
+
+#define DHS_UNPACK_HISTORY 1u /* rows of a source by number */
+
+/*
+ * `count` packed rows to be read back:
+ *   - DHS_UNPACK_HISTORY: rows [first, first + count) of (req, src), each at
+ *     the first of the tail ring, a ready optional page and the pinned host
+ *     copy.  All of them must be served: DHS_EINVAL outside [0, L), or
+ *     [L - tail_rows, L) of a window source;
+ *   - else, rows_dev not NULL: consecutive rows of the caller's memory;
+ *   - else the rows that loc_dev [count] names.  As in dhs_gather DHS_NO_LOC
+ *     gives zeros, DHS_END_LOC leaves the output untouched, a location outside
+ *     its arena gives zeros and DHS_STATUS_ELOC.
+ */
+typedef struct {
+  int32_t req;
+  int32_t src;
+  int32_t count;
+  uint32_t flags;
+  int64_t first;
+  const uint32_t *loc_dev;
+  const void *rows_dev;  /* 16-byte aligned */
+  void *key_dev;         /* [count][kv_heads][key_elems] out, or NULL */
+  void *value_dev;       /* [count][kv_heads][value_elems] out, or NULL */
+} dhs_unpack_item;
+
+/* Strides of the outputs in elements.  A shared value is part of the key;
+ * asked for, it is written a second time. */
+typedef struct {
+  dhs_packed_rows rows;
+  int32_t n_items;
+  int32_t reserved;
+  int64_t key_row_stride, key_head_stride;
+  int64_t value_row_stride, value_head_stride;
+  const dhs_unpack_item *items;
+} dhs_unpack_step;
+
+/* Read packed rows back into 16 bits: an attention in 16 bits of a prompt's
+ * next chunk, or staging.  Codes times scales, rounded once (exact unless the
+ * number leaves an f16's range); wide elements as they are.  The pool's
+ * row_bytes must be dhs_packed_bytes unless every item names rows_dev.
+ * Asynchronous, in order on the pool's stream.  Errors: DHS_EINVAL,
+ * DHS_ESTATE, DHS_ENOMEM, DHS_ECUDA. */
+int dhs_unpack(dhs_pool *pool, const dhs_unpack_step *st);
+
+/* dhs_unpack on a caller's stream (not NULL), ordered as dhs_gather_on. */
+int dhs_unpack_on(dhs_pool *pool, const dhs_unpack_step *st, void *stream);
+
+/* An attention step over packed rows: items, heads, strides and workspace as
+ * in dhs_attend_step; queries [Q][heads][key_elems] and outputs
+ * [Q][heads][value_elems] of the layout's dtype. */
+typedef struct {
+  dhs_packed_rows rows;
+  int32_t n_items;
+  int32_t heads;
+  float scale;
+  int32_t reserved;
+  int64_t q_query_stride;
+  int64_t q_head_stride;
+  int64_t out_query_stride;
+  int64_t out_head_stride;
+  const dhs_attend_item *items;
+  void *work_dev;
+  size_t work_bytes;
+} dhs_attend_packed_step;
+
+/* As dhs_attend_bytes, with its bound. */
+int dhs_attend_packed_bytes(dhs_pool *pool, const dhs_attend_packed_step *st, size_t *bytes);
+
+/*
+ * dhs_attend over packed rows, located or a source's history, read in 8 bits
+ * where they lie: the attention of the numbers that the rows' codes and wide
+ * elements stand for, which dhs_unpack would give.  Scores, weights' sums and
+ * outputs are accumulated in float.  The products take queries and weights in
+ * 8-bit pieces whose sum they are: a query's coded part exactly, but for less
+ * than 2^-18 of its largest element; a weight (times its row's value scale) to
+ * 2^-8 of itself, or 2^-11 if the type is DHS_F16, down to 2^-27 of the largest
+ * of its query.  A query's coded part that holds an infinity or NaN gives NaN.
+ * The pool's row_bytes must be dhs_packed_bytes.  Order, bits and errors as
+ * dhs_attend's.
+ */
+int dhs_attend_packed(dhs_pool *pool, const dhs_attend_packed_step *st);
+
+/* dhs_attend_packed on a caller's stream (not NULL), ordered as dhs_gather_on. */
+int dhs_attend_packed_on(dhs_pool *pool, const dhs_attend_packed_step *st, void *stream);
+
 /*
  * Synchronise the pool's stream, read and clear the sticky device status.
  * The pages have no passage for this call: device-side errors cannot be
