@@ -66,6 +66,10 @@
 namespace dhs {
 namespace {
 
+constexpr int kSoftThreads = 256, kLoadThreads = 128;
+constexpr int kIssueWarp = (kSoftThreads + kLoadThreads) / 32, kFindWarp = kIssueWarp + 1;
+constexpr int kRowWarp = kFindWarp + 1, kRowThreads = 64;
+constexpr int kThreads = 32 * kRowWarp + kRowThreads;
 constexpr int kChunk = kTile * 128;        // bytes of a 64-element column chunk of a tile
 constexpr int kUnit = 2 * kChunk;          // a value unit: 128 elements
 constexpr int kMaxK = 12, kMaxV = 8;       // ring slots at most
@@ -92,7 +96,7 @@ static_assert(sizeof(Params<kAttendItemsLarge>) <= 32764, "attend item table too
 
 constexpr int kUnusedBars = 8 - 2 * kRowSlots;
 struct Control {
-  static constexpr int kRowSlots = dhs::kRowSlots;
+  static constexpr int kRowSlots = dhs::kRowSlots, kRowThreads = dhs::kRowThreads;
   uint64_t kfull[kMaxK], kempty[kMaxK], vfull[kMaxV], vempty[kMaxV];
   uint64_t qfull, qempty, sfull[2], pfull, odone, oempty, rfull[kRowSlots], rempty[kRowSlots], drain;
   uint64_t segfull[kSegments], segempty[kSegments];

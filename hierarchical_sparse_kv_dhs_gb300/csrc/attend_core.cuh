@@ -51,12 +51,7 @@ inline uint32_t round_up(uint32_t x, uint32_t to) { return (x + to - 1) / to * t
 #ifdef __CUDACC__
 namespace {
 
-constexpr int kSoftThreads = 256, kLoadThreads = 128;
-constexpr int kIssueWarp = (kSoftThreads + kLoadThreads) / 32, kFindWarp = kIssueWarp + 1;
-constexpr int kRowWarp = kFindWarp + 1, kRowThreads = 64;
-constexpr int kThreads = 32 * kRowWarp + kRowThreads;
 constexpr int kSegments = 4;               // segments found ahead
-
 
 // A launch's item table, which travels with it.
 template <int MAXI, class Plan>
@@ -454,7 +449,7 @@ __device__ void find_segments(const P_& P, C_& ctl) {
 // Row warps: the addresses of every tile's rows, ahead of the loading warps.
 template <class P_, class C_>
 __device__ void find_rows(const P_& P, C_& ctl, int tid) {
-  constexpr int R = kTile / kRowThreads, kRowSlots = C_::kRowSlots;
+  constexpr int kRowThreads = C_::kRowThreads, kRowSlots = C_::kRowSlots, R = kTile / kRowThreads;
   const AttendCommon& c = P.c;
   const Patience until{&ctl.gave_up, c.polls};
   Ring seg, rr;

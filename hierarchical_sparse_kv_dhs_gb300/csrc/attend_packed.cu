@@ -36,6 +36,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstddef>
 
 #include "attend_core.cuh"
 
@@ -44,8 +45,9 @@ namespace {
 
 constexpr int kChunk = kTile * 128;  // bytes of a ring slot: 128 bytes of each row
 constexpr int kMaxSlots = 12;
-constexpr float kSlack = 4.f;        // log2 units that a weight may pass the reference by
-constexpr float kLift = 11.f;        // log2 of a weight at the reference
+constexpr float kSlack = 6.f;        // log2 units that a weight may pass the reference by
+constexpr float kLift = 9.f;         // log2 of a weight at the reference
+constexpr int kLoadThreads = 128, kRowThreads = 32;
 constexpr int kTmemColumns = 512;
 
 // How a launch's rows are staged.
@@ -55,7 +57,8 @@ struct PackedPlan {
   int32_t units;         // value units of 128 codes: tiles of O^T's M side
   int32_t per_tile;      // ring slots of a tile: keys, wide elements, values unless shared
   int32_t slots;
-  int32_t ahead;         // the next tile's scores are made beside this tile's weights
+  int32_t bufs;          // buffers of scores: 2: the next tile's are made beside this tile's weights
+  int32_t weight_bufs;   // buffers of weights: 2: filled beside the products of the tile before
   int32_t buf_columns;   // tensor memory of one buffer of scores
   int32_t sum_column;    // where the sums begin
   int32_t key8, wide;    // elements of a head
@@ -77,13 +80,30 @@ struct Pieces {
   static constexpr int kSum = kStack ? kP * N : N;  // columns of a unit's sums
   static constexpr int kRow = kSum <= 32 ? 32 : kSum <= 64 ? 64 : 128;  // bytes of a row of weights
   static constexpr int kTileBytes = kTile * kRow;
-  static constexpr int kWeights = (kStack ? 1 : kP) * kTileBytes;
+  static constexpr int kWeights = (kStack ? 1 : kP) * kTileBytes;  // of one buffer
+  // Softmax threads: one for each row and group of columns.
+  static constexpr int kGroups = 2, kSoft = kTile * kGroups;
+  static constexpr int kLoadWarp = kSoft / 32, kKeyWarp = kLoadWarp + kLoadThreads / 32,
+                       kSumWarp = kKeyWarp + 1, kFindWarp = kKeyWarp + 2, kRowWarp = kKeyWarp + 3,
+                       kThreads = 32 * kRowWarp + kRowThreads;
   static constexpr uint32_t kSwizzle = kRow == 32 ? 6 : kRow == 64 ? 4 : 2;
 };
 
 // ------------------------------------------------------------------ PTX
 
-// D += A B (D = A B unless add) of 8-bit operands.
+// The waits of attend_core.cuh with the waiting itself out of line: code that
+// runs every tile is short that way, and stays in the instruction caches.
+__device__ __noinline__ void spin(uint32_t bar, uint32_t parity, const Patience& until) {
+  bar_wait(bar, parity, until);
+}
+__device__ __forceinline__ void await(uint32_t bar, uint32_t parity, const Patience& until) {
+  bar_wait(bar, parity, until);
+  __syncwarp();
+}
+
+// D += A B (D = A B unless add) of 8-bit operands.  A product of M = 128 takes
+// 32 + N/4 cycles in either kind (N 16 to 128, K 16 elements of 16 bits or 32 of
+// 8), whichever operand is transposed.
 __device__ __forceinline__ void mma8(uint32_t d, uint32_t a, uint32_t ahi, uint32_t b, uint32_t bhi,
                                      uint32_t idesc, bool add) {
   asm volatile(
@@ -108,21 +128,32 @@ __device__ __forceinline__ float2 numbers2(uint32_t codes) {
 
 // ------------------------------------------------------------------ kernel
 
+// Where rows lie that location vectors name: tail ring, pages, hot cache, and no
+// rows for the fourth value that the two bits can have.
+struct Tier {
+  const uint8_t* base;
+  uint32_t rows;
+};
+
 struct Control {
-  static constexpr int kRowSlots = 4;  // tiles whose row addresses are found ahead
+  static constexpr int kRowSlots = 3;  // tiles whose row addresses are found ahead
+  // Barriers.  Those of buffers that a warp may be a use behind on come in
+  // pairs, by the tile's number, so that their phases cannot lap each other.
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t qfull[2], qempty, sfull[2], pfull, odone, oempty, rfull[kRowSlots], rempty[kRowSlots], drain;
-  uint64_t segfull[kSegments], segempty[kSegments];
+  uint64_t qfull, sfull[2], sread[2], pfull[2], odone[2], oempty, rfull[kRowSlots], rempty[kRowSlots];
+  uint64_t drain, segfull[kSegments], segempty[kSegments];
   Segment seg[kSegments];  // from the finding warp to the others
+  Tier tier[4];
   const uint8_t* row[kRowSlots][kTile];
+  uint32_t all[kRowSlots];  // none of them is null
+  uint32_t word[2][kTile];  // the row warp's: entries or page slots, and positions in a list
+  int32_t position[2][kTile];
+  float scale[kRowSlots][2][kTile];  // the rows' key and value scales, loaded with the rows
   int64_t out_off[64];
   int32_t lse_at[64];
   int32_t col_lo[64], col_hi[64];
   alignas(16) float m[64], base[64], fac[64];
-  // What a column's coded scores are multiplied by.  Two tables in turn: queries
-  // are loaded up to a segment ahead (never two: the products of a segment wait
-  // for the weights of the one before).
-  alignas(16) float qk[2][64];
+  alignas(16) float qk[2][64];  // what a column's coded scores are multiplied by, by segment
   float part[4][64];
   uint32_t odd[4];    // rows of the tile whose products are taken by hand
   const uint8_t* odd_row;
@@ -130,11 +161,18 @@ struct Control {
   uint32_t tmem;
   volatile uint32_t gave_up;
 };
-constexpr int kBarQfull = 2 * kMaxSlots, kBarPfull = kBarQfull + 5, kBarOempty = kBarQfull + 7,
-              kBarRfull = kBarQfull + 8, kBarRempty = kBarRfull + Control::kRowSlots,
-              kBarDrain = kBarRempty + Control::kRowSlots, kBarSegempty = kBarDrain + 1 + kSegments,
-              kBarriers = kBarSegempty + kSegments;
+enum Bar {  // places in Control's order
+  kBarEmpty = kMaxSlots, kBarQfull = 2 * kMaxSlots, kBarSfull, kBarSread = kBarSfull + 2,
+  kBarPfull = kBarSread + 2, kBarOdone = kBarPfull + 2, kBarOempty = kBarOdone + 2, kBarRfull,
+  kBarRempty = kBarRfull + Control::kRowSlots, kBarDrain = kBarRempty + Control::kRowSlots,
+  kBarSegfull, kBarSegempty = kBarSegfull + kSegments, kBarriers = kBarSegempty + kSegments
+};
+static_assert(offsetof(Control, drain) == 8 * kBarDrain, "barrier table");
 constexpr uint32_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
+static_assert(kControlBytes <= 14336, "32 columns of latent rows just have slots for two tiles");
+
+// A value that all lanes have alike, known as such to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
 
 // A ring position `k` slots further on.
 __device__ __forceinline__ Ring further(Ring r, int k, int n) {
@@ -146,148 +184,174 @@ __device__ __forceinline__ Ring further(Ring r, int k, int n) {
   return r;
 }
 
-// Sixteen or eight 16-bit elements at `p`, zeros if !on.
-__device__ __forceinline__ uint4 eight(const uint8_t* p, bool on, bool aligned) {
-  if (!on) return make_uint4(0, 0, 0, 0);
-  if (aligned) return *reinterpret_cast<const uint4*>(p);
-  const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
-  return make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16,
-                    s[4] | (uint32_t)s[5] << 16, s[6] | (uint32_t)s[7] << 16);
+// Queries of a segment in pieces: coded part [chunk][piece][column][128 B], wide
+// part [column][128 B], zeros past the elements and the columns; sixteen threads
+// have a column.  By the softmax warps, which have nothing else to do then: at
+// the first segment, and later between a segment's last weights and its sums.
+// Elements wait for their column's largest in the pieces' own places, so that
+// what comes after is a short loop: code that runs once a segment is fetched
+// anew each time.
+template <int N, bool F16, int MAXI>
+__device__ __noinline__ void split_queries(const Params<MAXI>& P, uint8_t* sm, Control& ctl,
+                                           const Segment& s, int tid, float* qk) {
+  using S = Pieces<N, F16>;
+  const AttendCommon& c = P.c;
+  const PackedPlan& pl = P.plan;
+  const AttendItem& it = s.it;
+  const bool aligned = !(((uintptr_t)it.q | c.q_qs | c.q_hs) & 15);
+  const int piece = tid & 15;
+#pragma unroll 1
+  for (int col = tid >> 4; col < N; col += S::kSoft / 16) {
+    const bool on = col < s.cols;
+    const int qc = s.col0 + min(col, s.cols - 1);
+    const int qi = it.loc ? s.qbase : qc / c.group;
+    const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
+    const uint8_t* src = it.q + qi * c.q_qs + h * c.q_hs + 16 * piece;
+    uint8_t* const to = sm + pl.off_q + col * 128 + ((piece >> 1 ^ (col & 7)) << 4) + (piece & 1) * 8;
+    uint32_t top = 0;  // the largest magnitude's bits
+    // six groups of eight elements: the chunks' of the coded part, and the wide one
+    uint4 w[6];
+#pragma unroll
+    for (int ch = 0; ch < 6; ++ch) {
+      const int el = (ch < 5 ? ch * 128 : pl.key8) + piece * 8;
+      const bool in = on && (ch < 5 ? el < pl.key8 : piece * 8 < pl.wide);
+      const uint8_t* p = src + 2 * (el - piece * 8);
+      w[ch] = make_uint4(0, 0, 0, 0);
+      if (in && aligned) w[ch] = *reinterpret_cast<const uint4*>(p);
+      if (in && !aligned)
+#pragma unroll 1
+        for (int k = 7; k >= 0; --k)  // shifted in from the end
+          w[ch] = make_uint4(w[ch].x << 16 | reinterpret_cast<const uint16_t*>(p)[k],
+                             w[ch].y << 16 | w[ch].x >> 16, w[ch].z << 16 | w[ch].y >> 16,
+                             w[ch].w << 16 | w[ch].z >> 16);
+    }
+#pragma unroll
+    for (int ch = 0; ch < 5; ++ch) {
+      if (ch >= pl.key_chunks) continue;
+      for (const uint32_t u : {w[ch].x, w[ch].y, w[ch].z, w[ch].w})
+        top = max(top, max(u & 0x7FFFu, u >> 16 & 0x7FFFu));
+      *reinterpret_cast<uint2*>(to + ch * (S::kQ * N * 128)) = make_uint2(w[ch].x, w[ch].y);
+      *reinterpret_cast<uint2*>(to + ch * (S::kQ * N * 128) + N * 128) = make_uint2(w[ch].z, w[ch].w);
+    }
+    if (pl.wide && piece < 8)
+      *reinterpret_cast<uint4*>(sm + pl.off_qw + col * 128 + ((piece ^ (col & 7)) << 4)) = w[5];
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) top = max(top, __shfl_xor_sync(~0u, top, x));
+    // 2^e: the least that brings the largest to 448 = 0.875 * 2^9
+    const bool finite = top < (F16 ? 0x7C00u : 0x7F80u);
+    const float most = F16 ? __half2float(__ushort_as_half((unsigned short)top))
+                           : __uint_as_float(top << 16);
+    const uint32_t bits = __float_as_uint(most);
+    int e = (int)(bits >> 23) - 126 - ((bits & 0x7FFFFFu) <= 0x600000u ? 9 : 8);
+    e = most == 0.f ? 0 : min(max(e, -110), 120);
+    const float down = finite ? __int_as_float((127 - e) << 23) : NAN;
+    if (piece == 0) qk[col] = __int_as_float((127 + e) << 23) * (c.scale * 1.44269504088896341f);
+#pragma unroll 1
+    for (int ch = 0; ch < pl.key_chunks; ++ch) {
+      uint8_t* const at = to + ch * (S::kQ * N * 128);
+      const uint2 x = *reinterpret_cast<const uint2*>(at), y = *reinterpret_cast<const uint2*>(at + N * 128);
+      const uint32_t in[4] = {x.x, x.y, y.x, y.y};
+      uint32_t out[S::kQ][2];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float2 f;
+        if (F16) f = __half22float2(*reinterpret_cast<const __half2*>(&in[k]));
+        else f = make_float2(__uint_as_float(in[k] << 16), __uint_as_float(in[k] & 0xFFFF0000u));
+        f.x *= down;
+        f.y *= down;
+#pragma unroll
+        for (int p = 0; p < S::kQ; ++p) {
+          const uint32_t z = codes2(f.x, f.y);
+          const float2 g = numbers2(z);
+          f.x -= g.x;
+          f.y -= g.y;
+          if (k & 1) out[p][k >> 1] |= z << 16;
+          else out[p][k >> 1] = z;
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < S::kQ; ++p)
+        *reinterpret_cast<uint2*>(at + p * (N * 128)) = make_uint2(out[p][0], out[p][1]);
+    }
+  }
+  fence_async();
+  __syncwarp();
+  if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.qfull));
 }
 
-// Loading warps: queries once per segment, rows tile by tile.
-template <int N, bool F16, int MAXI>
+// Loading warps: rows tile by tile, 128 bytes of each row a slot.  A thread has
+// 16 bytes of every 128 of eight rows.  Copies alone bring 656-byte rows at 7.7
+// TB/s (64 verify blocks' rows, mostly from L2) and 6.2 (a history, from DRAM).
+// A row of an odd number of 16-byte pieces begins inside a 32-byte sector every
+// other time, and its slices then touch one sector more each; copies shifted to
+// sectors move a third fewer, but were slower (7.1 and 5.9 TB/s).
+template <int MAXI>
 __device__ void load_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, int tid) {
-  using S = Pieces<N, F16>;
   const AttendCommon& c = P.c;
   const Patience until{&ctl.gave_up, c.polls};
   const PackedPlan& pl = P.plan;
-  const uint32_t base = smem_u32(sm);
-  Ring ring, rr, seg;
-  uint32_t n_queries = 0;
   const int piece = tid & 7, r0 = tid >> 3;  // rows r0 + 16 i
+  const uint32_t mine = smem_u32(sm) + pl.off_rows + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+  const int nk = pl.key_chunks, nw = pl.wide ? 1 : 0;
+  Ring ring, rr, seg;
 #pragma unroll 1
   for (;;) {
-    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+    await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
     if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
     const int32_t v0 = s.v0, v1 = s.v1;
-    const AttendItem& it = s.it;
-    // Queries: coded part [chunk][piece][column][128 B], wide part [column][128
-    // B], zeros past the elements and the columns.  Eight threads have a column.
-    auto load_queries = [&] {
-      if (n_queries) warp_wait(smem_u32(&ctl.qempty), (n_queries - 1) & 1, until);
-      const bool aligned = !(((uintptr_t)it.q | c.q_qs | c.q_hs) & 15);
-      float* const qk = ctl.qk[n_queries & 1];
-#pragma unroll 1
-      for (int col = r0; col < N; col += kLoadThreads / 8) {
-        const bool on = col < s.cols;
-        const int qc = s.col0 + min(col, s.cols - 1);
-        const int qi = it.loc ? s.qbase : qc / c.group;
-        const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
-        const uint8_t* src = it.q + qi * c.q_qs + h * c.q_hs;
-        constexpr int kChunks = 5;
-        uint4 w[kChunks][2];
-        uint32_t top = 0;  // the largest magnitude's bits
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch)
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const int el = ch * 128 + piece * 16 + z * 8;
-            w[ch][z] = eight(src + 2 * el, on && el < pl.key8, aligned);
-            for (const uint32_t u : {w[ch][z].x, w[ch][z].y, w[ch][z].z, w[ch][z].w})
-              top = max(top, max(u & 0x7FFFu, u >> 16 & 0x7FFFu));
-          }
-        const uint4 wide = eight(src + 2 * (pl.key8 + piece * 8), on && piece * 8 < pl.wide, aligned);
-#pragma unroll
-        for (int x = 1; x < 8; x <<= 1) top = max(top, __shfl_xor_sync(~0u, top, x));
-        // 2^e: the least that brings the largest to 448 = 0.875 * 2^9
-        const bool finite = top < (F16 ? 0x7C00u : 0x7F80u);
-        const float most = F16 ? __half2float(__ushort_as_half((unsigned short)top))
-                               : __uint_as_float(top << 16);
-        const uint32_t bits = __float_as_uint(most);
-        int e = (int)(bits >> 23) - 126 - ((bits & 0x7FFFFFu) <= 0x600000u ? 9 : 8);
-        e = most == 0.f ? 0 : min(max(e, -110), 120);
-        const float down = __int_as_float((127 - e) << 23);
-        if (piece == 0) qk[col] = __int_as_float((127 + e) << 23) * (c.scale * 1.44269504088896341f);
-        uint8_t* const to = sm + pl.off_q + col * 128 + ((piece ^ (col & 7)) << 4);
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          if (ch >= pl.key_chunks) continue;
-          const uint32_t in[8] = {w[ch][0].x, w[ch][0].y, w[ch][0].z, w[ch][0].w,
-                                  w[ch][1].x, w[ch][1].y, w[ch][1].z, w[ch][1].w};
-          uint32_t out[S::kQ][4];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float2 f;
-            if (F16) f = __half22float2(*reinterpret_cast<const __half2*>(&in[k]));
-            else f = make_float2(__uint_as_float(in[k] << 16), __uint_as_float(in[k] & 0xFFFF0000u));
-            f.x = finite ? f.x * down : NAN;
-            f.y = finite ? f.y * down : NAN;
-#pragma unroll
-            for (int p = 0; p < S::kQ; ++p) {
-              const uint32_t z = codes2(f.x, f.y);
-              const float2 y = numbers2(z);
-              f.x -= y.x;
-              f.y -= y.y;
-              if (k & 1) out[p][k >> 1] |= z << 16;
-              else out[p][k >> 1] = z;
-            }
-          }
-#pragma unroll
-          for (int p = 0; p < S::kQ; ++p)
-            *reinterpret_cast<uint4*>(to + (ch * S::kQ + p) * (N * 128)) =
-                make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
-        }
-        if (pl.wide)
-          *reinterpret_cast<uint4*>(sm + pl.off_qw + col * 128 + ((piece ^ (col & 7)) << 4)) = wide;
-      }
-      fence_async();
-      bar_arrive(smem_u32(&ctl.qfull[n_queries & 1]));
-      ++n_queries;
-    };
-
-    const int nk = pl.key_chunks, nw = pl.wide ? 1 : 0;
-    const uint32_t key_at = s.g * pl.key8, wide_at = pl.off_wide + s.g * pl.wide * 2;
-    const uint32_t val_at = pl.off_value + s.g * c.dv;
+    const uint32_t key_at = s.g * pl.key8 + 16 * piece;
+    const uint32_t wide_at = pl.off_wide + s.g * pl.wide * 2 + 16 * piece + 128;  // u is -1 there
+    const uint32_t val_at = pl.off_value + s.g * c.dv + 16 * piece;
+    const uint32_t scale_at = pl.off_scale + 4 * s.g;
 #pragma unroll 1
     for (int tile = v0; tile < v1; ++tile) {
-      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
+      await(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
       const uint8_t* row[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = ctl.row[rr.slot][r0 + 16 * i];
+      const bool all = ctl.all[rr.slot];
+      // the scales arrive with the tile's first slot
+      const uint8_t* const at = ctl.row[rr.slot][tid];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                         smem_u32(&ctl.scale[rr.slot][k][tid])),
+                     "l"(at ? at + scale_at + 4 * k * pl.value_scales : c.tail), "r"(at ? 4 : 0)
+                     : "memory");
       __syncwarp();
       if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
       rr.next(Control::kRowSlots);
+      // slots: 128 bytes of each row of the keys, the wide elements, the values
 #pragma unroll 1
       for (int i = 0; i < pl.per_tile; ++i) {
-        // loaded behind the rows that need no slot of this tile's own
-        if (tile == v0 && i == pl.slots) load_queries();
-        uint32_t at, n;  // the slice of the row that this slot takes
-        if (i < nk) at = key_at + i * 128, n = pl.key8 - i * 128;
-        else if (i < nk + nw) at = wide_at, n = 2 * pl.wide;
-        else at = val_at + (i - nk - nw) * 128, n = c.dv - (i - nk - nw) * 128;
-        warp_wait(smem_u32(&ctl.empty[ring.slot]), ring.phase ^ 1, until);
-        const uint32_t dst = base + pl.off_rows + ring.slot * kChunk;
-        const bool in = (uint32_t)piece * 16 < n;
+        const int u = i < nk ? i : i - nk - nw;
+        const uint32_t from = (i < nk ? key_at : u < 0 ? wide_at : val_at) + u * 128;
+        const int left = u < 0 ? 2 * pl.wide : (i < nk ? pl.key8 : c.dv) - u * 128;
+        await(smem_u32(&ctl.empty[ring.slot]), ring.phase ^ 1, until);
+        const uint32_t dst = mine + ring.slot * kChunk;
+        if (all && left >= 128) {
+          // (a wait that ran out may leave a null beside an old `all`: any row then)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = r0 + 16 * k;
-          const bool on = row[k] && in;
-          const uint8_t* src = on ? row[k] + at + 16 * piece : c.tail;
-          asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(
-                           dst + r * 128 + ((piece ^ (r & 7)) << 4)),
-                       "l"(src), "r"(on ? 16 : 0)
-                       : "memory");
+          for (int k = 0; k < 8; ++k)
+            asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst + k * 2048),
+                         "l"((row[k] ? row[k] : c.tail) + from)
+                         : "memory");
+        } else {  // zeros for rows that are none and past the slice
+          const bool in = piece * 16 < left;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst + k * 2048),
+                         "l"(in && row[k] ? row[k] + from : c.tail), "r"(in && row[k] ? 16 : 0)
+                         : "memory");
         }
         // The slot's barrier gets this thread's arrival when its copies so far
-        // have landed; the issuing warp makes them visible to the tensor cores.
+        // have landed; the issuing warps make them visible to the tensor cores.
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                          smem_u32(&ctl.full[ring.slot]))
                      : "memory");
         ring.next(pl.slots);
       }
-      if (tile == v0 && pl.per_tile <= pl.slots) load_queries();
     }
     __syncwarp();
     if ((tid & 31) == 0) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
@@ -296,119 +360,230 @@ __device__ void load_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, int 
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Issuing warp: all its lanes walk the same path, one of them issues.
+// Row warp: the addresses of every tile's rows, ahead of the loading warps.
+// What a row's address hangs on (its entry, or its page's slot) is asked for a
+// tile ahead, the list position that a union entry hangs on two tiles, by copies
+// into shared memory, so that the four rows of a lane take one short loop.
+template <int MAXI>
+__device__ void place_rows(const Params<MAXI>& P, Control& ctl, int lane) {
+  const AttendCommon& c = P.c;
+  const Patience until{&ctl.gave_up, c.polls};
+  const uint32_t rb = c.row_bytes;
+  const int shift = c.page_shift, in_page = (1 << shift) - 1;
+  const uint32_t words = smem_u32(&ctl.word[0][0]), positions = smem_u32(&ctl.position[0][0]);
+  auto fetch = [&](uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+  };
+  Ring seg, rr;
+#pragma unroll 1
+  for (;;) {
+    await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+    const Segment& s = ctl.seg[seg.slot];
+    if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
+    const AttendItem& it = s.it;
+    const bool located = it.loc != nullptr;
+    // rows [lo, lo + n) of the job (fewer than 2^31: a source's length is)
+    const int32_t lo = (int32_t)s.lo;
+    const uint32_t n = (uint32_t)(s.hi - s.lo);
+    // located: the query's entries, or its positions in a list of `listed`
+    // entries; histories: its first row, and the first one that the ring holds
+    const int64_t entries = located ? (int64_t)s.qbase * it.len : 0;
+    const int32_t* const index = located && it.index ? it.index + entries : nullptr;
+    const uint32_t* const from = located ? it.loc + (index ? 0 : entries)
+                                         : (const uint32_t*)c.map + (size_t)it.pair * c.Pmax;
+    const uint32_t listed = index ? (uint32_t)min((int64_t)it.Q * it.len, (int64_t)INT32_MAX)
+                            : located ? 0x7FFFFFFFu : (uint32_t)it.complete;
+    const int32_t first = (int32_t)it.first, ring = (int32_t)(it.first + it.len) - c.T;
+#pragma unroll 1
+    for (int tile = s.v0 - 2; tile < s.v1; ++tile) {
+      asm volatile("cp.async.wait_all;" ::: "memory");  // asked for a tile ago
+      if (tile >= s.v0) {
+        await(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1, until);
+        bool all = true;
+#pragma unroll 1
+        for (int k = lane; k < kTile; k += 32) {
+          const int32_t i = tile * kTile + k;
+          uint32_t w = ctl.word[tile & 1][k];
+          const uint8_t* p = nullptr;
+          if ((uint32_t)(i - lo) >= n) {
+          } else if (located) {
+            const uint32_t x = w & 0x3FFFFFFFu;
+            const Tier& t = ctl.tier[w >> 30];
+            if (x < t.rows) p = t.base + (size_t)x * rb;
+            else if (w < kEndLoc) atomicOr(c.status, kStatusEloc);
+          } else {
+            const uint32_t r = (uint32_t)(first + i);
+            if ((int32_t)r >= ring) p = c.tail + ((size_t)it.pair * c.T + r % (uint32_t)c.T) * rb;
+            else if ((int32_t)w >= 0) p = c.opt + (((size_t)w << shift) + (r & in_page)) * rb;
+            else p = it.host + (size_t)r * rb;
+          }
+          ctl.row[rr.slot][k] = p;
+          all &= p != nullptr;
+        }
+        all = __all_sync(~0u, all);
+        if (lane == 0) {
+          ctl.all[rr.slot] = all;
+          bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
+        }
+        rr.next(Control::kRowSlots);
+      }
+#pragma unroll 1
+      for (int k = lane; k < kTile; k += 32) {
+        // a position past the list is a location of no tier; a page that is not
+        // complete has no slot
+        const int32_t i = (tile + 1) * kTile + k;
+        const uint32_t x = index ? (uint32_t)ctl.position[tile & 1][k]
+                           : located ? (uint32_t)i : (uint32_t)(first + i) >> shift;
+        const bool on = tile >= s.v0 - 1 && (uint32_t)(i - lo) < n;
+        if (on && x < listed) fetch(words + ((tile + 1 & 1) * kTile + k) * 4, from + x);
+        else ctl.word[tile + 1 & 1][k] = index && (int32_t)x >= 0 ? 3u << 30 : kNoLoc;
+        const int32_t next = i + kTile;
+        if (index && (uint32_t)(next - lo) < n) fetch(positions + ((tile + 1 & 1) * kTile + k) * 4, index + next);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
+    seg.next(kSegments);
+  }
+}
+
+// Two warps issue the products, one those of the scores and one those of the
+// sums: for one alone, waiting for each slot and issuing its four products took
+// longer (260 cycles a slot) than making them (160).  All lanes of a warp walk
+// the same path, one of them issues.
 template <int N, bool F16, int MAXI>
-__device__ void issue_products(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
+__device__ void issue_scores(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
   using S = Pieces<N, F16>;
   const Patience until{&ctl.gave_up, P.c.polls};
   const PackedPlan& pl = P.plan;
-  const uint32_t base = smem_u32(sm);
-  const uint32_t tm_s = ctl.tmem, tm_o = ctl.tmem + pl.sum_column;
-  // float accumulators, operand types (8 bits: 0 e4m3, 1 e5m2; 16 bits: 0 f16,
-  // 1 bf16), N, M = 128; the weights' product takes both operands M/N-major
-  constexpr uint32_t common = 1u << 4 | 8u << 24;
+  const uint32_t base = smem_u32(sm), tm_s = uniform(ctl.tmem);
+  // float accumulators, operand types (8 bits: 0 e4m3; 16 bits: 0 f16, 1 bf16),
+  // N, M = 128
+  constexpr uint32_t common = 1u << 4 | 8u << 24, type = F16 ? 0u : 1u;
   constexpr uint32_t id_key = common | (uint32_t)(S::kQ * N >> 3) << 17;
-  constexpr uint32_t type = F16 ? 0u : 1u;
   constexpr uint32_t id_wide = common | type << 7 | type << 10 | (uint32_t)(N >> 3) << 17;
-  constexpr uint32_t id_sum = common | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(S::kSum >> 3) << 17;
-  constexpr uint32_t hi = operand_hi(1024, 2), hi_p = operand_hi(8 * S::kRow, S::kSwizzle);
+  constexpr uint32_t hi = operand_hi(1024, 2);
   const uint32_t q_lo = operand_lo(base + pl.off_q, 16), qw_lo = operand_lo(base + pl.off_qw, 16);
-  const uint32_t p_lo = operand_lo(base + pl.off_p, 16);
   const uint32_t rows_lo = operand_lo(base + pl.off_rows, 16);
-  const bool lead = elected();
-  const int nk = pl.key_chunks, nw = pl.wide ? 1 : 0, held = pl.shared ? pl.units : 0;
-  Ring qr, seg;  // first slot of the tile whose scores are next
-  uint32_t n_queries = 0, pphase = 0, ophase = 0, n_scores = 0;
-  bool first = true;
+  const bool lead = elected(), two = pl.bufs == 2;
+  const int nk = pl.key_chunks, parts = nk + (pl.wide ? 1 : 0), held = pl.shared ? pl.units : 0;
+  Ring ring, seg;
+  uint32_t n = 0, qphase = 0;
 #pragma unroll 1
   for (;;) {
-    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+    await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
-    const int32_t v0 = s.v0, v1 = s.v1, cols = s.cols;
+    const int32_t v0 = uniform(s.v0), v1 = uniform(s.v1), cols = uniform(s.cols);
     if (__any_sync(~0u, ctl.gave_up) || !cols) break;
     if (lead) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
     seg.next(kSegments);
     if (v0 >= v1) continue;
-    warp_wait(smem_u32(&ctl.qfull[n_queries & 1]), n_queries >> 1 & 1, until);
+    await(smem_u32(&ctl.qfull), qphase, until);
     fence_async();
-    ++n_queries;
-    int next = v0;   // the tile whose scores are next
-    Ring vr = qr;    // first slot of the tile whose sums are next
+    qphase ^= 1;
 #pragma unroll 1
-    for (int tile = v0; tile < v1; ++tile) {
-      const int last = pl.ahead ? min(tile + 1, v1 - 1) : tile;
+    for (int tile = v0; tile < v1; ++tile, ++n) {
+      const uint32_t buf = two ? n & 1 : 0, use = two ? n >> 1 : n, d = tm_s + buf * pl.buf_columns;
+      if (use > 0) await(smem_u32(&ctl.sread[buf]), (use - 1) & 1, until);
+      // Copies land in order: a slot that is full says that those before it are.
+      // Waiting at the second slot and at the last one costs less than at each.
+      // Every slot is 128 bytes wide, zeros past its slice.
 #pragma unroll 1
-      for (; next <= last; ++next) {
-        const uint32_t buf = pl.ahead ? n_scores & 1 : 0, d = tm_s + buf * pl.buf_columns;
-        Ring at = qr;
-#pragma unroll 1
-        for (int i = 0; i < nk + nw; ++i) {
-          warp_wait(smem_u32(&ctl.full[at.slot]), at.phase, until);
-          fence_async();
-          tc_after();
-          if (lead) {
-            const uint32_t a = rows_lo + at.slot * (kChunk >> 4);
-            if (i < nk) {
-              const uint32_t b = q_lo + i * (S::kQ * N * 128 >> 4);
-              const int steps = min(4, (pl.key8 - i * 128 + 31) / 32);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (k < steps) mma8(d, a + 2 * k, hi, b + 2 * k, hi, id_key, i > 0 || k > 0);
-            } else {
-              const int steps = (pl.wide + 15) / 16;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (k < steps) mma(d + S::kQ * N, a + 2 * k, hi, qw_lo + 2 * k, hi, id_wide, k > 0);
-            }
-            if (i >= held) commit(smem_u32(&ctl.empty[at.slot]));
-          }
-          at.next(pl.slots);
-        }
+      for (int i = 0; i < parts; ++i) {
+        await(smem_u32(&ctl.full[ring.slot]), ring.phase, until);
+        fence_async();
+        tc_after();
         if (lead) {
-          commit(smem_u32(&ctl.sfull[buf]));
-          if (next + 1 == v1) commit(smem_u32(&ctl.qempty));
+          const uint32_t a = rows_lo + ring.slot * (kChunk >> 4);
+          if (i < nk) {
+            const uint32_t b = q_lo + i * (S::kQ * N * 128 >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma8(d, a + 2 * k, hi, b + 2 * k, hi, id_key, i > 0 || k > 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma(d + S::kQ * N, a + 2 * k, hi, qw_lo + 2 * k, hi, id_wide, k > 0);
+          }
+          if (i >= held) commit(smem_u32(&ctl.empty[ring.slot]));
+          if (i + 1 == parts) commit(smem_u32(&ctl.sfull[buf]));
         }
-        ++n_scores;
-        qr = further(qr, pl.per_tile, pl.slots);
+        __syncwarp();
+        ring.next(pl.slots);
       }
-      warp_wait(smem_u32(&ctl.pfull), pphase, until);
-      pphase ^= 1;
+      ring = further(ring, pl.per_tile - parts, pl.slots);
+    }
+  }
+  if (lead) commit(smem_u32(&ctl.drain));
+  __syncwarp();
+}
+
+template <int N, bool F16, int MAXI>
+__device__ void issue_sums(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
+  using S = Pieces<N, F16>;
+  const Patience until{&ctl.gave_up, P.c.polls};
+  const PackedPlan& pl = P.plan;
+  const uint32_t base = smem_u32(sm), tm_o = uniform(ctl.tmem) + pl.sum_column;
+  // float accumulators, A e4m3, B e5m2, both M/N-major, N, M = 128
+  constexpr uint32_t id_sum =
+      1u << 4 | 8u << 24 | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(S::kSum >> 3) << 17;
+  constexpr uint32_t hi = operand_hi(1024, 2), hi_p = operand_hi(8 * S::kRow, S::kSwizzle);
+  const uint32_t rows_lo = operand_lo(base + pl.off_rows, 16);
+  const bool lead = elected(), two = pl.weight_bufs == 2;
+  const int before = pl.shared ? 0 : pl.key_chunks + (pl.wide ? 1 : 0);
+  const int after = pl.per_tile - before - pl.units;
+  Ring ring, seg;
+  uint32_t n = 0, ophase = 0;
+  bool first = true;
+#pragma unroll 1
+  for (;;) {
+    await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+    const Segment& s = ctl.seg[seg.slot];
+    const int32_t v0 = uniform(s.v0), v1 = uniform(s.v1), cols = uniform(s.cols);
+    if (__any_sync(~0u, ctl.gave_up) || !cols) break;
+    if (lead) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
+    seg.next(kSegments);
+#pragma unroll 1
+    for (int tile = v0; tile < v1; ++tile, ++n) {
+      const uint32_t p_lo = operand_lo(base + pl.off_p + (two && n & 1 ? S::kWeights : 0), 16);
+      ring = further(ring, before, pl.slots);
+      await(smem_u32(&ctl.pfull[n & 1]), n >> 1 & 1, until);
       if (tile == v0 && !first) {  // the previous segment's sums are read
-        warp_wait(smem_u32(&ctl.oempty), ophase, until);
+        await(smem_u32(&ctl.oempty), ophase, until);
         ophase ^= 1;
       }
+      first = false;
       tc_after();
-      const bool begun = tile > v0 || *(volatile uint32_t*)&ctl.o_begun;
-      Ring at = pl.shared ? vr : further(vr, nk + nw, pl.slots);
+      const bool begun = tile > v0 || uniform(*(volatile uint32_t*)&ctl.o_begun);
+      if (!pl.shared) {
+        const Ring end = further(ring, pl.units - 1, pl.slots);
+        await(smem_u32(&ctl.full[end.slot]), end.phase, until);
+        fence_async();
+        tc_after();
+      }
 #pragma unroll 1
       for (int u = 0; u < pl.units; ++u) {
-        if (!pl.shared) {
-          warp_wait(smem_u32(&ctl.full[at.slot]), at.phase, until);
-          fence_async();
-          tc_after();
-        }
         if (lead) {
-          const uint32_t a = rows_lo + at.slot * (kChunk >> 4), d = tm_o + u * S::kSum;
+          const uint32_t a = rows_lo + ring.slot * (kChunk >> 4), d = tm_o + u * S::kSum;
 #pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
+          for (int p = 0; p < (S::kStack ? 1 : S::kP); ++p)
 #pragma unroll
-            for (int p = 0; p < (S::kStack ? 1 : S::kP); ++p)
-              mma8(d, a + k * (4096 >> 4), hi,
-                   p_lo + (p * S::kTileBytes + k * 32 * S::kRow >> 4), hi_p, id_sum,
-                   begun || k > 0 || p > 0);
-          commit(smem_u32(&ctl.empty[at.slot]));
+            for (int k = 0; k < kTile / 32; ++k)
+              mma8(d, a + k * (4096 >> 4), hi, p_lo + (p * S::kTileBytes + k * 32 * S::kRow >> 4), hi_p,
+                   id_sum, begun || k > 0 || p > 0);
+          commit(smem_u32(&ctl.empty[ring.slot]));
+          if (u + 1 == pl.units) commit(smem_u32(&ctl.odone[n & 1]));
         }
-        at.next(pl.slots);
+        __syncwarp();
+        ring.next(pl.slots);
       }
-      if (lead && (pl.ahead || tile + 1 == v1)) commit(smem_u32(&ctl.odone));
-      vr = further(vr, pl.per_tile, pl.slots);
+      ring = further(ring, after, pl.slots);
     }
-    first = false;
   }
-  // nothing of ours is in flight when tensor memory goes back
+  // nothing of either warp's is in flight when tensor memory goes back
   if (lead) commit(smem_u32(&ctl.drain));
 #pragma unroll 1
-  for (uint32_t n = 0; n < kAttendPolls && !bar_try(smem_u32(&ctl.drain), 0); ++n) {
+  for (uint32_t k = 0; k < kAttendPolls && !bar_try(smem_u32(&ctl.drain), 0); ++k) {
   }
   __syncwarp();
 }
@@ -432,28 +607,32 @@ struct RowScale {
   float inverse;  // 2^-v, 0 without a row
 };
 
-// A row's scores of eight columns in log2 units, value scale included.
-template <int N, bool F16>
-__device__ __forceinline__ void scores8(uint32_t tm, const float* qk, float wide, bool has_wide,
-                                        const RowScale& z, bool row, float (&x)[8]) {
+// A row's scores of B columns in log2 units, value scale included.
+template <int N, bool F16, int B>
+__device__ __forceinline__ void scores(uint32_t tm, const float* qk, float wide, bool has_wide,
+                                       const RowScale& z, bool row, float* x) {
   using S = Pieces<N, F16>;
-  float v[S::kQ + 1][8];
+  float v[(S::kQ + 1) * B];
   __syncwarp();
 #pragma unroll
-  for (int p = 0; p < S::kQ; ++p) tm_load8(tm + p * N, v[p]);
-  if (has_wide) tm_load8(tm + S::kQ * N, v[S::kQ]);
+  for (int p = 0; p < S::kQ + 1; ++p)
+    if (p < S::kQ || has_wide)
 #pragma unroll
-  for (int p = 0; p < S::kQ + 1; ++p) tm_wait(v[p]);
-  const float4 q0 = *reinterpret_cast<const float4*>(qk), q1 = *reinterpret_cast<const float4*>(qk + 4);
-  const float q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+      for (int k = 0; k < B; k += 8) tm_load8(tm + p * N + k, v + p * B + k);
+  tm_wait(v);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float y = v[0][k];
+  for (int k = 0; k < B; k += 4) {
+    const float4 q4 = *reinterpret_cast<const float4*>(qk + k);
+    const float q[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-    for (int p = 1; p < S::kQ; ++p) y += v[p][k];
-    y = fmaf(y * z.key, q[k], z.value);
-    if (has_wide) y = fmaf(v[S::kQ][k], wide, y);
-    x[k] = row ? y : -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      float y = v[k + i];
+#pragma unroll
+      for (int p = 1; p < S::kQ; ++p) y += v[p * B + k + i];
+      y = fmaf(y * z.key, q[i], z.value);
+      if (has_wide) y = fmaf(v[S::kQ * B + k + i], wide, y);
+      x[k + i] = row ? y : -INFINITY;
+    }
   }
 }
 
@@ -467,7 +646,7 @@ __device__ __noinline__ void odd_rows(const Params<MAXI>& P, uint8_t* sm, Contro
                                       bool first, uint32_t tm_scores, const float* qk,
                                       const RowScale& z) {
   using S = Pieces<N, F16>;
-  constexpr int C = N / 2;
+  constexpr int C = N / S::kGroups, kSoftThreads = S::kSoft;
   const AttendCommon& c = P.c;
   const Patience until{&ctl.gave_up, c.polls};
   const PackedPlan& pl = P.plan;
@@ -493,7 +672,7 @@ __device__ __noinline__ void odd_rows(const Params<MAXI>& P, uint8_t* sm, Contro
     if ((r >> 5) == (i >> 5)) {  // the warps that own the row
 #pragma unroll 1
       for (int k = 0; k < C; k += 8) {
-        scores8<N, F16>(tm_scores + k, qk + k0 + k, wide, pl.wide > 0, z, true, v);
+        scores<N, F16, 8>(tm_scores + k, qk + k0 + k, wide, pl.wide > 0, z, true, v);
         if (r == i)
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
@@ -523,7 +702,7 @@ __device__ __noinline__ void odd_rows(const Params<MAXI>& P, uint8_t* sm, Contro
   }
 #pragma unroll 1
   for (int u = 0; u < pl.units; ++u) {
-    warp_wait(smem_u32(&ctl.full[at.slot]), at.phase, until);
+    await(smem_u32(&ctl.full[at.slot]), at.phase, until);
     if (odd && tid < kTile) {
       uint8_t* to = sm + pl.off_rows + at.slot * kChunk + r * 128;
 #pragma unroll 1
@@ -533,224 +712,239 @@ __device__ __noinline__ void odd_rows(const Params<MAXI>& P, uint8_t* sm, Contro
   }
 }
 
-// Softmax warps: a thread has one row of the tile and half of the columns;
-// then the segment's output.
+// Softmax warps: a thread has one row of the tile and some of the columns; then
+// the segment's output.
 template <int N, bool F16, int MAXI>
 __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, int tid, float* parts) {
   using S = Pieces<N, F16>;
-  constexpr int C = N / 2;
+  constexpr int C = N / S::kGroups, kSoftThreads = S::kSoft;
   const AttendCommon& c = P.c;
   const Patience until{&ctl.gave_up, c.polls};
   const PackedPlan& pl = P.plan;
   const int lane = tid & 31, r = tid & (kTile - 1), quarter = r >> 5, k0 = tid / kTile * C;
   const uint32_t tm_s = ctl.tmem + ((uint32_t)(r & ~31) << 16) + k0, tm_o = tm_s + pl.sum_column;
   const float wide = c.scale * 1.44269504088896341f;  // log2 e
-  uint8_t* const weights = sm + pl.off_p + r * S::kRow;
   const bool quads_ok = !(((uintptr_t)c.o_qs | c.o_hs) & 7);  // outputs store four elements at once
   const int turn = S::kRow == 32 ? (r >> 2) & 1 : S::kRow == 64 ? (r >> 1) & 3 : r & 7;
   const int nk = pl.key_chunks, nw = pl.wide ? 1 : 0;
+  const bool two = pl.bufs == 2;
   Ring rr, tr, seg;  // row slots, first ring slot of the tile, segments
-  uint32_t n_scores = 0, ophase = 0, n_queries = 0;
+  uint32_t n = 0, n_queries = 0;  // tiles and segments with tiles so far
   auto larger = [](float a, float b) { return fmaxf(a, b); };
   auto sum = [](float a, float b) { return a + b; };
+  // waits for tile m's sums
+  auto summed = [&](uint32_t m) {
+    await(smem_u32(&ctl.odone[m & 1]), m >> 1 & 1, until);
+    tc_after();
+  };
 #pragma unroll 1
-  for (;;) {
-    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+  for (bool begin = true;; begin = false) {  // first for the queries of the first segment alone
     const Segment& s = ctl.seg[seg.slot];
     const AttendItem& it = s.it;
-    // the previous segment's column tables are read; all leave together
-    if (named_or(1, kSoftThreads, ctl.gave_up) || !s.cols) break;
-    if (tid == 0) ctl.o_begun = 0;
-    if (tid < N) {
-      const bool on = tid < s.cols;
-      const int qc = s.col0 + min(tid, s.cols - 1);
-      const int qi = it.loc ? s.qbase : qc / c.group;
-      const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
-      ctl.out_off[tid] = qi * c.o_qs + h * c.o_hs;
-      ctl.lse_at[tid] = on ? qi * c.heads + h : -1;
-      int64_t lo = 0, hi = it.len;
-      if (!it.loc) query_rows(it, qi, lo, hi);
-      ctl.col_lo[tid] = (int32_t)min(lo, (int64_t)INT32_MAX);
-      ctl.col_hi[tid] = (int32_t)max(hi, (int64_t)INT32_MIN);
-      ctl.m[tid] = -INFINITY;
-      ctl.base[tid] = 0.f;
-    }
-    named_sync(1, kSoftThreads);
-    // rows [all_lo, all_hi) are visible to every column
-    int32_t all_lo = 0, all_hi = INT32_MAX;
-    if (!it.loc) {
-#pragma unroll 1
-      for (int k = 0; k < s.cols; ++k) {
-        all_lo = max(all_lo, ctl.col_lo[k]);
-        all_hi = min(all_hi, ctl.col_hi[k]);
-      }
-    }
     float l[C];
 #pragma unroll
     for (int k = 0; k < C; ++k) l[k] = 0.f;
-    const bool some = s.v0 < s.v1;
-    const float* const qk = ctl.qk[n_queries & 1];
-    const uint32_t scale_at = pl.off_scale + 4 * s.g;
-    // The next tile's row and scales, asked for a tile ahead.
-    const uint8_t* row = nullptr;
-    float ks = 0.f, vs = 1.f;
-    auto find = [&](const uint8_t*& p, float& a, float& b) {
-      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
-      p = ctl.row[rr.slot][r];
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
-      rr.next(Control::kRowSlots);
-      a = p ? __ldg(reinterpret_cast<const float*>(p + scale_at)) : 0.f;
-      b = p ? __ldg(reinterpret_cast<const float*>(p + scale_at) + pl.value_scales) : 1.f;
-    };
-    if (some) {
-      find(row, ks, vs);
-      warp_wait(smem_u32(&ctl.qfull[n_queries & 1]), n_queries >> 1 & 1, until);
-      ++n_queries;
-    }
+    bool some = false;
+    if (!begin) {
+      await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+      // the previous segment's column tables are read; all leave together
+      if (named_or(1, kSoftThreads, ctl.gave_up) || !s.cols) break;
+      if (tid == 0) ctl.o_begun = 0;
+      if (tid < N) {
+        const bool on = tid < s.cols;
+        const int qc = s.col0 + min(tid, s.cols - 1);
+        const int qi = it.loc ? s.qbase : qc / c.group;
+        const int h = s.g * c.group + (it.loc ? qc : qc % c.group);
+        ctl.out_off[tid] = qi * c.o_qs + h * c.o_hs;
+        ctl.lse_at[tid] = on ? qi * c.heads + h : -1;
+        int64_t lo = 0, hi = it.len;
+        if (!it.loc) query_rows(it, qi, lo, hi);
+        ctl.col_lo[tid] = (int32_t)min(lo, (int64_t)INT32_MAX);
+        ctl.col_hi[tid] = (int32_t)max(hi, (int64_t)INT32_MIN);
+        ctl.m[tid] = -INFINITY;
+        ctl.base[tid] = 0.f;
+      }
+      named_sync(1, kSoftThreads);
+      // rows [all_lo, all_hi) are visible to every column
+      int32_t all_lo = 0, all_hi = INT32_MAX;
+      if (!it.loc) {
+#pragma unroll 1
+        for (int k = 0; k < s.cols; ++k) {
+          all_lo = max(all_lo, ctl.col_lo[k]);
+          all_hi = min(all_hi, ctl.col_hi[k]);
+        }
+      }
+      some = s.v0 < s.v1;
+      const float* const qk = ctl.qk[n_queries & 1];
+      if (some) ++n_queries;
 
 #pragma unroll 1
-    for (int tile = s.v0; tile < s.v1; ++tile) {
-      const int32_t j = tile * kTile + r;
-      const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
-      const uint32_t buf = pl.ahead ? n_scores & 1 : 0, tm = tm_s + buf * pl.buf_columns;
-      const uint8_t* next_row = nullptr;
-      float next_ks = 0.f, next_vs = 1.f;
-      if (tile + 1 < s.v1) find(next_row, next_ks, next_vs);
-      const uint32_t vbits = __float_as_uint(vs) >> 23 & 255;
-      const RowScale z{ks, (float)((int)vbits - 127),
-                       row ? __uint_as_float(max(1u, min(253u, 254u - vbits)) << 23) : 0.f};
-      warp_wait(smem_u32(&ctl.sfull[buf]), (pl.ahead ? n_scores >> 1 : n_scores) & 1, until);
-      ++n_scores;
-      tc_after();
-      // The products of the tile before: complete, unless these scores were
-      // made beside its weights.
-      bool pending = pl.ahead && tile > s.v0;
-      auto settle = [&] {
-        if (!pending) return;
-        warp_wait(smem_u32(&ctl.odone), ophase, until);
-        ophase ^= 1;
+      for (int tile = s.v0; tile < s.v1; ++tile, ++n) {
+        const int32_t j = tile * kTile + r;
+        const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
+        const uint32_t buf = two ? n & 1 : 0, tm = tm_s + buf * pl.buf_columns;
+        await(smem_u32(&ctl.sfull[buf]), (two ? n >> 1 : n) & 1, until);
         tc_after();
-        pending = false;
-      };
-      float x[C];  // scores and value scale in log2 units
+        // the row and its scales: there since before its scores were made
+        await(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
+        const uint8_t* const row = ctl.row[rr.slot][r];
+        const float ks = ctl.scale[rr.slot][0][r];
+        const uint32_t vbits = __float_as_uint(ctl.scale[rr.slot][1][r]) >> 23 & 255;
+        const RowScale z{ks, (float)((int)vbits - 127),
+                         row ? __uint_as_float(max(1u, min(253u, 254u - vbits)) << 23) : 0.f};
+        float x[C];  // scores and value scale in log2 units
+        constexpr int kBatch = 8;
 #pragma unroll
-      for (int k = 0; k < C; k += 8) {
-        float y[8];
-        scores8<N, F16>(tm + k, qk + k0 + k, wide, pl.wide > 0, z, row != nullptr, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[k + i] = y[i];
-      }
-      if (ragged) {
-#pragma unroll
-        for (int k = 0; k < C; ++k)
-          if (j < ctl.col_lo[k0 + k] || j >= ctl.col_hi[k0 + k]) x[k] = -INFINITY;
-      }
-      bool move = tile == s.v0;
-      if (!move) {
-        // an unset reference (-inf) gives +inf, or NaN for a score of -inf
-        float over = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < C; k += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&ctl.m[k0 + k]);
-          over = fmaxf(fmaxf(fmaxf(over, x[k] - m.x), x[k + 1] - m.y),
-                       fmaxf(x[k + 2] - m.z, x[k + 3] - m.w));
+        for (int k = 0; k < C; k += kBatch)
+          scores<N, F16, kBatch>(tm + k, qk + k0 + k, wide, pl.wide > 0, z, row != nullptr, x + k);
+        tc_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(smem_u32(&ctl.rempty[rr.slot]));
+          if (!ragged) bar_arrive(smem_u32(&ctl.sread[buf]));
         }
-        move = named_or(1, kSoftThreads, over > kSlack);
-      }
-      if (move) {  // new references: the maxima so far
+        rr.next(Control::kRowSlots);
+        if (ragged) {
+#pragma unroll
+          for (int k = 0; k < C; ++k)
+            if (j < ctl.col_lo[k0 + k] || j >= ctl.col_hi[k0 + k]) x[k] = -INFINITY;
+        }
+        bool move = tile == s.v0;
+        if (!move) {
+          // an unset reference (-inf) gives +inf, or NaN for a score of -inf
+          float over = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < C; k += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&ctl.m[k0 + k]);
+            over = fmaxf(fmaxf(fmaxf(over, x[k] - m.x), x[k + 1] - m.y),
+                         fmaxf(x[k + 2] - m.z, x[k + 3] - m.w));
+          }
+          move = named_or(1, kSoftThreads, over > kSlack);
+        }
+        if (n >= (uint32_t)pl.weight_bufs) summed(n - pl.weight_bufs);
+        uint8_t* const weights = sm + pl.off_p + r * S::kRow +
+                                 (pl.weight_bufs == 2 && n & 1 ? S::kWeights : 0);
+        bool odd = false;
+        if (move) {  // new references: the maxima so far
+#pragma unroll
+          for (int k = 0; k < C; k += 8) {
+            const float y = fold8(x + k, lane, larger);
+            if (lane < 8) ctl.part[quarter][k0 + k + lane] = y;
+          }
+          named_sync(1, kSoftThreads);
+          if (tid < N) {
+            const float old = ctl.m[tid];
+            const float m = fmaxf(fmaxf(fmaxf(ctl.part[0][tid], ctl.part[1][tid]),
+                                        fmaxf(ctl.part[2][tid], ctl.part[3][tid])), old);
+            ctl.fac[tid] = old == -INFINITY ? 0.f : exp2_fast(old - m);
+            ctl.m[tid] = m;
+            ctl.base[tid] = m == -INFINITY ? 0.f : m - kLift;
+          }
+          named_sync(1, kSoftThreads);
+          if (tile > s.v0) {
+            summed(n - 1);
+#pragma unroll
+            for (int k = 0; k < C; k += 8) {
+              float f[8];
+              bool same = true;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                f[i] = ctl.fac[k0 + k + i];
+                l[k + i] *= f[i];
+                same &= f[i] == 1.f;
+              }
+              if (same) continue;  // as for all lanes of the warp
+#pragma unroll 1
+              for (int u = 0; u < pl.units; ++u) {
+                constexpr int kSums = S::kSum / N;
+                float v[8 * kSums];
+                __syncwarp();
+#pragma unroll
+                for (int p = 0; p < kSums; ++p) tm_load8(tm_o + u * S::kSum + p * N + k, v + 8 * p);
+                tm_wait(v);
+#pragma unroll
+                for (int p = 0; p < kSums; ++p) {
+                  float y[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) y[i] = v[8 * p + i] * f[i];
+                  tm_store(tm_o + u * S::kSum + p * N + k, y);
+                }
+              }
+            }
+          }
+        }
+        // A row that only some of the columns see would reach the others too
+        // if its value is not finite (0 x NaN): such rows leave the tile, and
+        // their products are added by hand to the columns that see them.
+        if (ragged) {
+          const uint8_t* value = row + (pl.shared ? s.g * pl.key8 : pl.off_value + s.g * c.dv);
+          if (row && (j < all_lo || j >= all_hi)) odd = !finite_codes(value, c.dv);
+          if (named_or(1, kSoftThreads, odd)) {
+            if (tile > s.v0) summed(n - 1);
+            odd_rows<N, F16>(P, sm, ctl, tid, odd, value,
+                             pl.shared ? tr : further(tr, nk + nw, pl.slots), tile * kTile,
+                             tile == s.v0, tm, qk, z);
+          }
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_u32(&ctl.sread[buf]));
+        }
+        // weights in pieces, in the swizzled layout
 #pragma unroll
         for (int k = 0; k < C; k += 8) {
-          const float y = fold8(x + k, lane, larger);
-          if (lane < 8) ctl.part[quarter][k0 + k + lane] = y;
-        }
-        named_sync(1, kSoftThreads);
-        if (tid < N) {
-          const float old = ctl.m[tid];
-          const float m = fmaxf(fmaxf(fmaxf(ctl.part[0][tid], ctl.part[1][tid]),
-                                      fmaxf(ctl.part[2][tid], ctl.part[3][tid])), old);
-          ctl.fac[tid] = old == -INFINITY ? 0.f : exp2_fast(old - m);
-          ctl.m[tid] = m;
-          ctl.base[tid] = m == -INFINITY ? 0.f : m - kLift;
-        }
-        named_sync(1, kSoftThreads);
-        if (tile > s.v0) {
+          const float4 b0 = *reinterpret_cast<const float4*>(&ctl.base[k0 + k]);
+          const float4 b1 = *reinterpret_cast<const float4*>(&ctl.base[k0 + k + 4]);
+          const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+          uint32_t w[S::kP][2];
 #pragma unroll
-          for (int k = 0; k < C; ++k) l[k] *= ctl.fac[k0 + k];
-          settle();
-#pragma unroll 1
-          for (int u = 0; u < pl.units * (S::kSum / N); ++u)
-#pragma unroll 1
-            for (int k = 0; k < C; k += 8) {
-              float v[8];
-              tm_load(tm_o + u * N + k, v);
+          for (int i = 0; i < 8; i += 4) {
+            __half2 h[2];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] *= ctl.fac[k0 + k + i];
-              tm_store(tm_o + u * N + k, v);
+            for (int q = 0; q < 2; ++q) {
+              const float p0 = exp2_fast(x[k + i + 2 * q] - b[i + 2 * q]);
+              const float p1 = exp2_fast(x[k + i + 2 * q + 1] - b[i + 2 * q + 1]);
+              l[k + i + 2 * q] = fmaf(p0, z.inverse, l[k + i + 2 * q]);
+              l[k + i + 2 * q + 1] = fmaf(p1, z.inverse, l[k + i + 2 * q + 1]);
+              h[q] = __floats2half2_rn(p0, p1);
             }
-        }
-      }
-      // A row that only some of the columns see would reach the others too
-      // if its value is not finite (0 x NaN): such rows leave the tile, and
-      // their products are added by hand to the columns that see them.
-      bool odd = false;
-      if (ragged) {
-        const uint8_t* value = row + (pl.shared ? s.g * pl.key8 : pl.off_value + s.g * c.dv);
-        if (row && (j < all_lo || j >= all_hi)) odd = !finite_codes(value, c.dv);
-        if (named_or(1, kSoftThreads, odd)) {
-          settle();
-          odd_rows<N, F16>(P, sm, ctl, tid, odd, value,
-                           pl.shared ? tr : further(tr, nk + nw, pl.slots), tile * kTile,
-                           tile == s.v0, tm, qk, z);
-        }
-      }
-      tr = further(tr, pl.per_tile, pl.slots);
-      // weights in pieces, in the swizzled layout
-      settle();
 #pragma unroll
-      for (int k = 0; k < C; k += 8) {
-        const float4 b0 = *reinterpret_cast<const float4*>(&ctl.base[k0 + k]);
-        const float4 b1 = *reinterpret_cast<const float4*>(&ctl.base[k0 + k + 4]);
-        const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-        uint32_t w[S::kP][2];
+            for (int p = 0; p < S::kP; ++p) {
+              uint32_t u[2];
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          __half2 h[2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = exp2_fast(x[k + i + 2 * n] - b[i + 2 * n]);
-            const float p1 = exp2_fast(x[k + i + 2 * n + 1] - b[i + 2 * n + 1]);
-            l[k + i + 2 * n] = fmaf(p0, z.inverse, l[k + i + 2 * n]);
-            l[k + i + 2 * n + 1] = fmaf(p1, z.inverse, l[k + i + 2 * n + 1]);
-            h[n] = __floats2half2_rn(p0, p1);
+              for (int q = 0; q < 2; ++q) {
+                // the upper byte of each number, rounded to nearest, and the rest
+                u[q] = (*reinterpret_cast<uint32_t*>(&h[q]) + 0x00800080u) & 0xFF00FF00u;
+                h[q] = __hsub2(h[q], *reinterpret_cast<__half2*>(&u[q]));
+              }
+              w[p][i / 4] = odd ? 0 : __byte_perm(u[0], u[1], 0x7531);
+            }
           }
 #pragma unroll
           for (int p = 0; p < S::kP; ++p) {
-            uint32_t u[2];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              // the upper byte of each number, rounded to nearest, and the rest
-              u[n] = (*reinterpret_cast<uint32_t*>(&h[n]) + 0x00800080u) & 0xFF00FF00u;
-              h[n] = __hsub2(h[n], *reinterpret_cast<__half2*>(&u[n]));
-            }
-            w[p][i / 4] = odd ? 0 : __byte_perm(u[0], u[1], 0x7531);
+            const int at = (S::kStack ? p * N : 0) + k0 + k;
+            *reinterpret_cast<uint2*>(weights + (S::kStack ? 0 : p * S::kTileBytes) +
+                                      ((at >> 4 ^ turn) << 4) + (at & 8)) = make_uint2(w[p][0], w[p][1]);
           }
         }
-#pragma unroll
-        for (int p = 0; p < S::kP; ++p) {
-          const int at = (S::kStack ? p * N : 0) + k0 + k;
-          *reinterpret_cast<uint2*>(weights + (S::kStack ? 0 : p * S::kTileBytes) +
-                                    ((at >> 4 ^ turn) << 4) + (at & 8)) = make_uint2(w[p][0], w[p][1]);
-        }
+        tr = further(tr, pl.per_tile, pl.slots);
+        fence_async();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_u32(&ctl.pfull[n & 1]));
       }
-      fence_async();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_u32(&ctl.pfull));
-      row = next_row;
-      ks = next_ks;
-      vs = next_vs;
     }
+
+    // the next segment's queries: its scores can be made beside this one's sums
+    // and outputs (the queries here are done with: so are their scores)
+    {
+      Ring next = seg;
+      if (!begin) next.next(kSegments);
+      await(smem_u32(&ctl.segfull[next.slot]), next.phase, until);
+      const Segment& t = ctl.seg[next.slot];
+      const bool split = !ctl.gave_up && t.cols && t.v0 < t.v1;
+      if (__all_sync(~0u, split)) split_queries<N, F16>(P, sm, ctl, t, tid, ctl.qk[n_queries & 1]);
+    }
+    if (begin) continue;
 
     named_sync(1, kSoftThreads);
 #pragma unroll
@@ -781,11 +975,7 @@ __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, i
       }
     }
     named_sync(1, kSoftThreads);
-    if (some) {
-      warp_wait(smem_u32(&ctl.odone), ophase, until);
-      ophase ^= 1;
-      tc_after();
-    }
+    if (some) summed(n - 1);
     const bool quads = quads_ok && !((uintptr_t)it.out & 7);
 #pragma unroll 1
     for (int u = 0; u < pl.units; ++u) {
@@ -795,13 +985,17 @@ __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, i
       for (int k = 0; k < C; k += 8) {
         float v[8] = {};
         if (some) {
-          tm_load(tm_o + u * S::kSum + k, v);
+          constexpr int kSums = S::kSum / N;
+          float y[8 * kSums];
+          __syncwarp();
 #pragma unroll
-          for (int p = 1; p < (S::kStack ? S::kP : 1); ++p) {
-            float y[8];
-            tm_load(tm_o + u * S::kSum + p * N + k, y);
+          for (int p = 0; p < kSums; ++p) tm_load8(tm_o + u * S::kSum + p * N + k, y + 8 * p);
+          tm_wait(y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += y[i];
+          for (int i = 0; i < 8; ++i) {
+            v[i] = y[i];
+#pragma unroll
+            for (int p = 1; p < kSums; ++p) v[i] += y[8 * p + i];
           }
         }
 #pragma unroll
@@ -858,27 +1052,33 @@ __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, i
 }
 
 template <int N, bool F16, int MAXI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Pieces<N, F16>::kThreads, 1)
     attend_packed_kernel(const __grid_constant__ Params<MAXI> P, float* parts) {
+  using S = Pieces<N, F16>;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   Control& ctl = *reinterpret_cast<Control*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
-  for (int k = tid; k < Control::kRowSlots * kTile; k += kThreads) (&ctl.row[0][0])[k] = nullptr;
-  if (warp == kIssueWarp) {
+  for (int k = tid; k < Control::kRowSlots * kTile; k += S::kThreads) (&ctl.row[0][0])[k] = nullptr;
+  if (tid < Control::kRowSlots) ctl.all[tid] = 0;
+  if (warp == S::kRowWarp && (tid & 31) < 4) {
+    const int k = tid & 3;
+    const AttendCommon& c = P.c;
+    ctl.tier[k] = {k == kTierTail ? c.tail : k == kTierOpt ? c.opt : c.hot,
+                   k == kTierTail ? c.tail_rows : k == kTierOpt ? c.opt_rows : k == kTierHot ? c.hot_rows : 0};
+  }
+  if (warp == S::kKeyWarp) {
 #pragma unroll
     for (int k = 0; k < kBarriers; k += 32) {
       const int i = k + (tid & 31);
-      const bool full = i < kMaxSlots || i == kBarQfull || i == kBarQfull + 1;
-      const bool soft = i == kBarPfull || i == kBarOempty;
-      const bool rows = i >= kBarRfull && i < kBarRempty;
-      const bool read = i >= kBarRempty && i < kBarDrain;
-      const bool segs = i >= kBarSegempty;
+      const bool soft = i == kBarQfull || (i >= kBarSread && i < kBarOdone) || i == kBarOempty;
+      const bool rows = i >= kBarRfull && i < kBarRempty, read = i >= kBarRempty && i < kBarDrain;
       if (i < kBarriers)
         bar_init(smem_u32(&ctl.full[0]) + 8 * i,
-                 full ? kLoadThreads : soft ? kSoftThreads / 32 : rows ? kRowThreads / 32
-                 : read ? (kSoftThreads + kLoadThreads) / 32 : segs ? kThreads / 32 - 1 : 1);
+                 i < kBarEmpty ? kLoadThreads : soft ? S::kSoft / 32 : rows ? kRowThreads / 32
+                 : read ? (S::kSoft + kLoadThreads) / 32 : i == kBarDrain ? 2
+                 : i >= kBarSegempty ? S::kThreads / 32 - 1 : 1);
     }
     ctl.gave_up = P.c.polls == 0;  // nothing is waited for then
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -889,22 +1089,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == kFindWarp) {
+  if (warp == S::kFindWarp) {
     find_segments(P, ctl);  // meets the others' barrier inside
   } else {
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp < kSoftThreads / 32) softmax_rows<N, F16>(P, sm, ctl, tid, parts);
-    else if (warp < kIssueWarp) load_rows<N, F16>(P, sm, ctl, tid - kSoftThreads);
-    else if (warp == kIssueWarp) issue_products<N, F16>(P, sm, ctl);
-    else find_rows(P, ctl, tid - 32 * kRowWarp);
+    if (warp < S::kLoadWarp) softmax_rows<N, F16>(P, sm, ctl, tid, parts);
+    else if (warp < S::kKeyWarp) load_rows(P, sm, ctl, tid - S::kSoft);
+    else if (warp == S::kKeyWarp) issue_scores<N, F16>(P, sm, ctl);
+    else if (warp == S::kSumWarp) issue_sums<N, F16>(P, sm, ctl);
+    else place_rows(P, ctl, tid - 32 * S::kRowWarp);
   }
   __syncwarp();
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == kIssueWarp)
+  if (warp == S::kKeyWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl.tmem),
                  "r"(kTmemColumns)
                  : "memory");
@@ -931,25 +1132,33 @@ PackedPlan plan_n(const AttendCommon& c, const PackedLayout& l) {
   p.off_q = kControlBytes;
   p.off_qw = p.off_q + (uint32_t)p.key_chunks * S::kQ * N * 128;
   p.off_p = p.off_qw + (uint32_t)nw * N * 128;
-  p.off_rows = p.off_p + S::kWeights;
-  const uint32_t room = kSmemLimit - 1024 > p.off_rows ? kSmemLimit - 1024 - p.off_rows : 0;
-  p.slots = std::min<int>(kMaxSlots, room / kChunk);
-  p.smem = 1024 + p.off_rows + (uint32_t)p.slots * kChunk;
   p.buf_columns = (S::kQ + nw) * N;
   const int sums = p.units * S::kSum;
+  auto slots = [&](int weight_bufs) {
+    const uint32_t used = 1024 + p.off_p + (uint32_t)weight_bufs * S::kWeights;
+    return used < kSmemLimit ? std::min<int>(kMaxSlots, (kSmemLimit - used) / kChunk) : 0;
+  };
   // The next tile's keys need slots of their own while this tile holds its
   // values: slots are taken in order, so that the ring has to reach from the
-  // first value (shared rows: the first slot) of a tile to the next one's last key.
-  p.ahead = 2 * p.buf_columns + sums <= kTmemColumns &&
-            p.slots >= (l.shared ? 2 : 1) * p.per_tile;
-  p.sum_column = (p.ahead ? 2 : 1) * p.buf_columns;
+  // first value (shared rows: the first slot) of a tile to the next one's last
+  // key.  A second buffer of weights may cost slots beyond that.
+  const int two = (l.shared ? 2 : 1) * p.per_tile;
+  p.weight_bufs = slots(2) >= two ? 2 : 1;
+  p.slots = slots(p.weight_bufs);
+  p.bufs = 2 * p.buf_columns + sums <= kTmemColumns && p.slots >= two ? 2 : 1;
+  p.sum_column = p.bufs * p.buf_columns;
+  p.off_rows = p.off_p + (uint32_t)p.weight_bufs * S::kWeights;
+  p.smem = 1024 + p.off_rows + (uint32_t)p.slots * kChunk;
   return p;
 }
 
-// Slots without which a tile cannot be worked on: shared rows stay until their
-// sums are made.
+// Shared rows stay until their sums are made: without slots for two tiles,
+// loads, scores, weights and sums would follow each other (128 heads in blocks of
+// 64 columns 209 us, of 32 178).  Others need those of a tile's scores, or of its
+// sums, at once.
 bool plan_fits(const PackedPlan& p) {
-  return p.slots >= (p.shared ? p.per_tile : std::min(p.per_tile, 2));
+  const int values = p.shared ? 0 : p.units;
+  return p.slots >= (p.shared ? 2 * p.per_tile : std::max(p.per_tile - values, values));
 }
 
 PackedPlan make_plan(const AttendCommon& c, const PackedLayout& l, int n) {
@@ -988,7 +1197,7 @@ template <int N, bool F16, int MAXI>
 cudaError_t launch_kernel(const Params<MAXI>& P, const Shape& s, float* parts, cudaStream_t stream) {
   cudaError_t e = use_all_smem<N, F16, MAXI>();
   if (e != cudaSuccess) return e;
-  attend_packed_kernel<N, F16><<<s.blocks, kThreads, P.plan.smem, stream>>>(P, parts);
+  attend_packed_kernel<N, F16><<<s.blocks, Pieces<N, F16>::kThreads, P.plan.smem, stream>>>(P, parts);
   e = cudaGetLastError();
   if (e != cudaSuccess || !s.n_cut) return e;
   return launch_merge(P.c, s, parts, stream);

@@ -6,8 +6,9 @@ and scales where a tiled, split kernel can go wrong.
 Bounds, from the number formats alone.  With weights w_j summing to 1, values
 y_j = 2^v_j d_j and A = sum w_j |y_j|:
   - weights: bf16 three e5m2 pieces of a number rounded to f16, 2^-9 + 2^-11 of
-    each; f16 2^-11; each at least to 2^-28 of the largest 2^v_j w_j, which
-    multiplies a code: F = 2^-28 max_j(2^v_j w_j) sum_j |d_j|;
+    each; f16 2^-11; each at least to half of e5m2's smallest number, 2^-17,
+    where the largest 2^v_j w_j is at least 2^9 (the reference's height):
+    multiplied by a code F = 2^-26 max_j(2^v_j w_j) sum_j |d_j|;
   - queries: to 2^-18 of the largest coded element, a score by at most
     q = 2^-18 max|a| scale sum_e |key_je|;
   - scores: float accumulation of key elements in steps of at least 16, with the
@@ -70,7 +71,7 @@ def reference(lay, q, rows, keep):
             top = qg[:, :lay.key8].abs().amax(1, keepdim=True)
             d = d + 2.0 ** -18 * top * lay.scale * x[:, :lay.key8].abs().sum(1).amax()
             vs = scales[:, g if lay.shared else lay.kv + g].double()
-            floor = 2.0 ** -28 * (w * vs).amax(1, keepdim=True) * (y / vs[:, None]).abs().sum(0)
+            floor = 2.0 ** -26 * (w * vs).amax(1, keepdim=True) * (y / vs[:, None]).abs().sum(0)
             a = w @ y.abs()
             tol[i, hs] = (1.02 * W[lay.dtype] + 2 * d + 2.0 ** -23 * (n / 32 + 8)) * a + \
                 1.02 * u * out[i, hs].abs() + floor + 2.0 ** -25
