@@ -385,7 +385,6 @@ struct PackCommon {
   Rotation r;
   uint8_t* tail;
   int32_t T, n_items;
-  int64_t tokens;                          // of all items
   int64_t k_ts, k_hs, w_ts, w_hs, v_ts, v_hs;  // bytes
 };
 cudaError_t launch_pack(const PackCommon& c, const PackItem* items, int n_items, int sms,
@@ -411,7 +410,6 @@ struct UnpackCommon {
   uint32_t tail_rows, opt_rows, hot_rows;
   int32_t T, Pmax, page_shift, n_items;
   uint32_t* status;
-  int64_t count;                           // of all items
   int64_t k_rs, k_hs, v_rs, v_hs;          // bytes
 };
 cudaError_t launch_unpack(const UnpackCommon& c, const UnpackItem* items, int n_items, int sms,

@@ -15,8 +15,7 @@
 // element too, which another lane of the group reads at the same time: an L1
 // hit).  Two roundings in all: to a code, and nothing else.
 //
-// Reading back.  A warp has four rows, whose addresses it finds at once; a lane
-// takes 16 codes (or 8 wide elements) at a time.
+// Reading back.  Eight to 32 lanes have a row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -49,18 +48,15 @@ __device__ __forceinline__ uint32_t narrow2(float a, float b) {
 }
 
 // Eight 16-bit elements at `p`, 16-byte aligned or not.
+__device__ __forceinline__ uint4 raw8(const uint8_t* p, bool aligned) {
+  if (aligned) return __ldg(reinterpret_cast<const uint4*>(p));
+  const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
+  return make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16,
+                    s[4] | (uint32_t)s[5] << 16, s[6] | (uint32_t)s[7] << 16);
+}
+
 template <bool F16>
-__device__ __forceinline__ void load8(const uint8_t* p, bool aligned, float (&v)[8]) {
-  uint4 w;
-  if (aligned) {
-    w = __ldg(reinterpret_cast<const uint4*>(p));
-  } else {
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
-    w.x = s[0] | (uint32_t)s[1] << 16;
-    w.y = s[2] | (uint32_t)s[3] << 16;
-    w.z = s[4] | (uint32_t)s[5] << 16;
-    w.w = s[6] | (uint32_t)s[7] << 16;
-  }
+__device__ __forceinline__ void floats8(const uint4& w, float (&v)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -70,18 +66,34 @@ __device__ __forceinline__ void load8(const uint8_t* p, bool aligned, float (&v)
   }
 }
 
-template <bool F16>
-__device__ __forceinline__ void store8(uint8_t* p, bool aligned, const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = narrow2<F16>(v[2 * k], v[2 * k + 1]);
+__device__ __forceinline__ void put8(uint8_t* p, bool aligned, const uint4& w) {
   if (aligned) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p) = w;
   } else {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
     uint16_t* s = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+    for (int k = 0; k < 8; ++k) s[k] = (uint16_t)(u[k >> 1] >> (16 * (k & 1)));
   }
+}
+
+template <bool F16>
+__device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
+  return make_uint4(narrow2<F16>(v[0], v[1]), narrow2<F16>(v[2], v[3]), narrow2<F16>(v[4], v[5]),
+                    narrow2<F16>(v[6], v[7]));
+}
+
+// n / d for n < 2^31, by one product: where a thread finds its place by division,
+// that costs more than what it then does.
+struct Div {
+  uint32_t mul, shift, d;
+  __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+Div div_by(uint32_t d) {
+  Div x{0, 0, d};
+  while ((1u << x.shift) < d) ++x.shift;
+  x.mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << x.shift) - d)) / d + 1);
+  return x;
 }
 
 __device__ __forceinline__ uint16_t codes2(float a, float b) {
@@ -121,87 +133,121 @@ __device__ __forceinline__ float2 sine_of(uint64_t turns, int32_t position, cons
   return make_float2(cosine * r.amplitude, sine * (r.amplitude * r.sign));
 }
 
-// The group of eight elements that begins at rotary element j, turned; `other`
-// has the eight partners of half pairs.
-__device__ __forceinline__ void turn8(float (&v)[8], const float (&other)[8], int j,
-                                      const Rotation& r, const float2* sines) {
-  if (r.interleaved) {
+// Sines lie so that the threads of a warp, which have neighbouring groups of eight
+// elements, read neighbouring 16 bytes: a group's (half pairs: of its lower half)
+// pairs two by two, the first two of all groups, the next two, and so on.
+struct SineTable {
+  int half, groups, shift;  // pairs, groups of them, log2 of pairs in a group
+  __device__ __forceinline__ SineTable(const Rotation& r) {
+    half = r.rotary / 2;
+    shift = r.interleaved ? 2 : 3;
+    groups = half >> shift;
+  }
+  __device__ __forceinline__ int place(int pair) const {
+    const int k = (pair >> 1) & ((1 << (shift - 1)) - 1);
+    return 2 * (k * groups + (pair >> shift)) + (pair & 1);
+  }
+};
+
+// Four pairs (a, b) next to each other; their sines begin at s.
+__device__ __forceinline__ void turn_pairs(float (&v)[8], const float4* s, int groups) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 s = sines[j / 2 + k];
-      const float a = v[2 * k], b = v[2 * k + 1];
-      v[2 * k] = a * s.x - b * s.y;
-      v[2 * k + 1] = b * s.x + a * s.y;
-    }
-  } else {
-    const int half = r.rotary / 2;
-    const bool up = j >= half;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 s = sines[(up ? j - half : j) + k];
-      v[k] = up ? v[k] * s.x + other[k] * s.y : v[k] * s.x - other[k] * s.y;
-    }
+  for (int k = 0; k < 2; ++k) {
+    const float4 z = s[k * groups];
+    const float a = v[4 * k], b = v[4 * k + 1], c = v[4 * k + 2], d = v[4 * k + 3];
+    v[4 * k] = a * z.x - b * z.y;
+    v[4 * k + 1] = b * z.x + a * z.y;
+    v[4 * k + 2] = c * z.z - d * z.w;
+    v[4 * k + 3] = d * z.z + c * z.w;
   }
 }
 
+// Eight elements whose partners are `u`: the lower ones of their pairs, or
+// (sign -1) the upper ones.
+__device__ __forceinline__ void turn_half(float (&v)[8], const float (&u)[8], float sign,
+                                          const float4* s, int groups) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 z = s[k * groups];
+    v[2 * k] = v[2 * k] * z.x - sign * u[2 * k] * z.y;
+    v[2 * k + 1] = v[2 * k + 1] * z.z - sign * u[2 * k + 1] * z.w;
+  }
+}
+
+struct RotateGrid {
+  Div groups, heads, half;
+  int32_t tokens_each;
+};
+
 // Rotates or copies groups of eight elements; a thread that has the lower half
-// of eight half pairs writes both halves.  Bound by memory: what it reads and
-// writes once.
+// of eight half pairs writes both halves.  Its first group is asked for ahead of
+// the sines.
 template <bool F16>
 __global__ void __launch_bounds__(kThreads)
-    rotate_kernel(const __grid_constant__ RotateParams P, int tokens_each) {
-  __shared__ float2 sines[kSinesMax];
+    rotate_kernel(const __grid_constant__ RotateParams P, const __grid_constant__ RotateGrid G) {
+  __shared__ alignas(16) float2 sines[kSinesMax];
   const Rotation& r = P.r;
-  const int half = r.rotary / 2;
-  const int64_t t0 = (int64_t)blockIdx.x * tokens_each;
-  const int n = (int)min((int64_t)tokens_each, P.tokens - t0);
-  for (int k = threadIdx.x; k < n * half; k += kThreads) {
-    const int t = k / half;
-    sines[k] = sine_of(__ldg(r.turns + (k - t * half)), __ldg(P.position + t0 + t), r);
-  }
-  __syncthreads();
-  const bool in_place = P.x == P.y;
+  const SineTable table(r);
+  const int half = table.half;
+  const int64_t t0 = (int64_t)blockIdx.x * G.tokens_each;
+  const int n = (int)min((int64_t)G.tokens_each, P.tokens - t0);
   const bool aligned_x = !(((uintptr_t)P.x | P.x_ts | P.x_hs) & 15);
   const bool aligned_y = !(((uintptr_t)P.y | P.y_ts | P.y_hs) & 15);
+  const uint8_t* const x0 = P.x + t0 * P.x_ts;
+  uint8_t* const y0 = P.y + t0 * P.y_ts;
   // of a head: groups that turn (half pairs: two groups each), then the rest
   const int turning = (r.interleaved ? r.rotary : half) / 8;
-  const int groups = turning + (in_place ? 0 : (P.elems - r.rotary) / 8);
-  const int all = n * P.heads * groups;
-#pragma unroll 2
+  const int all = n * P.heads * (int)G.groups.d;
+  uint4 a, b;
+  int t, g, h;
+  auto element = [&] {
+    if (g < turning) return r.offset + g * 8;
+    const int el = (g - turning) * 8;
+    return el >= r.offset ? el + r.rotary : el;
+  };
+  auto ask = [&](int k) {
+    const int th = G.groups.of(k);
+    t = G.heads.of(th);
+    h = th - t * P.heads;
+    g = k - th * (int)G.groups.d;
+    const uint8_t* x = x0 + t * P.x_ts + h * P.x_hs + 2 * element();
+    a = raw8(x, aligned_x);
+    if (!r.interleaved && g < turning) b = raw8(x + 2 * half, aligned_x);
+  };
+  if ((int)threadIdx.x < all) ask(threadIdx.x);
+  for (int k = threadIdx.x; k < n * half; k += kThreads) {
+    const int i = G.half.of(k);
+    sines[i * half + table.place(k - i * half)] =
+        sine_of(__ldg(r.turns + (k - i * half)), __ldg(P.position + t0 + i), r);
+  }
+  __syncthreads();
+#pragma unroll 1
   for (int k = threadIdx.x; k < all; k += kThreads) {
-    const int th = k / groups, g = k - th * groups;
-    const int t = th / P.heads, h = th - t * P.heads;
-    const uint8_t* x = P.x + (t0 + t) * P.x_ts + h * P.x_hs;
-    uint8_t* y = P.y + (t0 + t) * P.y_ts + h * P.y_hs;
-    float v[8];
-    if (g >= turning) {
-      int el = (g - turning) * 8;
-      if (el >= r.offset) el += r.rotary;
-      if (aligned_x && aligned_y)
-        *reinterpret_cast<uint4*>(y + 2 * el) = __ldg(reinterpret_cast<const uint4*>(x + 2 * el));
-      else
-        for (int i = 0; i < 8; ++i)
-          reinterpret_cast<uint16_t*>(y)[el + i] = reinterpret_cast<const uint16_t*>(x)[el + i];
-      continue;
-    }
-    const int el = r.offset + g * 8;
-    float u[8];
-    load8<F16>(x + 2 * el, aligned_x, v);
-    if (!r.interleaved) load8<F16>(x + 2 * (el + half), aligned_x, u);
-    const float2* s = sines + t * half;
-    if (!r.interleaved) {
-      float w[8];
+    if (k >= kThreads) ask(k);
+    uint8_t* to = y0 + t * P.y_ts + h * P.y_hs + 2 * element();
+    if (g < turning) {
+      const float4* s = reinterpret_cast<const float4*>(sines + t * half) + g;
+      float v[8];
+      floats8<F16>(a, v);
+      if (r.interleaved) {
+        turn_pairs(v, s, table.groups);
+      } else {
+        float w[8];
+        floats8<F16>(b, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 z = s[g * 8 + i];
-        w[i] = u[i] * z.x + v[i] * z.y;
-        v[i] = v[i] * z.x - u[i] * z.y;
+        for (int i = 0; i < 4; ++i) {
+          const float4 z = s[i * table.groups];
+          const float v0 = v[2 * i], v1 = v[2 * i + 1], w0 = w[2 * i], w1 = w[2 * i + 1];
+          v[2 * i] = v0 * z.x - w0 * z.y;
+          v[2 * i + 1] = v1 * z.z - w1 * z.w;
+          w[2 * i] = w0 * z.x + v0 * z.y;
+          w[2 * i + 1] = w1 * z.z + v1 * z.w;
+        }
+        put8(to + 2 * half, aligned_y, narrow8<F16>(w));
       }
-      store8<F16>(y + 2 * (el + half), aligned_y, w);
-    } else {
-      turn8(v, v, g * 8, r, s);
+      a = narrow8<F16>(v);
     }
-    store8<F16>(y + 2 * el, aligned_y, v);
+    put8(to, aligned_y, a);
   }
 }
 
@@ -210,22 +256,24 @@ __global__ void __launch_bounds__(kThreads)
 struct PackParams {
   PackCommon c;
   int32_t lanes;         // of a head of codes: a power of two
-  int32_t key_passes, value_passes, wide_passes;  // of a warp over a token's heads
+  int32_t key_passes, value_passes;  // of a warp over a token's heads; then the wide ones
+  int32_t keys_each;     // passes over keys of a block; of the others it has one
   int32_t tokens_each;   // tokens of a block
-  int64_t first[kPackItemsMax];  // first token of each item, past the last one INT64_MAX
+  Div half, wide;
+  int32_t first[kPackItemsMax];  // first block of each item, past the last one INT32_MAX
   PackItem items[kPackItemsMax];
 };
 static_assert(sizeof(PackParams) <= 32764, "pack item table too large");
 
-// The last of n entries that is <= x.
-__device__ __forceinline__ int item_of(const int64_t* first, int n, int64_t x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= x) lo = mid;
-    else hi = mid - 1;
+// The last of the entries that is <= x; called by whole warps.
+template <class T, int MAX>
+__device__ __forceinline__ int item_of(const T (&first)[MAX], int n, T x) {
+  int found = 0;
+  for (int k = 0; k < n; k += 32) {
+    const int i = k + (threadIdx.x & 31);
+    found += __popc(__ballot_sync(~0u, i < n && first[i] <= x));
   }
-  return lo;
+  return found - 1;
 }
 
 // Where the bytes of one packed row go: the caller's row, or the tail ring and
@@ -241,123 +289,159 @@ __device__ __forceinline__ void put(const RowOut& to, int at, T v) {
   if (to.b) *reinterpret_cast<T*>(to.b + at) = v;
 }
 
-template <bool F16>
+// A block has some tokens of an item and one pass over their heads: as many heads
+// of keys, or of values, as the warp has groups of lanes for, or 256 wide
+// elements.  So a thread's heads and elements are the same for all its tokens, and
+// finding them costs it nothing per token.  Where there are blocks enough, one has
+// all passes over its tokens' keys instead, and makes their sines once.  A token's
+// elements are asked for a token ahead.  The conversions bound it: 67 MB in, 35 MB out
+// in 30 us where a copy takes 15.  LONG: heads of more than 512 elements, 32 a lane.
+template <bool F16, bool LONG>
 __global__ void __launch_bounds__(kThreads)
     pack_kernel(const __grid_constant__ PackParams P) {
-  __shared__ float2 sines[kSinesMax];
+  __shared__ alignas(16) float2 sines[kSinesMax];
+  constexpr int Z = LONG ? 2 : 1;
   const PackCommon& c = P.c;
   const PackedLayout& l = c.l;
   const Rotation& r = c.r;
-  const int half = r.rotary / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t0 = (int64_t)blockIdx.x * P.tokens_each;
-  const int n = (int)min((int64_t)P.tokens_each, c.tokens - t0);
-  if (r.rotary) {
+  const SineTable table(r);
+  const int half = table.half, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = c.n_items > 1 ? item_of(P.first, c.n_items, (int32_t)blockIdx.x) : 0;
+  const PackItem& it = P.items[item];
+  const int t0 = (blockIdx.x - P.first[item]) * P.tokens_each, n = min(P.tokens_each, it.count - t0);
+  // what this thread has of every token
+  const int key_blocks = (P.key_passes + P.keys_each - 1) / P.keys_each;
+  const bool wide = (int)blockIdx.y >= key_blocks + P.value_passes;
+  const bool value = !wide && (int)blockIdx.y >= key_blocks;
+  int pass = (int)blockIdx.y - (wide ? key_blocks + P.value_passes : value ? key_blocks : 0);
+  int passes = 1;
+  if (!wide && !value) {
+    pass *= P.keys_each;
+    passes = min(P.keys_each, P.key_passes - pass);
+  }
+  const int at = lane & (P.lanes - 1);
+  int g = wide ? (int)P.wide.of(pass * 32 + lane) : pass * (32 / P.lanes) + lane / P.lanes;
+  bool on = g < l.kv;
+  const int elems = wide ? l.wide : value ? l.value : l.key8;
+  const int el0 = wide ? (pass * 32 + lane - g * (int)P.wide.d) * 8 : at * 16;
+  const uint8_t* const base = wide ? it.wide : value ? it.value : it.key;
+  const int64_t ts = wide ? c.w_ts : value ? c.v_ts : c.k_ts, hs = wide ? c.w_hs : value ? c.v_hs : c.k_hs;
+  const bool aligned = !(((uintptr_t)base | ts | hs) & 15);
+  const int from = r.offset - (wide ? l.key8 : 0);  // the rotary range among these elements
+  const bool turned = r.rotary && !value && from >= 0 && from < elems;
+  const uint8_t* const x0 = base + (int64_t)(t0 + warp) * ts + 2 * el0;
+  const uint8_t* x = x0 + (on ? g : 0) * hs;
+  uint4 a[Z][2], b[Z][2];  // elements, and the partners of half pairs
+  auto each = [&](auto f) {  // f(z, q, element) for the groups of eight of this thread
+#pragma unroll
+    for (int z = 0; z < Z; ++z)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int e = el0 + z * P.lanes * 16 + 8 * q;
+        if (on && e < elems && !(wide && (z || q))) f(z, q, e);
+      }
+  };
+  auto in_range = [&](int e) { return turned && e >= from && e < from + r.rotary; };
+  auto ask = [&] {
+    each([&](int z, int q, int e) {
+      const uint8_t* p = x + 2 * (e - el0);
+      a[z][q] = raw8(p, aligned);
+      if (!r.interleaved && in_range(e)) b[z][q] = raw8(p + (e - from < half ? 2 * half : -2 * half), aligned);
+    });
+    x += kWarps * ts;
+  };
+  if (warp < n) ask();
+  if (turned) {  // for all threads of the block
     for (int k = threadIdx.x; k < n * half; k += kThreads) {
-      const int t = k / half;
-      const int i = item_of(P.first, c.n_items, t0 + t);
-      sines[k] = sine_of(__ldg(r.turns + (k - t * half)),
-                         __ldg(P.items[i].position + (t0 + t - P.first[i])), r);
+      const int i = P.half.of(k);
+      sines[i * half + table.place(k - i * half)] =
+          sine_of(__ldg(r.turns + (k - i * half)), __ldg(it.position + t0 + i), r);
     }
     __syncthreads();
   }
-  const int passes = P.key_passes + P.value_passes + P.wide_passes;
+  int t = warp;
 #pragma unroll 1
-  for (int unit = warp; unit < n * passes; unit += kWarps) {
-    const int t = unit / passes;
-    int pass = unit - t * passes;
-    const int i = item_of(P.first, c.n_items, t0 + t);
-    const PackItem& it = P.items[i];
-    const int64_t j = t0 + t - P.first[i];
+  for (;;) {
+    if (t >= n) {  // the block's next heads
+      if (!--passes || warp >= n) break;
+      g += 32 / P.lanes;
+      on = g < l.kv;
+      x = x0 + (on ? g : 0) * hs;
+      t = warp;
+      ask();
+    }
+    const int now = t;
+    t += kWarps;
+    float v[Z][2][8];
+    float top = 0.f;
+    uint4 raw = a[0][0];
+    each([&](int z, int q, int e) {
+      floats8<F16>(a[z][q], v[z][q]);
+      if (in_range(e)) {
+        const int j = e - from;
+        const float4* s = reinterpret_cast<const float4*>(sines + now * half);
+        if (r.interleaved) {
+          turn_pairs(v[z][q], s + j / 8, table.groups);
+        } else {
+          float u[8];
+          floats8<F16>(b[z][q], u);
+          turn_half(v[z][q], u, j < half ? 1.f : -1.f, s + (j < half ? j : j - half) / 8, table.groups);
+        }
+        if (wide) raw = narrow8<F16>(v[0][0]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[z][q][k]));
+    });
+    if (t < n) ask();
     RowOut to;
     if (it.rows) {
-      to = {it.rows + j * l.row_bytes, nullptr};
+      to = {it.rows + (int64_t)(t0 + now) * l.row_bytes, nullptr};
     } else {
-      const int64_t row = it.L0 + j;
-      to = {c.tail + ((size_t)it.pair * c.T + (size_t)(row % c.T)) * l.row_bytes,
-            it.host ? it.host + row * l.row_bytes : nullptr};
+      const uint32_t row = (uint32_t)(it.L0 + t0 + now);
+      to = {c.tail + ((size_t)it.pair * c.T + row % (uint32_t)c.T) * l.row_bytes,
+            it.host ? it.host + (size_t)row * l.row_bytes : nullptr};
     }
-    const float2* s = sines + t * half;
-    if (pass >= P.key_passes + P.value_passes) {  // wide elements, 8 a lane
-      const int per = l.wide / 8, k = (pass - P.key_passes - P.value_passes) * 32 + lane;
-      const int g = k / per, el = (k - g * per) * 8;
-      if (g >= l.kv) continue;
-      const uint8_t* x = it.wide + j * c.w_ts + g * c.w_hs;
-      const bool aligned = !(((uintptr_t)it.wide | c.w_ts | c.w_hs) & 15);
-      const int from = r.offset - l.key8;  // rotary range within the wide elements
-      float v[8], u[8];
-      load8<F16>(x + 2 * el, aligned, v);
-      if (r.rotary && el >= from && el < from + r.rotary) {
-        const int e = el - from;
-        if (!r.interleaved) load8<F16>(x + 2 * (e < half ? el + half : el - half), aligned, u);
-        turn8(v, u, e, r, s);
-      }
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) w[q] = narrow2<F16>(v[2 * q], v[2 * q + 1]);
-      put(to, l.off_wide + 2 * (g * l.wide + el), make_uint4(w[0], w[1], w[2], w[3]));
+    if (wide) {
+      if (on) put(to, l.off_wide + 2 * (g * l.wide + el0), raw);
       continue;
     }
-    const bool value = pass >= P.key_passes;
-    if (value) pass -= P.key_passes;
-    const int elems = value ? l.value : l.key8;
-    const int g = pass * (32 / P.lanes) + lane / P.lanes, at = lane % P.lanes;
-    const bool on = g < l.kv;
-    const uint8_t* base = value ? it.value : it.key;
-    const int64_t ts = value ? c.v_ts : c.k_ts, hs = value ? c.v_hs : c.k_hs;
-    const bool aligned = !(((uintptr_t)base | ts | hs) & 15);
-    const uint8_t* x = base + j * ts + (on ? g : 0) * hs;
-    // 16 elements a lane; heads of more than 512 have lanes with 16 more
-    float v[2][2][8];
-    float top = 0.f;
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const int el = (at + z * P.lanes) * 16;
-      if (!on || el >= elems) continue;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int e = el + 8 * q;
-        load8<F16>(x + 2 * e, aligned, v[z][q]);
-        if (!value && r.rotary && e >= r.offset && e < r.offset + r.rotary && r.offset < l.key8) {
-          float u[8];
-          const int k = e - r.offset;
-          if (!r.interleaved) load8<F16>(x + 2 * (k < half ? e + half : e - half), aligned, u);
-          turn8(v[z][q], u, k, r, s);
-        }
+    // Infinities, which are rare, make NaN codes and leave the scale to the rest;
+    // a NaN is passed over by the maximum and is a NaN code by itself.
+    if (top == INFINITY) {
+      top = 0.f;
+      each([&](int z, int q, int) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float m = fabsf(v[z][q][k]);
-          if (m < INFINITY) top = fmaxf(top, m);
+          if (fabsf(v[z][q][k]) == INFINITY) v[z][q][k] = NAN;
+          top = fmaxf(top, fabsf(v[z][q][k]));
         }
-      }
+      });
     }
+    __syncwarp();
 #pragma unroll
     for (int w = 16; w; w >>= 1)
       if (w < P.lanes) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
     if (!on) continue;
     const int e = exponent_of(top);
     const float inverse = power_of_two(-e);
+    const int head = (value ? l.off_value : 0) + g * elems;
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const int el = (at + z * P.lanes) * 16;
+    for (int z = 0; z < Z; ++z) {
+      const int el = el0 + z * P.lanes * 16;
       if (el >= elems) continue;
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float f[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float a = v[z][k >> 1][(k & 1) * 4 + q];
-          f[q] = fabsf(a) < INFINITY ? a * inverse : NAN;
-        }
-        w[k] = codes2(f[0], f[1]) | (uint32_t)codes2(f[2], f[3]) << 16;
+        const float* f = &v[z][k >> 1][(k & 1) * 4];
+        w[k] = codes2(f[0] * inverse, f[1] * inverse) |
+               (uint32_t)codes2(f[2] * inverse, f[3] * inverse) << 16;
       }
-      put(to, (value ? l.off_value : 0) + g * elems + el, make_uint4(w[0], w[1], w[2], w[3]));
+      put(to, head + el, make_uint4(w[0], w[1], w[2], w[3]));
     }
     if (at == 0) {
       put(to, l.off_scale + 4 * (value ? l.kv + g : g), power_of_two(e));
       if (!value && g == 0)  // what is left of the last 16 bytes
-        for (int b = l.off_scale + 4 * l.kv * (l.shared ? 1 : 2); b < l.row_bytes; b += 4)
-          put(to, b, 0.f);
+        for (int k = l.off_scale + 4 * l.kv * (l.shared ? 1 : 2); k < l.row_bytes; k += 4) put(to, k, 0.f);
     }
   }
 }
@@ -366,16 +450,18 @@ __global__ void __launch_bounds__(kThreads)
 
 struct UnpackParams {
   UnpackCommon c;
-  int32_t pieces;        // of a row: 16 codes or 8 wide elements each
-  int64_t first[kUnpackItemsMax];
+  int32_t coded, values, wides;  // pieces of a row, of 8 elements
+  int32_t lanes, lanes_log;      // of a row
+  Div key, value, wide;          // of a head
+  int32_t first[kUnpackItemsMax];  // first block of each item, past the last one INT32_MAX
   UnpackItem items[kUnpackItemsMax];
 };
 static_assert(sizeof(UnpackParams) <= 32764, "unpack item table too large");
 
-constexpr int kWarpRows = 4;
-
-// Where entry j of an item lies: 0: zeros, 1: untouched.
-__device__ __forceinline__ uintptr_t entry_of(const UnpackCommon& c, const UnpackItem& it, int64_t j) {
+// Where entry j of an item lies: 0: zeros, 1: untouched.  `first`: the one thread
+// that says so where a location is outside its arena.
+__device__ __forceinline__ uintptr_t entry_of(const UnpackCommon& c, const UnpackItem& it, int64_t j,
+                                              bool first) {
   const size_t rb = (size_t)c.l.row_bytes;
   if (it.rows) return (uintptr_t)(it.rows + j * rb);
   if (it.loc) {
@@ -386,14 +472,14 @@ __device__ __forceinline__ uintptr_t entry_of(const UnpackCommon& c, const Unpac
     const uint32_t rows = tier == kTierTail ? c.tail_rows : tier == kTierOpt ? c.opt_rows
                           : tier == kTierHot ? c.hot_rows : 0;
     if (x >= rows) {
-      atomicOr(c.status, kStatusEloc);
+      if (first) atomicOr(c.status, kStatusEloc);
       return 0;
     }
     return (uintptr_t)((tier == kTierTail ? c.tail : tier == kTierOpt ? c.opt : c.hot) + x * rb);
   }
   const int64_t row = it.first + j;
-  if (row >= it.L - c.T)
-    return (uintptr_t)(c.tail + ((size_t)it.pair * c.T + (size_t)(row % c.T)) * rb);
+  if (row >= it.L - c.T)  // (rows are numbered in 31 bits)
+    return (uintptr_t)(c.tail + ((size_t)it.pair * c.T + (uint32_t)row % (uint32_t)c.T) * rb);
   const int64_t page = row >> c.page_shift;
   const int32_t slot = page < it.complete ? __ldg(c.map + (size_t)it.pair * c.Pmax + page) : -1;
   if (slot >= 0)
@@ -401,74 +487,66 @@ __device__ __forceinline__ uintptr_t entry_of(const UnpackCommon& c, const Unpac
   return (uintptr_t)(it.host + row * rb);
 }
 
+// Eight lanes have a row (16 or 32 where each still has 16 elements or more), each
+// eight of its elements at a time, so that their stores are whole lines; they ask
+// for those of four turns at once.  What belongs to the row (its address, where
+// its numbers go) is found once, for four rows of a warp together: the instructions
+// bound it.  262,144 located rows of 656 bytes, whose 16-bit numbers are 4/5 of the
+// bytes: 86 us, 4.1 TB/s (each lane finding row, item and head of each piece: 158; a
+// warp's rows in turn 125; a row a warp 123).
 template <bool F16>
 __global__ void __launch_bounds__(kThreads)
     unpack_kernel(const __grid_constant__ UnpackParams P) {
   const UnpackCommon& c = P.c;
   const PackedLayout& l = c.l;
-  const int lane = threadIdx.x & 31;
-  const int64_t e0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kWarpRows;
-  if (e0 >= c.count) return;
-  // lane r finds the address of row r
-  uintptr_t mine = 1;
-  int item = 0;
-  int64_t entry = 0;
-  if (lane < kWarpRows && e0 + lane < c.count) {
-    item = item_of(P.first, c.n_items, e0 + lane);
-    entry = e0 + lane - P.first[item];
-    mine = entry_of(c, P.items[item], entry);
-  }
-  const int coded = l.kv * l.key8 / 16, values = l.shared ? 0 : l.kv * l.value / 16;
-#pragma unroll 2
-  for (int k0 = 0; k0 < kWarpRows * P.pieces; k0 += 32) {
-    const int k = k0 + lane, row = min(k / P.pieces, kWarpRows - 1), p = k - row * P.pieces;
-    const uintptr_t from = __shfl_sync(~0u, (unsigned long long)mine, row);
-    const int64_t j = __shfl_sync(~0u, (long long)entry, row);
-    const UnpackItem& it = P.items[__shfl_sync(~0u, item, row)];
-    if (from == 1 || p >= P.pieces) continue;
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(from);
-    uint8_t* key = it.key ? it.key + j * c.k_rs : nullptr;
-    uint8_t* value = it.value ? it.value + j * c.v_rs : nullptr;
-    if (p >= coded + values) {
-      const int per = l.wide / 8, q = p - coded - values, g = q / per, el = (q - g * per) * 8;
-      if (!key) continue;
-      float v[8] = {};
-      if (src) load8<F16>(src + l.off_wide + 16 * q, true, v);
-      uint8_t* to = key + g * c.k_hs + 2 * (l.key8 + el);
-      store8<F16>(to, !((uintptr_t)to & 15), v);
-      continue;
-    }
-    const bool is_value = p >= coded;
-    const int n = is_value ? l.value : l.key8, at = (is_value ? p - coded : p) * 16;
-    const int g = at / n, el = at - g * n;
-    float v[2][8] = {};
+  const int lanes = P.lanes, lane = threadIdx.x & (lanes - 1);
+  const int item = c.n_items > 1 ? item_of(P.first, c.n_items, (int32_t)blockIdx.x) : 0;
+  const UnpackItem& it = P.items[item];
+  const int64_t j = ((int64_t)(blockIdx.x - P.first[item]) * kThreads + threadIdx.x) >> P.lanes_log;
+  if (j >= it.count) return;
+  const uintptr_t from = entry_of(c, it, j, lane == 0);
+  if (from == 1) return;
+  const uint8_t* const src = reinterpret_cast<const uint8_t*>(from);
+  uint8_t* const key = it.key ? it.key + j * c.k_rs : nullptr;
+  uint8_t* const value = it.value ? it.value + j * c.v_rs : nullptr;
+  const float* const scales = reinterpret_cast<const float*>(src + l.off_scale);
+  const bool plain = l.kv == 1, too = l.shared && value;
+  const bool aligned = !(((uintptr_t)it.key | c.k_rs | c.k_hs | (uintptr_t)it.value | c.v_rs | c.v_hs) & 15);
+  const float only = src && plain ? __ldg(scales) : 0.f;
+  // key codes, then value codes, which follow them in the row
+  const int q0 = key || too ? 0 : P.coded, q1 = P.coded + (value ? P.values : 0);
+#pragma unroll 4
+  for (int q = q0 + lane; q < q1; q += lanes) {
+    const bool v = q >= P.coded;
+    const int i = v ? q - P.coded : q;
+    const int g = plain ? 0 : (int)(v ? P.value.of(i) : P.key.of(i));
+    const int el = (i - g * (int)(v ? P.value.d : P.key.d)) * 8;
+    uint4 y = make_uint4(0, 0, 0, 0);
     if (src) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + (is_value ? l.off_value : 0) + at));
-      const float scale = __ldg(reinterpret_cast<const float*>(src + l.off_scale) +
-                                (is_value ? l.kv + g : g));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float2 f = numbers2((uint16_t)(u[q >> 1] >> (16 * (q & 1))), scale);
-        v[q >> 2][2 * (q & 3)] = f.x;
-        v[q >> 2][2 * (q & 3) + 1] = f.y;
-      }
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(src) + q);
+      const float z = plain && !v ? only : __ldg(scales + (v ? l.kv + g : g));
+      const float2 a = numbers2((uint16_t)w.x, z), b = numbers2((uint16_t)(w.x >> 16), z);
+      const float2 d = numbers2((uint16_t)w.y, z), e = numbers2((uint16_t)(w.y >> 16), z);
+      y = make_uint4(narrow2<F16>(a.x, a.y), narrow2<F16>(b.x, b.y), narrow2<F16>(d.x, d.y),
+                     narrow2<F16>(e.x, e.y));
     }
-    auto out = [&](uint8_t* to) {
-      const bool aligned = !((uintptr_t)to & 15);
-      store8<F16>(to, aligned, v[0]);
-      store8<F16>(to + 16, aligned, v[1]);
-    };
-    if (is_value) {
-      if (value) out(value + g * c.v_hs + 2 * el);
+    if (v) {
+      put8(value + g * c.v_hs + 2 * el, aligned, y);
     } else {
-      if (key) out(key + g * c.k_hs + 2 * el);
-      if (l.shared && value && el < l.value) out(value + g * c.v_hs + 2 * el);
+      if (key) put8(key + g * c.k_hs + 2 * el, aligned, y);
+      if (too && el < l.value) put8(value + g * c.v_hs + 2 * el, aligned, y);
     }
+  }
+  if (!key) return;
+#pragma unroll 1
+  for (int q = lane; q < P.wides; q += lanes) {
+    const int g = plain ? 0 : (int)P.wide.of(q);
+    const uint4 y = src ? __ldg(reinterpret_cast<const uint4*>(src + l.off_wide) + q) : make_uint4(0, 0, 0, 0);
+    put8(key + g * c.k_hs + 2 * (l.key8 + (q - g * (int)P.wide.d) * 8), aligned, y);
   }
 }
 
-// Tokens of a block of which each has `units` of work: enough for its warps,
+// Tokens of a block of which each has `units` of work: enough for its threads,
 // no more than the sines hold or than leave every SM a block.
 int tokens_of_block(int64_t tokens, int rotary, int units, int want, int sms) {
   int64_t n = std::max<int64_t>(1, want / std::max(1, units));
@@ -483,8 +561,11 @@ cudaError_t launch_rotate(const RotateParams& p, int sms, cudaStream_t stream) {
   const int groups = p.elems / 8;
   const int each = tokens_of_block(p.tokens, p.r.rotary, p.heads * groups, 4 * kThreads, sms);
   const int blocks = (p.tokens + each - 1) / each;
-  if (p.f16) rotate_kernel<true><<<blocks, kThreads, 0, stream>>>(p, each);
-  else rotate_kernel<false><<<blocks, kThreads, 0, stream>>>(p, each);
+  const int turning = (p.r.interleaved ? p.r.rotary : p.r.rotary / 2) / 8;
+  const int rest = p.x == p.y ? 0 : (p.elems - p.r.rotary) / 8;  // in place: nothing is copied
+  const RotateGrid g{div_by(turning + rest), div_by(p.heads), div_by(p.r.rotary / 2), each};
+  if (p.f16) rotate_kernel<true><<<blocks, kThreads, 0, stream>>>(p, g);
+  else rotate_kernel<false><<<blocks, kThreads, 0, stream>>>(p, g);
   return cudaGetLastError();
 }
 
@@ -495,15 +576,6 @@ cudaError_t launch_pack(const PackCommon& c, const PackItem* items, int n_items,
   PackParams P;
   P.c = c;
   P.c.n_items = n_items;
-  int64_t tokens = 0;
-  for (int i = 0; i < kPackItemsMax; ++i) {
-    P.first[i] = i < n_items ? tokens : INT64_MAX;
-    if (i >= n_items) continue;
-    P.items[i] = items[i];
-    tokens += items[i].count;
-  }
-  P.c.tokens = tokens;
-  if (!tokens) return cudaSuccess;
   const PackedLayout& l = c.l;
   const int longest = std::max(l.key8, l.shared ? 0 : l.value);
   P.lanes = 1;
@@ -511,13 +583,27 @@ cudaError_t launch_pack(const PackCommon& c, const PackItem* items, int n_items,
   const int heads = 32 / P.lanes;  // of a pass
   P.key_passes = (l.kv + heads - 1) / heads;
   P.value_passes = l.shared ? 0 : P.key_passes;
-  P.wide_passes = (l.kv * (l.wide / 8) + 31) / 32;
-  const int passes = P.key_passes + P.value_passes + P.wide_passes;
-  P.tokens_each = tokens_of_block(tokens, c.r.rotary, passes, 2 * kWarps, sms);
-  const int64_t blocks = (tokens + P.tokens_each - 1) / P.tokens_each;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  if (l.f16) pack_kernel<true><<<(int)blocks, kThreads, 0, stream>>>(P);
-  else pack_kernel<false><<<(int)blocks, kThreads, 0, stream>>>(P);
+  const int wide_passes = (l.kv * (l.wide / 8) + 31) / 32;
+  int64_t tokens = 0, blocks = 0;
+  for (int i = 0; i < n_items; ++i) tokens += items[i].count;
+  const int64_t passes = P.key_passes + P.value_passes + wide_passes;
+  P.tokens_each = tokens_of_block(tokens * passes, c.r.rotary, 1, 4 * kWarps, sms);
+  for (int i = 0; i < kPackItemsMax; ++i) {
+    P.first[i] = i < n_items ? (int32_t)std::min<int64_t>(blocks, INT32_MAX) : INT32_MAX;
+    if (i >= n_items) continue;
+    P.items[i] = items[i];
+    blocks += ((int64_t)items[i].count + P.tokens_each - 1) / P.tokens_each;
+  }
+  if (!blocks) return cudaSuccess;
+  P.keys_each = blocks >= 2 * sms ? P.key_passes : 1;
+  const int64_t rows = (P.key_passes + P.keys_each - 1) / P.keys_each + P.value_passes + wide_passes;
+  if (blocks > INT32_MAX || rows > 65535) return cudaErrorInvalidValue;
+  P.half = div_by(std::max(1, c.r.rotary / 2));
+  P.wide = div_by(std::max(1, l.wide / 8));
+  const bool wider = P.lanes * 16 < longest;
+  auto kernel = l.f16 ? (wider ? pack_kernel<true, true> : pack_kernel<true, false>)
+                      : (wider ? pack_kernel<false, true> : pack_kernel<false, false>);
+  kernel<<<dim3((unsigned)blocks, (unsigned)rows), kThreads, 0, stream>>>(P);
   return cudaGetLastError();
 }
 
@@ -529,18 +615,25 @@ cudaError_t launch_unpack(const UnpackCommon& c, const UnpackItem* items, int n_
   UnpackParams P;
   P.c = c;
   P.c.n_items = n_items;
-  int64_t count = 0;
+  const PackedLayout& l = c.l;
+  P.coded = l.kv * l.key8 / 8;
+  P.values = l.shared ? 0 : l.kv * l.value / 8;
+  P.wides = l.kv * l.wide / 8;
+  P.lanes_log = 3;
+  while (P.lanes_log < 5 && P.coded + P.values >= 16 << P.lanes_log) ++P.lanes_log;
+  P.lanes = 1 << P.lanes_log;
+  const int rows = kThreads / P.lanes;  // of a block
+  int64_t blocks = 0;
   for (int i = 0; i < kUnpackItemsMax; ++i) {
-    P.first[i] = i < n_items ? count : INT64_MAX;
+    P.first[i] = i < n_items ? (int32_t)std::min<int64_t>(blocks, INT32_MAX) : INT32_MAX;
     if (i >= n_items) continue;
     P.items[i] = items[i];
-    count += items[i].count;
+    blocks += ((int64_t)items[i].count + rows - 1) / rows;
   }
-  P.c.count = count;
-  if (!count) return cudaSuccess;
-  const PackedLayout& l = c.l;
-  P.pieces = l.kv * (l.key8 / 16 + (l.shared ? 0 : l.value / 16) + l.wide / 8);
-  const int64_t blocks = (count + kWarps * kWarpRows - 1) / (kWarps * kWarpRows);
+  if (!blocks) return cudaSuccess;
+  P.key = div_by(l.key8 / 8);
+  P.value = div_by(l.value / 8);
+  P.wide = div_by(std::max(1, l.wide / 8));
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (l.f16) unpack_kernel<true><<<(int)blocks, kThreads, 0, stream>>>(P);
   else unpack_kernel<false><<<(int)blocks, kThreads, 0, stream>>>(P);
