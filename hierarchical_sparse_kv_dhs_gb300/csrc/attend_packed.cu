@@ -23,11 +23,12 @@
 //     first, a piece is the upper byte of the number plus half a unit, and what
 //     is left is exact in f16: 3 pieces hold 9 bits (an error of 2^-9 of a
 //     weight and f16's 2^-11: less than bf16's 2^-8), 4 hold all of f16's 11.
-//     m follows the maximum of s_j + v_j: weights reach 2^11..2^15, and those
-//     down to 2^-17 are held, 2^-28 to 2^-32 of the largest.  (e4m3 would hold
-//     2^-18 at best: half a million rows that share the weight of one that
-//     stands out would be lost.)
-// l sums the weights unrounded, without 2^v_j, which is divided out exactly.
+//     m follows the maximum of s_j + v_j, and moves when one passes it by 2^6:
+//     the largest weight is 2^9 to 2^15, and those down to 2^-17 are held, 2^-26
+//     to 2^-32 of the largest.  (e4m3 would hold 2^-18 at best: half a million rows
+//     that share the weight of one that stands out would be lost.)
+// l sums the weights unrounded, without 2^v_j, which is divided out exactly (from
+// floats, which end at 2^-126 where the largest weight has 2^9 or more).
 //
 // The rest is the 16-bit attention's (attend.cu): roles, tiles of 128 rows, the
 // dealing of jobs and the joining of parts.
@@ -90,16 +91,6 @@ struct Pieces {
 };
 
 // ------------------------------------------------------------------ PTX
-
-// The waits of attend_core.cuh with the waiting itself out of line: code that
-// runs every tile is short that way, and stays in the instruction caches.
-__device__ __noinline__ void spin(uint32_t bar, uint32_t parity, const Patience& until) {
-  bar_wait(bar, parity, until);
-}
-__device__ __forceinline__ void await(uint32_t bar, uint32_t parity, const Patience& until) {
-  bar_wait(bar, parity, until);
-  __syncwarp();
-}
 
 // D += A B (D = A B unless add) of 8-bit operands.  A product of M = 128 takes
 // 32 + N/4 cycles in either kind (N 16 to 128, K 16 elements of 16 bits or 32 of
@@ -296,7 +287,7 @@ __device__ void load_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, int 
   Ring ring, rr, seg;
 #pragma unroll 1
   for (;;) {
-    await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
     if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
     const int32_t v0 = s.v0, v1 = s.v1;
@@ -306,7 +297,7 @@ __device__ void load_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, int 
     const uint32_t scale_at = pl.off_scale + 4 * s.g;
 #pragma unroll 1
     for (int tile = v0; tile < v1; ++tile) {
-      await(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
+      warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
       const uint8_t* row[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = ctl.row[rr.slot][r0 + 16 * i];
@@ -328,7 +319,7 @@ __device__ void load_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, int 
         const int u = i < nk ? i : i - nk - nw;
         const uint32_t from = (i < nk ? key_at : u < 0 ? wide_at : val_at) + u * 128;
         const int left = u < 0 ? 2 * pl.wide : (i < nk ? pl.key8 : c.dv) - u * 128;
-        await(smem_u32(&ctl.empty[ring.slot]), ring.phase ^ 1, until);
+        warp_wait(smem_u32(&ctl.empty[ring.slot]), ring.phase ^ 1, until);
         const uint32_t dst = mine + ring.slot * kChunk;
         if (all && left >= 128) {
           // (a wait that ran out may leave a null beside an old `all`: any row then)
@@ -377,7 +368,7 @@ __device__ void place_rows(const Params<MAXI>& P, Control& ctl, int lane) {
   Ring seg, rr;
 #pragma unroll 1
   for (;;) {
-    await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
     if (__any_sync(~0u, ctl.gave_up) || !s.cols) break;
     const AttendItem& it = s.it;
@@ -398,7 +389,7 @@ __device__ void place_rows(const Params<MAXI>& P, Control& ctl, int lane) {
     for (int tile = s.v0 - 2; tile < s.v1; ++tile) {
       asm volatile("cp.async.wait_all;" ::: "memory");  // asked for a tile ago
       if (tile >= s.v0) {
-        await(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1, until);
+        warp_wait(smem_u32(&ctl.rempty[rr.slot]), rr.phase ^ 1, until);
         bool all = true;
 #pragma unroll 1
         for (int k = lane; k < kTile; k += 32) {
@@ -472,26 +463,26 @@ __device__ void issue_scores(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
   uint32_t n = 0, qphase = 0;
 #pragma unroll 1
   for (;;) {
-    await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
     const int32_t v0 = uniform(s.v0), v1 = uniform(s.v1), cols = uniform(s.cols);
     if (__any_sync(~0u, ctl.gave_up) || !cols) break;
     if (lead) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
     seg.next(kSegments);
     if (v0 >= v1) continue;
-    await(smem_u32(&ctl.qfull), qphase, until);
+    warp_wait(smem_u32(&ctl.qfull), qphase, until);
     fence_async();
     qphase ^= 1;
 #pragma unroll 1
     for (int tile = v0; tile < v1; ++tile, ++n) {
       const uint32_t buf = two ? n & 1 : 0, use = two ? n >> 1 : n, d = tm_s + buf * pl.buf_columns;
-      if (use > 0) await(smem_u32(&ctl.sread[buf]), (use - 1) & 1, until);
+      if (use > 0) warp_wait(smem_u32(&ctl.sread[buf]), (use - 1) & 1, until);
       // Copies land in order: a slot that is full says that those before it are.
       // Waiting at the second slot and at the last one costs less than at each.
       // Every slot is 128 bytes wide, zeros past its slice.
 #pragma unroll 1
       for (int i = 0; i < parts; ++i) {
-        await(smem_u32(&ctl.full[ring.slot]), ring.phase, until);
+        warp_wait(smem_u32(&ctl.full[ring.slot]), ring.phase, until);
         fence_async();
         tc_after();
         if (lead) {
@@ -537,7 +528,7 @@ __device__ void issue_sums(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
   bool first = true;
 #pragma unroll 1
   for (;;) {
-    await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+    warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
     const Segment& s = ctl.seg[seg.slot];
     const int32_t v0 = uniform(s.v0), v1 = uniform(s.v1), cols = uniform(s.cols);
     if (__any_sync(~0u, ctl.gave_up) || !cols) break;
@@ -547,9 +538,9 @@ __device__ void issue_sums(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
     for (int tile = v0; tile < v1; ++tile, ++n) {
       const uint32_t p_lo = operand_lo(base + pl.off_p + (two && n & 1 ? S::kWeights : 0), 16);
       ring = further(ring, before, pl.slots);
-      await(smem_u32(&ctl.pfull[n & 1]), n >> 1 & 1, until);
+      warp_wait(smem_u32(&ctl.pfull[n & 1]), n >> 1 & 1, until);
       if (tile == v0 && !first) {  // the previous segment's sums are read
-        await(smem_u32(&ctl.oempty), ophase, until);
+        warp_wait(smem_u32(&ctl.oempty), ophase, until);
         ophase ^= 1;
       }
       first = false;
@@ -557,7 +548,7 @@ __device__ void issue_sums(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
       const bool begun = tile > v0 || uniform(*(volatile uint32_t*)&ctl.o_begun);
       if (!pl.shared) {
         const Ring end = further(ring, pl.units - 1, pl.slots);
-        await(smem_u32(&ctl.full[end.slot]), end.phase, until);
+        warp_wait(smem_u32(&ctl.full[end.slot]), end.phase, until);
         fence_async();
         tc_after();
       }
@@ -702,7 +693,7 @@ __device__ __noinline__ void odd_rows(const Params<MAXI>& P, uint8_t* sm, Contro
   }
 #pragma unroll 1
   for (int u = 0; u < pl.units; ++u) {
-    await(smem_u32(&ctl.full[at.slot]), at.phase, until);
+    warp_wait(smem_u32(&ctl.full[at.slot]), at.phase, until);
     if (odd && tid < kTile) {
       uint8_t* to = sm + pl.off_rows + at.slot * kChunk + r * 128;
 #pragma unroll 1
@@ -734,7 +725,7 @@ __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, i
   auto sum = [](float a, float b) { return a + b; };
   // waits for tile m's sums
   auto summed = [&](uint32_t m) {
-    await(smem_u32(&ctl.odone[m & 1]), m >> 1 & 1, until);
+    warp_wait(smem_u32(&ctl.odone[m & 1]), m >> 1 & 1, until);
     tc_after();
   };
 #pragma unroll 1
@@ -746,7 +737,7 @@ __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, i
     for (int k = 0; k < C; ++k) l[k] = 0.f;
     bool some = false;
     if (!begin) {
-      await(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
+      warp_wait(smem_u32(&ctl.segfull[seg.slot]), seg.phase, until);
       // the previous segment's column tables are read; all leave together
       if (named_or(1, kSoftThreads, ctl.gave_up) || !s.cols) break;
       if (tid == 0) ctl.o_begun = 0;
@@ -783,20 +774,19 @@ __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, i
         const int32_t j = tile * kTile + r;
         const bool ragged = tile * kTile < all_lo || tile * kTile + kTile > all_hi;
         const uint32_t buf = two ? n & 1 : 0, tm = tm_s + buf * pl.buf_columns;
-        await(smem_u32(&ctl.sfull[buf]), (two ? n >> 1 : n) & 1, until);
+        warp_wait(smem_u32(&ctl.sfull[buf]), (two ? n >> 1 : n) & 1, until);
         tc_after();
         // the row and its scales: there since before its scores were made
-        await(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
+        warp_wait(smem_u32(&ctl.rfull[rr.slot]), rr.phase, until);
         const uint8_t* const row = ctl.row[rr.slot][r];
         const float ks = ctl.scale[rr.slot][0][r];
         const uint32_t vbits = __float_as_uint(ctl.scale[rr.slot][1][r]) >> 23 & 255;
         const RowScale z{ks, (float)((int)vbits - 127),
                          row ? __uint_as_float(max(1u, min(253u, 254u - vbits)) << 23) : 0.f};
         float x[C];  // scores and value scale in log2 units
-        constexpr int kBatch = 8;
 #pragma unroll
-        for (int k = 0; k < C; k += kBatch)
-          scores<N, F16, kBatch>(tm + k, qk + k0 + k, wide, pl.wide > 0, z, row != nullptr, x + k);
+        for (int k = 0; k < C; k += 8)
+          scores<N, F16, 8>(tm + k, qk + k0 + k, wide, pl.wide > 0, z, row != nullptr, x + k);
         tc_before();
         __syncwarp();
         if (lane == 0) {
@@ -939,7 +929,7 @@ __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, i
     {
       Ring next = seg;
       if (!begin) next.next(kSegments);
-      await(smem_u32(&ctl.segfull[next.slot]), next.phase, until);
+      warp_wait(smem_u32(&ctl.segfull[next.slot]), next.phase, until);
       const Segment& t = ctl.seg[next.slot];
       const bool split = !ctl.gave_up && t.cols && t.v0 < t.v1;
       if (__all_sync(~0u, split)) split_queries<N, F16>(P, sm, ctl, t, tid, ctl.qk[n_queries & 1]);

@@ -331,6 +331,8 @@ def make_step(step: int, items) -> tuple:
 
 
 def _address(t):
+    if t is None:
+        return None
     return t.data_ptr() if hasattr(t, "data_ptr") else t
 
 
@@ -454,8 +456,8 @@ def dhs_packed_bytes(rows: dhs_packed_rows) -> int:
 def pack_item(count, key, *, wide=None, value=None, positions=None, rows=None, req=0,
               src=0) -> dhs_pack_item:
     """A dhs_pack_item from torch tensors (or device addresses)."""
-    return dhs_pack_item(req, src, count, 0, *[_address(t) for t in (key, wide, value, positions,
-                                                                     rows)])
+    return dhs_pack_item(req, src, count, 0, _address(key), _address(wide), _address(value),
+                         _address(positions), _address(rows))
 
 
 def make_pack(items, rows, *, rotary_offset=0, rotary_elems=0, pairs="half", amplitude=1.0,
@@ -487,8 +489,8 @@ def dhs_append_packed(h, st: dhs_pack_step):
 def unpack_item(count, key, *, value=None, loc=None, rows=None, req=0, src=0, first=0,
                 flags=0) -> dhs_unpack_item:
     """A dhs_unpack_item from torch tensors (or device addresses)."""
-    return dhs_unpack_item(req, src, count, flags, first, *[_address(t) for t in (loc, rows, key,
-                                                                                  value)])
+    return dhs_unpack_item(req, src, count, flags, first, _address(loc), _address(rows),
+                           _address(key), _address(value))
 
 
 def make_unpack(items, rows, *, key_strides=None, value_strides=None) -> tuple:
