@@ -51,8 +51,8 @@
 // What bounds it (16 query heads on a 1152-byte latent row unless said):
 // 64 verify blocks of 8 queries over 2048 rows each, 234 us: every query's
 // rows staged once, 1.21 GB through the loading warps at 5.2 TB/s (DRAM
-// reads 409 MB, each distinct row once).  One token over 512K rows, 115 us:
-// 590 MB of DRAM reads at 5.8 TB/s between a start of 4 us and a merge of 10.
+// reads 409 MB, each distinct row once).  One token over 512K rows, 107 us:
+// 590 MB of DRAM reads at 5.8 TB/s between a start of 4 us and a merge of 5.
 // 128 heads, 158 us: one tile at a time is resident beside 64 queries, so
 // that loads, scores, weights and sums follow each other.
 #include <cuda_bf16.h>

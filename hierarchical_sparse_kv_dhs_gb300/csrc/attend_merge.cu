@@ -26,9 +26,13 @@ struct MergeParams {
 // Joins the parts of the split jobs in block order.  A warp has 128 value
 // elements of one column and every `groups`-th part; the groups' sums meet in
 // shared memory.  Bound by latency: statistics, then weights, then parts, each
-// a trip to L2; 104 jobs of 64 columns in 2 to 3 parts, 34 MB, take 23 us, one
-// job of 16 columns in 152 parts 13 (each on cold caches).
-__global__ void __launch_bounds__(kMergeWarps * 32, 2)
+// a trip to L2; 104 jobs of 64 columns in 2 to 3 parts, 34 MB, take 23 us.
+// MANY (16 groups): a warp asks for all of its parts and statistics at once, in
+// 128 registers; the sums are the same (one token over 512 K rows in 152 parts:
+// 16-bit rows 113 -> 107 us, packed rows 77.5 -> 71.9).  With few parts to a warp
+// there is nothing to ask for ahead, and two blocks to an SM are worth more.
+template <bool MANY>
+__global__ void __launch_bounds__(kMergeWarps * 32, MANY ? 1 : 2)
     merge_kernel(const __grid_constant__ MergeParams M, const float* parts) {
   __shared__ float4 sums[kMergeWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -44,7 +48,48 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   float base = 0.f, z = 0.f;
-  if (on) {
+  if (on && MANY) {
+    constexpr int kStats = (kAttendMaxBlocks + 31) / 32;
+    constexpr int kParts = (kAttendMaxBlocks + kMergeWarps - 1) / kMergeWarps;
+    const size_t ml = (size_t)M.columns * M.dv + col;
+    float m[kStats], l[kStats];
+    float4 y[kParts];
+#pragma unroll
+    for (int k = 0; k < kStats; ++k) {
+      const int i = lane + 32 * k;
+      m[k] = i < n ? part(i)[ml] : -INFINITY;
+      l[k] = i < n ? part(i)[ml + M.columns] : 0.f;
+    }
+    const int mine = group + lane * kMergeWarps;
+    const float my = mine < n ? part(mine)[ml] : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      if (group + k * kMergeWarps < n && d < M.dv)
+        y[k] = *reinterpret_cast<const float4*>(part(group + k * kMergeWarps) + (size_t)col * M.dv + d);
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kStats; ++k) top = fmaxf(top, m[k]);
+#pragma unroll
+    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+    base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int k = 0; k < kStats; ++k)
+      if (lane + 32 * k < n) z += exp2_fast(m[k] - base) * l[k];
+#pragma unroll
+    for (int w = 16; w; w >>= 1) z += __shfl_xor_sync(~0u, z, w);
+    const float weight = mine < n ? exp2_fast(my - base) : 0.f;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const float w = __shfl_sync(~0u, weight, k);
+      // a part without weight may hold sums that are not finite
+      if (group + k * kMergeWarps < n && w != 0.f && d < M.dv) {
+        x.x += w * y[k].x;
+        x.y += w * y[k].y;
+        x.z += w * y[k].z;
+        x.w += w * y[k].w;
+      }
+    }
+  } else if (on) {
     const size_t ml = (size_t)M.columns * M.dv + col;
     float m = -INFINITY;
 #pragma unroll 1
@@ -181,7 +226,8 @@ Shape shape_of(AttendCommon& c, AttendItem* items, int n_items, int sms, int mos
   const int parts = rest ? (int)std::min<int64_t>(s.blocks, longest * s.blocks / rest + 2) : 0;
   // Warps that share a column: few parts leave too little to each, many wait
   // in line.  8 x 2048 rows in 20 parts: 4 groups 16.4 us, 1 18.5, 16 20.5;
-  // 512 K rows in 152 parts: 16 groups 116.5 us, 4 122.3.
+  // 512 K rows in 152 parts: 16 groups 116.5 us, 4 122.3 (107 since 16 groups
+  // have a kernel of their own).
   s.groups = parts > 24 ? 16 : parts > 4 ? 4 : 1;
   if (rest) {
     int k = 0;
@@ -237,7 +283,8 @@ cudaError_t launch_merge(const AttendCommon& c, const Shape& s, const float* par
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel, M, parts);
+  return cudaLaunchKernelEx(&cfg, s.groups == kMergeWarps ? merge_kernel<true> : merge_kernel<false>, M,
+                            parts);
 }
 
 }  // namespace dhs
