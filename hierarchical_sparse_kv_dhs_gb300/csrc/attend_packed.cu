@@ -32,6 +32,25 @@
 //
 // The rest is the 16-bit attention's (attend.cu): roles, tiles of 128 rows, the
 // dealing of jobs and the joining of parts.
+//
+// What it takes and what bounds it (latent rows of 656 bytes and 16 heads in bf16
+// unless said; in parentheses the same call over 16-bit rows of 1152 bytes):
+//   - 64 verify blocks of 8 queries over 2048 rows each: 168 us (234), 688 MB of
+//     rows staged at 4.1 TB/s.  The copies alone take 90 us, the products 43 (36
+//     of 40 to 45 cycles a tile); what a tile waits for is the way from its scores
+//     to its weights.  An earlier step of this kernel took 170 us, and 135 without
+//     its copies: its softmax warps worked through 200 of 279 thousand cycles, and
+//     waited for scores for 66.  Some SMs run a fifth slower than the mean.
+//   - 128 heads, 16 blocks of 8: 169 us (158), the same way with 32 columns: a
+//     weight is made and written in three pieces instead of one, and a query's 128
+//     heads take four passes over the rows instead of two (48 or 64 columns a
+//     block, whose pieces' sums tensor memory does not hold apart: 210 us).
+//   - a history of 512,000 rows: 72 us (107), its rows at 4.9 TB/s of DRAM reads,
+//     then the joining kernel.
+//   - one query of 256 rows 12.3 us (14.3), 8 requests of 2048 rows 16.4 (17): once
+//     through the pipeline, and the joining kernel.
+//   - ragged f16 histories, 4 kv heads with values of their own: 51 us (41): 64 MB,
+//     12 tiles a block, of which each weight takes four pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

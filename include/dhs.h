@@ -700,7 +700,8 @@ int dhs_rope_table(const dhs_rope_config *cfg, uint64_t *turns);
  *                  strides are multiples of 8 move faster)
  *   position_dev   int32 [tokens]
  *   turns_dev      uint64 [rotary_elems / 2] (dhs_rope_table), device memory
- * head_elems and rotary_offset are multiples of 8, rotary_elems of 16.
+ * head_elems and rotary_offset are multiples of 8, rotary_elems of 16; heads and
+ * head_elems are at most 65536, rotary_elems at most 4096.
  */
 typedef struct {
   int32_t dtype;
