@@ -453,6 +453,16 @@ def dhs_packed_bytes(rows: dhs_packed_rows) -> int:
     return n.value
 
 
+def _array(kind, items):
+    """The items as a C array; by their bytes, which is several times faster
+    than an argument each."""
+    if not items:
+        return (kind * 1)()
+    if any(type(it) is not kind for it in items):
+        raise TypeError(f"{kind.__name__}s are needed")
+    return (kind * len(items)).from_buffer_copy(b"".join(items))
+
+
 def pack_item(count, key, *, wide=None, value=None, positions=None, rows=None, req=0,
               src=0) -> dhs_pack_item:
     """A dhs_pack_item from torch tensors (or device addresses)."""
@@ -465,7 +475,7 @@ def make_pack(items, rows, *, rotary_offset=0, rotary_elems=0, pairs="half", amp
     """A dhs_pack_step plus the item array that must stay alive with it.
     Strides are (between tokens, between heads) in elements; the default is
     contiguous [count][kv_heads][elems]."""
-    arr = (dhs_pack_item * max(1, len(items)))(*items)
+    arr = _array(dhs_pack_item, items)
     st = dhs_pack_step()
     st.rows, st.n_items, st.items = rows, len(items), arr
     st.rotary_offset, st.rotary_elems = rotary_offset, rotary_elems
@@ -497,7 +507,7 @@ def make_unpack(items, rows, *, key_strides=None, value_strides=None) -> tuple:
     """A dhs_unpack_step plus the item array that must stay alive with it.
     Strides are (between rows, between heads) in elements; the default is
     contiguous [count][kv_heads][elems]."""
-    arr = (dhs_unpack_item * max(1, len(items)))(*items)
+    arr = _array(dhs_unpack_item, items)
     st = dhs_unpack_step()
     st.rows, st.n_items, st.items = rows, len(items), arr
     flat = lambda m: (rows.kv_heads * m, m)  # noqa: E731
@@ -517,7 +527,7 @@ def dhs_unpack_on(h, st: dhs_unpack_step, stream):
 def make_attend_packed(items, rows, *, heads, scale, q_strides=None, out_strides=None) -> tuple:
     """A dhs_attend_packed_step (without a workspace) over attend_item()s plus
     the item array that must stay alive with it; strides as make_attend's."""
-    arr = (dhs_attend_item * max(1, len(items)))(*items)
+    arr = _array(dhs_attend_item, items)
     st = dhs_attend_packed_step()
     st.rows, st.n_items, st.items, st.heads, st.scale = rows, len(items), arr, heads, scale
     n, m = rows.key_elems, rows.value_elems
