@@ -412,7 +412,7 @@ struct UnpackCommon {
   uint32_t* status;
   int64_t k_rs, k_hs, v_rs, v_hs;          // bytes
 };
-cudaError_t launch_unpack(const UnpackCommon& c, const UnpackItem* items, int n_items, int sms,
+cudaError_t launch_unpack(const UnpackCommon& c, const UnpackItem* items, int n_items,
                           cudaStream_t stream);
 
 // Attention over packed rows (attend_packed.cu), as attend_shape and

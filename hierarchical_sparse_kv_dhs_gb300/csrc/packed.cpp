@@ -265,7 +265,7 @@ int unpack_tables(dhs_pool* p, const dhs_unpack_step* st, dhs::UnpackCommon* out
 int launch_unpacks(dhs_pool* p, const dhs::UnpackCommon& c, const std::vector<dhs::UnpackItem>& items) {
   for (size_t b = 0; b < items.size(); b += dhs::kUnpackItemsMax) {
     const int n = (int)std::min<size_t>(dhs::kUnpackItemsMax, items.size() - b);
-    if (dhs::launch_unpack(c, items.data() + b, n, std::max(1, p->sm_count), p->stream) != cudaSuccess)
+    if (dhs::launch_unpack(c, items.data() + b, n, p->stream) != cudaSuccess)
       return DHS_ECUDA;
   }
   return DHS_OK;
