@@ -430,11 +430,11 @@ __device__ void place_rows(const Params<MAXI>& P, Control& ctl, int lane) {
           ctl.row[rr.slot][k] = p;
           all &= p != nullptr;
         }
+        // the vote orders no stores: all lanes' addresses have to be behind the arrival
         all = __all_sync(~0u, all);
-        if (lane == 0) {
-          ctl.all[rr.slot] = all;
-          bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
-        }
+        if (lane == 0) ctl.all[rr.slot] = all;
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_u32(&ctl.rfull[rr.slot]));
         rr.next(Control::kRowSlots);
       }
 #pragma unroll 1
@@ -486,6 +486,7 @@ __device__ void issue_scores(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
     const Segment& s = ctl.seg[seg.slot];
     const int32_t v0 = uniform(s.v0), v1 = uniform(s.v1), cols = uniform(s.cols);
     if (__any_sync(~0u, ctl.gave_up) || !cols) break;
+    __syncwarp();
     if (lead) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
     seg.next(kSegments);
     if (v0 >= v1) continue;
@@ -551,6 +552,7 @@ __device__ void issue_sums(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
     const Segment& s = ctl.seg[seg.slot];
     const int32_t v0 = uniform(s.v0), v1 = uniform(s.v1), cols = uniform(s.cols);
     if (__any_sync(~0u, ctl.gave_up) || !cols) break;
+    __syncwarp();
     if (lead) bar_arrive(smem_u32(&ctl.segempty[seg.slot]));
     seg.next(kSegments);
 #pragma unroll 1
