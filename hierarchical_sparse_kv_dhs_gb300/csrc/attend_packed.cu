@@ -20,13 +20,17 @@
 //     sign one more), but for elements under 2^-9 of a step's unit, 2^-18 of
 //     the largest one;
 //   - the weights exp(s_j - m) 2^v_j: e5m2, whose range is f16's.  Taken to f16
-//     first, a piece is the upper byte of the number plus half a unit, and what
-//     is left is exact in f16: 3 pieces hold 9 bits (an error of 2^-9 of a
-//     weight and f16's 2^-11: less than bf16's 2^-8), 4 hold all of f16's 11.
-//     m follows the maximum of s_j + v_j, and moves when one passes it by 2^6:
-//     the largest weight is 2^9 to 2^15, and those down to 2^-17 are held, 2^-26
-//     to 2^-32 of the largest.  (e4m3 would hold 2^-18 at best: half a million rows
-//     that share the weight of one that stands out would be lost.)
+//     first (2^-11 of a weight at most), a piece is the upper byte of the number
+//     plus half a unit, and what is left is exact in f16.  Three pieces hold every
+//     f16 number from 2^-6 up exactly, the smaller ones to 2^-17, half of e5m2's
+//     smallest; a fourth, which f16 rows make, holds nothing better.
+//     m follows the maximum of s_j + v_j, and moves when one passes it by 2^6: the
+//     largest weight is 2^9 to 2^15, so that 2^-17 is 2^-26 of it at most.  That
+//     much is lost or added by each row alike where many share a small weight, in
+//     the part of a job that holds the large one: 2^-7 of its value in all for
+//     half a million rows.  Smaller steps of m would hold more, 2^-28 where it
+//     moves at 2^4 and 2^-30 at 2^2, but the sums are rescaled at each (128 heads
+//     168 us, then 176 and 185).  (e4m3 would hold 2^-18 at best.)
 // l sums the weights unrounded, without 2^v_j, which is divided out exactly (from
 // floats, which end at 2^-126 where the largest weight has 2^9 or more).
 //

@@ -890,10 +890,13 @@ int dhs_attend_packed_bytes(dhs_pool *pool, const dhs_attend_packed_step *st, si
  * outputs are accumulated in float.  The products take queries and weights in
  * 8-bit pieces whose sum they are: a query's coded part exactly, but for less
  * than 2^-18 of its largest element; a weight (times its row's value scale) to
- * 2^-8 of itself, or 2^-11 if the type is DHS_F16, down to 2^-26 of the largest
- * of its query.  (Value scales of one query's rows may lie 2^100 apart; beyond
- * that a row of a small one may be lost from the sum of weights.)  A query's
- * coded part that holds an infinity or NaN gives NaN.
+ * 2^-11 of itself plus 2^-26 of the largest of its query.  What a row is off by
+ * the second way adds up where many rows share a small weight: to 2^-7 of the
+ * largest weighted value for half a million equal ones beside it; weights under
+ * 2^-26 of the largest may be lost from the sums of values, not from the sum of
+ * weights.  (Value scales of one query's rows may lie 2^100 apart; beyond that a
+ * row of a small one may be lost from the sum of weights too.)  A query's coded
+ * part that holds an infinity or NaN gives NaN.
  * The pool's row_bytes must be dhs_packed_bytes.  Order, bits and errors as
  * dhs_attend's.
  */
