@@ -48,9 +48,12 @@ __device__ __forceinline__ uint32_t narrow2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight 16-bit elements at `p`, 16-byte aligned or not.
+// Eight 16-bit elements at `p`, 16-byte aligned or not.  CONST: of memory that the
+// kernel does not write, which the read-only path is for.
+template <bool CONST>
 __device__ __forceinline__ uint4 raw8(const uint8_t* p, bool aligned) {
-  if (aligned) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (CONST && aligned) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (aligned) return *reinterpret_cast<const uint4*>(p);
   const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
   return make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16,
                     s[4] | (uint32_t)s[5] << 16, s[6] | (uint32_t)s[7] << 16);
@@ -215,8 +218,8 @@ __global__ void __launch_bounds__(kThreads)
     h = th - t * P.heads;
     g = k - th * (int)G.groups.d;
     const uint8_t* x = x0 + t * P.x_ts + h * P.x_hs + 2 * element();
-    a = raw8(x, aligned_x);
-    if (!r.interleaved && g < turning) b = raw8(x + 2 * half, aligned_x);
+    a = raw8<false>(x, aligned_x);  // y may be the same memory
+    if (!r.interleaved && g < turning) b = raw8<false>(x + 2 * half, aligned_x);
   };
   if ((int)threadIdx.x < all) ask(threadIdx.x);
   for (int k = threadIdx.x; k < n * half; k += kThreads) {
@@ -350,8 +353,9 @@ __global__ void __launch_bounds__(kThreads)
   auto ask = [&] {
     each([&](int z, int q, int e) {
       const uint8_t* p = x + 2 * (e - el0);
-      a[z][q] = raw8(p, aligned);
-      if (!r.interleaved && in_range(e)) b[z][q] = raw8(p + (e - from < half ? 2 * half : -2 * half), aligned);
+      a[z][q] = raw8<true>(p, aligned);
+      if (!r.interleaved && in_range(e))
+        b[z][q] = raw8<true>(p + (e - from < half ? 2 * half : -2 * half), aligned);
     });
     x += kWarps * ts;
   };

@@ -29,3 +29,17 @@ def test_a_warp_meets_before_one_lane_arrives(name):
         arrivals += 1
         assert lines[i - 1] == "__syncwarp();", "%s: %s" % (name, body)
     assert arrivals >= 2
+
+
+def test_a_rotation_reads_as_what_it_may_write():
+    """x and y of a rotation may be one tensor: x is not read through the read-only
+    path, which is for memory that the kernel does not write."""
+    with open(os.path.join(CSRC, "packed_rows.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    kernel = text[text.index("rotate_kernel(const"):text.index("struct PackParams")]
+    reads = re.findall(r"\b(\w+(?:<\w+>)?)\(x\b", kernel)
+    assert reads and set(reads) == {"raw8<false>"}
+    assert set(re.findall(r"__ldg\(([\w.]+)", kernel)) == {"r.turns", "P.position"}
+    body = text[text.index("uint4 raw8("):]
+    body = body[:body.index("\n}")]
+    assert re.search(r"if \(CONST[^\n]*__ldg", body) and body.count("__ldg") == 1
