@@ -11,8 +11,11 @@ Importing this module fails loudly when libdhs.so has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import mmap
 import os
+import struct
+import sys
 
 import numpy as np
 
@@ -129,6 +132,7 @@ class dhs_packed_rows(ctypes.Structure):
 
 
 class dhs_pack_item(ctypes.Structure):
+    __slots__ = ("given",)
     _fields_ = [("req", _i32), ("src", _i32), ("count", _i32), ("reserved", _i32),
                 ("key_dev", _vp), ("wide_dev", _vp), ("value_dev", _vp), ("position_dev", _vp),
                 ("rows_dev", _vp)]
@@ -144,6 +148,7 @@ class dhs_pack_step(ctypes.Structure):
 
 
 class dhs_unpack_item(ctypes.Structure):
+    __slots__ = ("given",)
     _fields_ = [("req", _i32), ("src", _i32), ("count", _i32), ("flags", _u32), ("first", _i64),
                 ("loc_dev", _vp), ("rows_dev", _vp), ("key_dev", _vp), ("value_dev", _vp)]
 
@@ -331,9 +336,12 @@ def make_step(step: int, items) -> tuple:
 
 
 def _address(t):
-    if t is None:
-        return None
-    return t.data_ptr() if hasattr(t, "data_ptr") else t
+    if t is None or type(t) is int:
+        return t
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        return t
 
 
 def attend_item(*, queries, q, out, req=0, src=0, topk=0, flags=0, loc=None, index=None,
@@ -399,11 +407,85 @@ def rope_table(rotary, *, base=10000.0, scaling="plain", factor=1.0, original=0.
     return out
 
 
-def _torch_dtype(t):
-    name = {"torch.bfloat16": "bf16", "torch.float16": "f16"}.get(str(t.dtype))
-    if name is None:
-        raise ValueError(f"a bfloat16 or float16 tensor is needed, not {t.dtype}")
-    return name
+@functools.lru_cache(maxsize=None)
+def _type_name(dtype):
+    return str(dtype).rpartition(".")[2]
+
+
+_WIDE = {"bfloat16": "bf16", "float16": "f16"}
+_TORCH_TYPES = {}
+_TURNS = ("int64", "uint64")
+
+
+def _torch_type(code):
+    """torch's type of a layout's (there are no tensors to check without torch)."""
+    if not _TORCH_TYPES and "torch" in sys.modules:
+        torch = sys.modules["torch"]
+        _TORCH_TYPES.update({DHS_BF16: torch.bfloat16, DHS_F16: torch.float16})
+    return _TORCH_TYPES.get(code)
+
+
+class _Parts:
+    """Checks of the tensors that a call reads or writes (None and addresses pass):
+    where they lie, their types, and that they hold what the call takes of them."""
+
+    def __init__(self, layout=None):
+        self.device = None  # that of the tensors so far
+        if layout is not None:
+            self.layout, self.kv, self.row_bytes = layout, layout.kv_heads, None
+            self.dtype = _torch_type(layout.dtype)
+
+    def reach(self, t, what):
+        """Whether t is a tensor; ValueError where the GPU cannot reach it, or not the others'."""
+        if t is None or not hasattr(t, "data_ptr"):
+            return False
+        if t.get_device() != self.device:
+            self.place(t, what)
+        return True
+
+    def place(self, t, what):
+        device = t.get_device()
+        if device < 0:
+            if not t.is_pinned():
+                raise ValueError(f"{what}: a tensor on the GPU is needed")
+        elif self.device is None:
+            self.device = device
+        else:
+            raise ValueError(f"{what}: tensors on one GPU are needed")
+
+    def entries(self, t, what, types, n):
+        """A list of n entries."""
+        if self.reach(t, what) and (_type_name(t.dtype) not in types or t.numel() < n or
+                                    not t.is_contiguous()):
+            raise ValueError(f"{what}: {n} contiguous entries of {types[0]} are needed")
+
+    def heads(self, t, what, count, elems, strides):
+        """`count` rows' heads of `elems` elements of the layout's type; strides
+        None: contiguous ones."""
+        if not self.reach(t, what):
+            return
+        if t.dtype is not self.dtype:
+            raise ValueError(f"{what}: {t.dtype} is not the layout's type")
+        if strides is None:
+            if t.numel() < count * self.kv * elems or not t.is_contiguous():
+                raise ValueError(f"{what}: contiguous [{count}][{self.kv}][{elems}] or strides are needed")
+        elif count > 0:
+            ends = [(n - 1) * s for n, s in zip((count, self.kv), strides)]
+            first, size = t.storage_offset(), t.untyped_storage().nbytes() // t.element_size()
+            if first + sum(min(0, e) for e in ends) < 0 or \
+                    first + sum(max(0, e) for e in ends) + elems > size:
+                raise ValueError(f"{what}: [{count}][{self.kv}][{elems}] by these strides leaves the tensor")
+
+    def packed(self, t, count):
+        """`count` packed rows (of a layout that is refused: the call says so)."""
+        if t is None or not self.reach(t, "rows"):
+            return
+        if self.row_bytes is None:
+            n = _i32(0)
+            lib.dhs_packed_bytes(ctypes.byref(self.layout), ctypes.byref(n))
+            self.row_bytes = n.value
+        if t.numel() * t.element_size() < count * self.row_bytes or not t.is_contiguous():
+            raise ValueError(f"rows: {count} contiguous rows of {self.row_bytes} bytes are needed")
 
 
 def make_rotate(x, positions, turns, *, out=None, offset=0, rotary=None, pairs="half",
@@ -417,13 +499,15 @@ def make_rotate(x, positions, turns, *, out=None, offset=0, rotary=None, pairs="
     if x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
         raise ValueError("the elements of a head must be contiguous")
     rotary = x.shape[2] - offset if rotary is None else rotary
-    if str(positions.dtype) != "torch.int32" or positions.numel() < x.shape[0] or \
-            not positions.is_contiguous():
-        raise ValueError("positions: contiguous int32, one a token")
-    if turns.element_size() != 8 or turns.numel() < rotary // 2 or not turns.is_contiguous():
-        raise ValueError("turns: contiguous 64-bit, one a pair")
+    if _type_name(x.dtype) not in _WIDE:
+        raise ValueError(f"a bfloat16 or float16 tensor is needed, not {x.dtype}")
+    parts = _Parts()
+    parts.reach(x, "x")
+    parts.reach(out, "out")
+    parts.entries(positions, "positions", ("int32",), x.shape[0])
+    parts.entries(turns, "turns", _TURNS, rotary // 2)
     st = dhs_rotate_step()
-    st.dtype = _DTYPES[_torch_dtype(x)]
+    st.dtype = _DTYPES[_WIDE[_type_name(x.dtype)]]
     st.tokens, st.heads, st.head_elems = x.shape
     st.rotary_offset, st.rotary_elems, st.pairs = offset, rotary, _PAIRS[pairs]
     st.flags, st.amplitude = DHS_ROPE_INVERSE if inverse else 0, amplitude
@@ -453,34 +537,65 @@ def dhs_packed_bytes(rows: dhs_packed_rows) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=64)
+def _array_type(kind, n):
+    return kind * n
+
+
 def _array(kind, items):
     """The items as a C array; by their bytes, which is several times faster
     than an argument each."""
     if not items:
         return (kind * 1)()
-    if any(type(it) is not kind for it in items):
+    if set(map(type, items)) != {kind}:
         raise TypeError(f"{kind.__name__}s are needed")
-    return (kind * len(items)).from_buffer_copy(b"".join(items))
+    return _array_type(kind, len(items)).from_buffer_copy(b"".join(items))
+
+
+# The items' fields: several times faster than a ctypes argument each.
+_pack_pack_item, _pack_unpack_item = struct.Struct("=4i5Q").pack, struct.Struct("=3iIq4Q").pack
+_new_pack_item, _new_unpack_item = dhs_pack_item.from_buffer_copy, dhs_unpack_item.from_buffer_copy
 
 
 def pack_item(count, key, *, wide=None, value=None, positions=None, rows=None, req=0,
               src=0) -> dhs_pack_item:
-    """A dhs_pack_item from torch tensors (or device addresses)."""
-    return dhs_pack_item(req, src, count, 0, _address(key), _address(wide), _address(value),
-                         _address(positions), _address(rows))
+    """A dhs_pack_item from torch tensors (or device addresses): key, wide and
+    value of the layout's type, positions int32 [count], rows for dhs_pack the
+    memory that packed rows go to."""
+    it = _new_pack_item(_pack_pack_item(
+        req, src, count, 0, 0 if key is None else _address(key), 0 if wide is None else _address(wide),
+        0 if value is None else _address(value), 0 if positions is None else _address(positions),
+        0 if rows is None else _address(rows)))
+    it.given = count, key, wide, value, positions, rows  # for make_pack's checks
+    return it
 
 
 def make_pack(items, rows, *, rotary_offset=0, rotary_elems=0, pairs="half", amplitude=1.0,
               turns=None, key_strides=None, wide_strides=None, value_strides=None) -> tuple:
     """A dhs_pack_step plus the item array that must stay alive with it.
     Strides are (between tokens, between heads) in elements; the default is
-    contiguous [count][kv_heads][elems]."""
+    contiguous [count][kv_heads][elems].  ValueError for tensors of another type
+    or with fewer elements, or that the GPU cannot reach."""
     arr = _array(dhs_pack_item, items)
+    parts, n = _Parts(rows), rows.key_elems - rows.wide_elems
+    for it in items:
+        count, key, wide, value, positions, packed = getattr(it, "given", (0,) + 5 * (None,))
+        if key is not None:
+            parts.heads(key, "key", count, n, key_strides)
+        if wide is not None and rows.wide_elems:
+            parts.heads(wide, "wide", count, rows.wide_elems, wide_strides)
+        if value is not None and not rows.shared:
+            parts.heads(value, "value", count, rows.value_elems, value_strides)
+        if rotary_elems:
+            parts.entries(positions, "positions", ("int32",), count)
+        if packed is not None:
+            parts.packed(packed, count)
+    if rotary_elems:
+        parts.entries(turns, "turns", _TURNS, rotary_elems // 2)
     st = dhs_pack_step()
     st.rows, st.n_items, st.items = rows, len(items), arr
     st.rotary_offset, st.rotary_elems = rotary_offset, rotary_elems
     st.pairs, st.amplitude, st.turns_dev = _PAIRS[pairs], amplitude, _address(turns)
-    n = rows.key_elems - rows.wide_elems
     flat = lambda m: (rows.kv_heads * m, m)  # noqa: E731
     st.key_token_stride, st.key_head_stride = key_strides or flat(n)
     st.wide_token_stride, st.wide_head_stride = wide_strides or flat(rows.wide_elems)
@@ -498,21 +613,43 @@ def dhs_append_packed(h, st: dhs_pack_step):
 
 def unpack_item(count, key, *, value=None, loc=None, rows=None, req=0, src=0, first=0,
                 flags=0) -> dhs_unpack_item:
-    """A dhs_unpack_item from torch tensors (or device addresses)."""
-    return dhs_unpack_item(req, src, count, flags, first, _address(loc), _address(rows),
-                           _address(key), _address(value))
+    """A dhs_unpack_item from torch tensors (or device addresses): key and value,
+    of the layout's type, are written; loc is int32 [count], rows the memory that
+    packed rows lie in."""
+    it = _new_unpack_item(_pack_unpack_item(
+        req, src, count, flags, first, 0 if loc is None else _address(loc),
+        0 if rows is None else _address(rows), 0 if key is None else _address(key),
+        0 if value is None else _address(value)))
+    it.given = count, key, value, loc, rows  # for make_unpack's checks
+    return it
 
 
 def make_unpack(items, rows, *, key_strides=None, value_strides=None) -> tuple:
     """A dhs_unpack_step plus the item array that must stay alive with it.
     Strides are (between rows, between heads) in elements; the default is
-    contiguous [count][kv_heads][elems]."""
+    contiguous [count][kv_heads][elems].  ValueError for tensors of another type
+    or with fewer elements, or that the GPU cannot reach."""
     arr = _array(dhs_unpack_item, items)
+    parts, n, m, kv = _Parts(rows), rows.key_elems, rows.value_elems, rows.kv_heads
+    device, dtype, flat = None, parts.dtype, key_strides is None
+    for it in items:
+        count, key, value, loc, packed = getattr(it, "given", (0,) + 4 * (None,))
+        # a decode step's items differ in little: what heads() asks, without the call
+        if key is not None and not (flat and device is not None and type(key) is kind and
+                                    key.get_device() == device and key.dtype is dtype and
+                                    key.numel() >= count * kv * n and key.is_contiguous()):
+            parts.heads(key, "key", count, n, key_strides)
+            device, kind = parts.device, type(key)
+        if value is not None:
+            parts.heads(value, "value", count, m, value_strides)
+        if packed is not None and not it.flags & DHS_UNPACK_HISTORY:
+            parts.packed(packed, count)
+        elif loc is not None and not it.flags & DHS_UNPACK_HISTORY:
+            parts.entries(loc, "loc", ("int32", "uint32"), count)
     st = dhs_unpack_step()
     st.rows, st.n_items, st.items = rows, len(items), arr
-    flat = lambda m: (rows.kv_heads * m, m)  # noqa: E731
-    st.key_row_stride, st.key_head_stride = key_strides or flat(rows.key_elems)
-    st.value_row_stride, st.value_head_stride = value_strides or flat(rows.value_elems)
+    st.key_row_stride, st.key_head_stride = key_strides or (kv * n, n)
+    st.value_row_stride, st.value_head_stride = value_strides or (kv * m, m)
     return st, arr
 
 
@@ -785,10 +922,10 @@ class Pool:
         return dhs_pack(self.h, st)
 
     def append_packed(self, st):
-        return dhs_append_packed(self.h, st)
+        return lib.dhs_append_packed(self.h, ctypes.byref(st))
 
     def unpack(self, st):
-        return dhs_unpack(self.h, st)
+        return lib.dhs_unpack(self.h, ctypes.byref(st))
 
     def unpack_on(self, st, stream):
         return dhs_unpack_on(self.h, st, stream)
