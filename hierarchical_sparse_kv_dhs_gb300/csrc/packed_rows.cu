@@ -639,7 +639,7 @@ cudaError_t launch_rotate(const RotateParams& p, int sms, cudaStream_t stream) {
   if (p.tokens <= 0 || p.heads <= 0) return cudaSuccess;
   const int groups = p.elems / 8;
   const int each = tokens_of_block(p.tokens, p.r.rotary, p.heads * groups, 4 * kThreads, sms);
-  const int blocks = (p.tokens + each - 1) / each;
+  const int blocks = (int)(((int64_t)p.tokens + each - 1) / each);
   const int turning = (p.r.interleaved ? p.r.rotary : p.r.rotary / 2) / 8;
   const int rest = p.x == p.y ? 0 : (p.elems - p.r.rotary) / 8;  // in place: nothing is copied
   const RotateGrid g{div_by(turning + rest), div_by(p.heads), div_by(p.r.rotary / 2), each};
