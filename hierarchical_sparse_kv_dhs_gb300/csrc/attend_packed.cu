@@ -63,6 +63,7 @@
 #include <cstddef>
 
 #include "attend_core.cuh"
+#include "dhs.h"
 
 namespace dhs {
 namespace {
@@ -1176,6 +1177,17 @@ bool plan_fits(const PackedPlan& p) {
   return p.slots >= (p.shared ? 2 * p.per_tile : std::max(p.per_tile - values, values));
 }
 
+// Sixteen columns are taken whether they fit so or not (shared rows of more than 512
+// coded elements and wide ones do not).  All that a plan needs is a tile of shared
+// rows, or the scores' part and the values of others, in the ring at once: six slots
+// at most, of five chunks of keys and one of wide elements.  Any layout has those:
+template <bool F16>
+constexpr uint32_t kFewestSlots =
+    (kSmemLimit - 1024 - kControlBytes - (5 * Pieces<16, F16>::kQ + 1) * 16 * 128 -
+     Pieces<16, F16>::kWeights) / kChunk;
+static_assert(kFewestSlots<false> >= 6 && kFewestSlots<true> >= 6, "a tile does not fit");
+static_assert((DHS_ATTEND_MAX_KEY + 127) / 128 == 5 && 2 * DHS_PACKED_MAX_WIDE <= 128, "slots of a tile");
+
 PackedPlan make_plan(const AttendCommon& c, const PackedLayout& l, int n) {
   switch (n) {
     case 16: return l.f16 ? plan_n<16, true>(c, l) : plan_n<16, false>(c, l);
@@ -1185,7 +1197,7 @@ PackedPlan make_plan(const AttendCommon& c, const PackedLayout& l, int n) {
   }
 }
 
-// The widest block of columns whose queries leave room for a tile.
+// The widest block of columns whose queries leave the slots that it wants, or 16.
 int widest_block(const AttendCommon& c, const PackedLayout& l) {
   int n = 64;
   while (n > 16 && !plan_fits(make_plan(c, l, n))) n -= 16;
