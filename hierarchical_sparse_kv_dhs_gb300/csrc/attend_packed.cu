@@ -72,6 +72,9 @@ constexpr int kChunk = kTile * 128;  // bytes of a ring slot: 128 bytes of each 
 constexpr int kMaxSlots = 12;
 constexpr float kSlack = 6.f;        // log2 units that a weight may pass the reference by
 constexpr float kLift = 9.f;         // log2 of a weight at the reference
+// log2 of what a row's key scale is held below itself by, and a query's above: a sum of
+// products of codes and pieces, 576 * 448 * 448 < 2^27, times 2^120 stays finite then.
+constexpr int kAside = 19;
 constexpr int kLoadThreads = 128, kRowThreads = 32;
 constexpr int kTmemColumns = 512;
 
@@ -260,7 +263,9 @@ __device__ __noinline__ void split_queries(const Params<MAXI>& P, uint8_t* sm, C
     int e = (int)(bits >> 23) - 126 - ((bits & 0x7FFFFFu) <= 0x600000u ? 9 : 8);
     e = most == 0.f ? 0 : min(max(e, -110), 120);
     const float down = finite ? __int_as_float((127 - e) << 23) : NAN;
-    if (piece == 0) qk[col] = __int_as_float((127 + e) << 23) * (c.scale * 1.44269504088896341f);
+    if (piece == 0)
+      qk[col] = c.scale * 1.44269504088896341f * __int_as_float((127 + (e >> 1)) << 23) *
+                __int_as_float((127 + e - (e >> 1) + kAside) << 23);  // neither half out of range
 #pragma unroll 1
     for (int ch = 0; ch < pl.key_chunks; ++ch) {
       uint8_t* const at = to + ch * (S::kQ * N * 128);
@@ -619,7 +624,7 @@ __device__ bool finite_codes(const uint8_t* p, int n) {
 
 // What a thread knows of its row of the tile: its scales.
 struct RowScale {
-  float key;      // 2^k, 0 without a row
+  float key;      // 2^(k - kAside), 0 without a row
   float value;    // v
   float inverse;  // 2^-v, 0 without a row
 };
@@ -807,7 +812,7 @@ __device__ void softmax_rows(const Params<MAXI>& P, uint8_t* sm, Control& ctl, i
         const uint8_t* const row = ctl.row[rr.slot][r];
         const float ks = ctl.scale[rr.slot][0][r];
         const uint32_t vbits = __float_as_uint(ctl.scale[rr.slot][1][r]) >> 23 & 255;
-        const RowScale z{ks, (float)((int)vbits - 127),
+        const RowScale z{ks * __int_as_float((127 - kAside) << 23), (float)((int)vbits - 127),
                          row ? __uint_as_float(max(1u, min(253u, 254u - vbits)) << 23) : 0.f};
         float x[C];  // scores and value scale in log2 units
 #pragma unroll
