@@ -261,7 +261,8 @@ __device__ __noinline__ void split_queries(const Params<MAXI>& P, uint8_t* sm, C
                            : __uint_as_float(top << 16);
     const uint32_t bits = __float_as_uint(most);
     int e = (int)(bits >> 23) - 126 - ((bits & 0x7FFFFFu) <= 0x600000u ? 9 : 8);
-    e = most == 0.f ? 0 : min(max(e, -110), 120);
+    // (-126: of smaller queries, which are bf16's last bits, 2^126 makes whole codes)
+    e = most == 0.f ? 0 : min(max(e, -126), 120);
     const float down = finite ? __int_as_float((127 - e) << 23) : NAN;
     if (piece == 0)
       qk[col] = c.scale * 1.44269504088896341f * __int_as_float((127 + (e >> 1)) << 23) *

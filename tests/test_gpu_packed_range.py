@@ -36,3 +36,10 @@ def sized(dhs, name, keys, queries):  # noqa: F811
 def test_key_sizes(dhs, name, keys):  # noqa: F811
     """Key scales up to 2^116 and down to 2^-64."""
     sized(dhs, name, keys, -100 if keys > 0 else 40)
+
+
+@pytest.mark.parametrize("queries", [-90, -105, -112, -118, -125])
+@pytest.mark.parametrize("name", ["no_wide", "grouped", "same"])
+def test_query_sizes(dhs, name, queries):  # noqa: F811
+    """Queries down to bf16's subnormal ones, whose bits count as any others'."""
+    sized(dhs, name, 30, queries)
