@@ -1656,9 +1656,11 @@ int dhs::check_attend_items(dhs_pool* p, const dhs_attend_item* items, int32_t n
       if (it.req < 0 || it.req >= c.max_requests || it.src < 0 || it.src >= c.sources)
         return DHS_EINVAL;
       if (!p->ps[(int64_t)it.req * c.sources + it.src].admitted) return DHS_ESTATE;
+      if (it.queries > 0 && (uintptr_t)it.range_dev & 3) return DHS_EINVAL;
     } else {
       const int64_t entries = (int64_t)it.queries * it.topk;
       if (entries > INT32_MAX || (entries > 0 && !it.loc_dev)) return DHS_EINVAL;
+      if (entries > 0 && ((uintptr_t)it.loc_dev | (uintptr_t)it.index_dev) & 3) return DHS_EINVAL;
     }
   }
   return DHS_OK;
