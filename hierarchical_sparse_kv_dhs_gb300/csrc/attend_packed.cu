@@ -508,9 +508,8 @@ __device__ void issue_scores(const Params<MAXI>& P, uint8_t* sm, Control& ctl) {
     for (int tile = v0; tile < v1; ++tile, ++n) {
       const uint32_t buf = two ? n & 1 : 0, use = two ? n >> 1 : n, d = tm_s + buf * pl.buf_columns;
       if (use > 0) warp_wait(smem_u32(&ctl.sread[buf]), (use - 1) & 1, until);
-      // Copies land in order: a slot that is full says that those before it are.
-      // Waiting at the second slot and at the last one costs less than at each.
-      // Every slot is 128 bytes wide, zeros past its slice.
+      // Each slot's products as soon as it has landed.  Every slot is 128 bytes wide,
+      // zeros past its slice.
 #pragma unroll 1
       for (int i = 0; i < parts; ++i) {
         warp_wait(smem_u32(&ctl.full[ring.slot]), ring.phase, until);

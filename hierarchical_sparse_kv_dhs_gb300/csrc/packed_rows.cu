@@ -5,7 +5,7 @@
 // turn, so that position * turns mod 2^64 is the angle, exactly, at any
 // position: one integer product.  Its top 32 bits are reduced to an eighth of a
 // turn around the nearest quarter before they become a float, which leaves the
-// angle 2^-26 off at most.  A block makes the sines of its tokens once, in
+// angle 2^-28 + 2^-32 turns off at most, under 2^-25 radians.  A block makes the sines of its tokens once, in
 // shared memory, for all their heads.
 //
 // Packing.  A group of lanes has a head (16 elements a lane): its largest
@@ -13,7 +13,7 @@
 // number's own exponent field, and the codes leave as 16-byte stores.  The
 // elements are read once and turned in registers (half pairs read the partner's
 // element too, which another lane of the group reads at the same time: an L1
-// hit).  Two roundings in all: to a code, and nothing else.
+// hit).  Sines and products aside, one rounding: to a code.
 //
 // Reading back.  Eight to 32 lanes have a row.
 #include <cuda_bf16.h>

@@ -400,7 +400,8 @@ def rope_table(rotary, *, base=10000.0, scaling="plain", factor=1.0, original=0.
                slow=1.0):
     """dhs_rope_table's turns as an int64 array (the bits of the uint64s), which
     torch.from_numpy takes: move it to the GPU once and hand it to make_rotate
-    and make_pack."""
+    and make_pack.  (scaling="parts" weights pairs by their turns; a ramp over the
+    pairs' numbers is a table of the caller's: see dhs_rope_config.)"""
     cfg = dhs_rope_config(rotary, _SCALINGS[scaling], base, factor, original, fast, slow)
     out = np.empty(max(1, rotary // 2), np.int64)
     check(lib.dhs_rope_table(ctypes.byref(cfg), out.ctypes.data), "dhs_rope_table")

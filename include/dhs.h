@@ -662,7 +662,10 @@ int64_t dhs_pool_capacity(const dhs_pool *pool);
 #define DHS_ROPE_PARTS 3  /* pairs that turn more than `fast` times over `original`
                            * positions as they are, those that turn less than `slow`
                            * times divided by factor, between them a mean of both,
-                           * weighted linearly by the turns */
+                           * weighted linearly by the turns.  Models trained with
+                           * weights linear in the pair's number instead need a
+                           * table of their own: of each pair's radians a position,
+                           * divided by 2 pi, times 2^64 */
 
 typedef struct {
   int32_t rotary_elems; /* elements of a head that turn: a multiple of 16 */
@@ -853,10 +856,11 @@ typedef struct {
 
 /* Read packed rows back into 16 bits: an attention in 16 bits of a prompt's
  * next chunk, or staging.  Codes times scales, rounded once (exact unless the
- * number leaves an f16's range); wide elements as they are.  The pool's
- * row_bytes must be dhs_packed_bytes unless every item names rows_dev.
- * Asynchronous, in order on the pool's stream.  Errors: DHS_EINVAL,
- * DHS_ESTATE, DHS_ENOMEM, DHS_ECUDA. */
+ * number leaves the type's range: infinity then, as for a bf16 of 2^128 (1 -
+ * 2^-5) or more, whose code stands for 2^128); wide elements as they are.
+ * The pool's row_bytes must be dhs_packed_bytes unless every item names
+ * rows_dev.  Asynchronous, in order on the pool's stream.  Errors:
+ * DHS_EINVAL, DHS_ESTATE, DHS_ENOMEM, DHS_ECUDA. */
 int dhs_unpack(dhs_pool *pool, const dhs_unpack_step *st);
 
 /* dhs_unpack on a caller's stream (not NULL), ordered as dhs_gather_on. */
